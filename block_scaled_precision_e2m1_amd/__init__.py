@@ -748,3 +748,10 @@ def fp8_blockwise_gemm(A, sA, B, sB, out=None, out_dtype=torch.bfloat16):
     st = lib.fp8_blockwise_gemm(M, N, K, _ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(D), dt, _stream(device))
     _raise_on("fp8_blockwise_gemm", st)
     return D
+
+
+# The feed-forward operators of include/fp4g_ffn.h live in a module of their own.
+from .ffn import *  # noqa: E402,F401,F403
+from .ffn import __all__ as _ffn_all  # noqa: E402
+
+__all__ += _ffn_all

@@ -1,0 +1,260 @@
+// C-ABI entry points of the feed-forward operators: validate on the host, pick a kernel,
+// launch on the caller's stream.  Validation runs before any HIP call, so an invalid call
+// returns its status without touching the device.
+#include "ffn_internal.h"
+
+#include <initializer_list>
+
+namespace {
+
+using fp4g::DenseArgs;
+using fp4g::DensePlan;
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxElems = (int64_t)1 << 50;
+// Row pitches below 2^22 bytes keep a tile of 256 rows inside a 31-bit buffer size.
+constexpr int64_t kMaxPitch = (int64_t)1 << 22;
+// int8 sums: K * 128 * 128 must stay below 2^31.
+constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 16;
+
+struct Buffer {
+  const void* p;
+  int64_t bytes;
+  uintptr_t align;
+};
+
+// Every buffer present and aligned, every output clear of the inputs and the other outputs.
+fp4g_status check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffer> outs) {
+  for (const auto* list : {&ins, &outs})
+    for (const Buffer& b : *list)
+      if (b.bytes > 0 && !b.p) return FP4G_EINVAL;
+  for (const auto* list : {&ins, &outs})
+    for (const Buffer& b : *list)
+      if (b.bytes > 0 && reinterpret_cast<uintptr_t>(b.p) % b.align != 0) return FP4G_EALIGN;
+  auto clash = [](const Buffer& a, const Buffer& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+  };
+  for (const Buffer* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buffer& i : ins)
+      if (clash(*o, i)) return FP4G_EINVAL;
+    for (const Buffer* q = outs.begin(); q != o; ++q)
+      if (clash(*o, *q)) return FP4G_EINVAL;
+  }
+  return FP4G_OK;
+}
+
+// Sizes of a product whose operand rows hold K elements of `elem` bytes.
+fp4g_status check_sizes(int64_t M, int64_t N, int64_t K, int elem) {
+  for (int64_t d : {M, N, K})
+    if (d < 0 || d >= kMaxDim) return FP4G_EINVAL;
+  for (int64_t d : {M, N})
+    if (K > 0 && d > kMaxElems / K) return FP4G_EINVAL;
+  if (N > 0 && M > kMaxElems / N) return FP4G_EINVAL;
+  if (K % (16 / elem) != 0 || K * elem > kMaxPitch) return FP4G_EUNSUPPORTED;
+  if (elem == 1 && K > kMaxInt8K) return FP4G_EUNSUPPORTED;
+  return FP4G_OK;
+}
+
+bool known_act(int act) { return act == FP4G_ACT_SILU || act == FP4G_ACT_GELU || act == FP4G_ACT_GELU_TANH; }
+bool known_out(int t) { return t == FP4G_OUT_F32 || t == FP4G_OUT_BF16; }
+
+fp4g_status finish(hipError_t e) { return e == hipSuccess ? FP4G_OK : FP4G_EHIP; }
+
+// The plan of L products with `gates` weights each, given room for its partial sums.
+DensePlan plan(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT, size_t room) {
+  const int64_t per = L * gates * M * N * 4;
+  const int64_t cap = per > 0 ? (int64_t)(room / (size_t)per) : 1;
+  return fp4g::dense_plan(M, gates * N, L, KT, cap > 1 ? cap : 1);
+}
+constexpr size_t kAnyRoom = ~(size_t)0 >> 1;
+size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT) {
+  const int S = plan(M, N, gates, L, KT, kAnyRoom).S;
+  return S > 1 ? (size_t)(L * S * gates * M * N * 4) : 0;
+}
+int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
+
+fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t* bytes) {
+  const fp4g_status st = check_sizes(M, N, K, elem);
+  if (st != FP4G_OK) return st;
+  if (!bytes) return FP4G_EINVAL;
+  *bytes = M == 0 || N == 0 || K == 0 ? 0 : partial_bytes(M, N, gates, 1, stages(K, elem));
+  return FP4G_OK;
+}
+
+// Rows of dG and dU: whole 128-byte K stages of dX.
+int64_t grad_pitch(int64_t N) { return (N + 63) / 64 * 64; }
+
+// Buffers of zero elements are not there.
+Buffer buf(const void* p, int64_t bytes, uintptr_t align = 16) { return Buffer{p, bytes, align}; }
+
+hipError_t zero(void* p, int64_t count, bool bf16, hipStream_t s) {
+  return count > 0 ? fp4g::launch_zero_fill(p, count, bf16, s) : hipSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp4g_status int8_quantize(int64_t rows, int64_t K, const void* X, int x_type, void* codes, float* scales,
+                          void* stream) {
+  const fp4g_status st = check_sizes(rows, 1, K, 1);
+  // The row length limits of the products' operands do not bind here.
+  if (st == FP4G_EINVAL) return st;
+  if (x_type != FP4G_IN_F32 && x_type != FP4G_IN_BF16) return FP4G_EINVAL;
+  if (K % 16 != 0) return FP4G_EUNSUPPORTED;
+  if (rows == 0) return FP4G_OK;
+  const bool bf16 = x_type == FP4G_IN_BF16;
+  const fp4g_status sb = check_buffers({buf(X, rows * K * (bf16 ? 2 : 4))},
+                                       {buf(codes, rows * K), buf(scales, rows * 4, 4)});
+  if (sb != FP4G_OK) return sb;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (K == 0) return finish(zero(scales, rows, false, s));
+  return finish(fp4g::launch_int8_quantize(rows, K, X, bf16, codes, scales, s));
+}
+
+fp4g_status w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return product_workspace(M, N, K, 1, 1, bytes);
+}
+
+fp4g_status w8a8_gemm(int64_t M, int64_t N, int64_t K, const void* A, const float* sa, const void* B, const float* sb,
+                      void* D, int d_type, void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_sizes(M, N, K, 1);
+  if (st != FP4G_OK) return st;
+  if (!known_out(d_type)) return FP4G_EINVAL;
+  if (M == 0 || N == 0) return FP4G_OK;
+  const bool bf16 = d_type == FP4G_OUT_BF16, some = K > 0;
+  st = check_buffers({buf(A, M * K), buf(sa, some ? M * 4 : 0, 4), buf(B, N * K), buf(sb, some ? N * 4 : 0, 4)},
+                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, (int64_t)workspace_bytes)});
+  if (st != FP4G_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (!some) return finish(zero(D, M * N, bf16, s));
+  const DensePlan p = plan(M, N, 1, 1, stages(K, 1), workspace_bytes);
+  DenseArgs a;
+  a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S;
+  a.A[0] = static_cast<const uint8_t*>(A), a.B[0] = static_cast<const uint8_t*>(B);
+  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sb, a.D[0] = D, a.P = workspace;
+  return finish(fp4g::launch_w8a8(a, p.tile, bf16, s));
+}
+
+fp4g_status w8a8_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return product_workspace(M, N, K, 1, 2, bytes);
+}
+
+fp4g_status w8a8_gated_gemm(int64_t M, int64_t N, int64_t K, const void* A, const float* sa, const void* Bg,
+                            const float* sg, const void* Bu, const float* su, int act, void* D, int d_type,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_sizes(M, N, K, 1);
+  if (st != FP4G_OK) return st;
+  if (!known_out(d_type) || !known_act(act)) return FP4G_EINVAL;
+  if (M == 0 || N == 0) return FP4G_OK;
+  const bool bf16 = d_type == FP4G_OUT_BF16, some = K > 0;
+  st = check_buffers({buf(A, M * K), buf(sa, some ? M * 4 : 0, 4), buf(Bg, N * K), buf(sg, some ? N * 4 : 0, 4),
+                      buf(Bu, N * K), buf(su, some ? N * 4 : 0, 4)},
+                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, (int64_t)workspace_bytes)});
+  if (st != FP4G_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (!some) return finish(zero(D, M * N, bf16, s));
+  const DensePlan p = plan(M, N, 2, 1, stages(K, 1), workspace_bytes);
+  DenseArgs a;
+  a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S, a.act = act;
+  a.A[0] = static_cast<const uint8_t*>(A);
+  a.B[0] = static_cast<const uint8_t*>(Bg), a.B[1] = static_cast<const uint8_t*>(Bu);
+  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sg, a.sb[1] = su, a.D[0] = D, a.P = workspace;
+  return finish(fp4g::launch_w8a8_gated(a, p.tile, bf16, s));
+}
+
+fp4g_status gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return product_workspace(M, N, K, 2, 2, bytes);
+}
+
+fp4g_status gated_gemm(int64_t M, int64_t N, int64_t K, const void* X, const void* Wg, const void* Wu, int act, void* H,
+                       float* G, float* U, void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_sizes(M, N, K, 2);
+  if (st != FP4G_OK) return st;
+  if (!known_act(act) || !G != !U) return FP4G_EINVAL;
+  if (M == 0 || N == 0) return FP4G_OK;
+  const int64_t kept = G ? M * N * 4 : 0;
+  st = check_buffers({buf(X, M * K * 2), buf(Wg, N * K * 2), buf(Wu, N * K * 2)},
+                     {buf(H, M * N * 2), buf(G, kept), buf(U, kept), buf(workspace, (int64_t)workspace_bytes)});
+  if (st != FP4G_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (K == 0) {
+    hipError_t e = zero(H, M * N, true, s);
+    if (e == hipSuccess && G) e = zero(G, M * N, false, s);
+    if (e == hipSuccess && G) e = zero(U, M * N, false, s);
+    return finish(e);
+  }
+  const DensePlan p = plan(M, N, 2, 1, stages(K, 2), workspace_bytes);
+  DenseArgs a;
+  a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S, a.act = act;
+  a.A[0] = static_cast<const uint8_t*>(X);
+  a.B[0] = static_cast<const uint8_t*>(Wg), a.B[1] = static_cast<const uint8_t*>(Wu);
+  a.lda = a.ldb = K * 2, a.D[0] = H, a.G = G, a.U = U, a.P = workspace;
+  return finish(fp4g::launch_gated(a, p.tile, s));
+}
+
+fp4g_status gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes, size_t* least) {
+  const fp4g_status st = check_sizes(M, N, K, 2);
+  if (st != FP4G_OK) return st;
+  if (!bytes || !least) return FP4G_EINVAL;
+  const int64_t pitch = grad_pitch(N);
+  if (pitch * 2 > kMaxPitch) return FP4G_EUNSUPPORTED;
+  *bytes = *least = 0;
+  if (M == 0 || N == 0 || K == 0) return FP4G_OK;
+  *least = (size_t)(4 * M * pitch);
+  const size_t x = partial_bytes(M, K, 1, 1, 2 * stages(N, 2)), w = partial_bytes(N, K, 1, 2, stages(M, 2));
+  *bytes = *least + (x > w ? x : w);
+  return FP4G_OK;
+}
+
+fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH, const void* X, const void* Wg,
+                                const void* Wu, const float* G, const float* U, int act, void* dX, void* dWg,
+                                void* dWu, void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_sizes(M, N, K, 2);
+  if (st != FP4G_OK) return st;
+  if (!known_act(act)) return FP4G_EINVAL;
+  const int64_t pitch = grad_pitch(N);
+  if (pitch * 2 > kMaxPitch) return FP4G_EUNSUPPORTED;
+  if (K == 0 || (M == 0 && N == 0)) return FP4G_OK;
+  const bool some = M > 0 && N > 0;
+  st = check_buffers({buf(dH, M * N * 2), buf(X, some ? M * K * 2 : 0), buf(Wg, some ? N * K * 2 : 0),
+                      buf(Wu, some ? N * K * 2 : 0), buf(G, M * N * 4), buf(U, M * N * 4)},
+                     {buf(dX, M * K * 2), buf(dWg, N * K * 2), buf(dWu, N * K * 2),
+                      buf(workspace, some ? (int64_t)workspace_bytes : 0)});
+  if (st != FP4G_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (!some) {
+    hipError_t e = zero(dX, M * K, true, s);
+    if (e == hipSuccess) e = zero(dWg, N * K, true, s);
+    if (e == hipSuccess) e = zero(dWu, N * K, true, s);
+    return finish(e);
+  }
+  const size_t least = (size_t)(4 * M * pitch);
+  if (workspace_bytes < least) return FP4G_EINVAL;
+  uint8_t* dG = static_cast<uint8_t*>(workspace);
+  uint8_t* dU = dG + 2 * M * pitch;
+  void* P = dG + least;
+  const size_t room = workspace_bytes - least;
+  hipError_t e = fp4g::launch_gate_grad(M, N, pitch, dH, G, U, act, dG, dU, s);
+  if (e != hipSuccess) return FP4G_EHIP;
+  {
+    const DensePlan p = plan(M, K, 1, 1, 2 * stages(N, 2), room);
+    DenseArgs a;
+    a.M = (int)M, a.N = (int)K, a.K = (int)N, a.S = p.S;
+    a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;
+    a.B[0] = static_cast<const uint8_t*>(Wg), a.B[1] = static_cast<const uint8_t*>(Wu), a.ldb = K * 2;
+    a.D[0] = dX, a.P = P;
+    e = fp4g::launch_grad_input(a, p.tile, s);
+    if (e != hipSuccess) return FP4G_EHIP;
+  }
+  const DensePlan p = plan(N, K, 1, 2, stages(M, 2), room);
+  DenseArgs a;
+  a.M = (int)N, a.N = (int)K, a.K = (int)M, a.L = 2, a.S = p.S;
+  a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;
+  a.B[0] = static_cast<const uint8_t*>(X), a.ldb = K * 2;
+  a.D[0] = dWg, a.D[1] = dWu, a.P = P;
+  return finish(fp4g::launch_grad_weights(a, p.tile, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,140 @@
+// Pieces shared by the unscaled-operand kernels (int8 and bf16 products, gated feed-forward
+// products and their gradients).
+//
+// Operand tiles reach LDS by buffer_load_dwordx4 ... lds through a raw buffer resource
+// whose size ends at the last valid byte of the tile: a lane past it (rows past M, K past
+// the end of a row, stages past the end of a slice) moves nothing from memory and writes
+// zeros to LDS, so ragged sizes need no masks in the product and no copy can leave its
+// operand.  A lane that must not load (the K tail of a row whose next bytes belong to the
+// next row) is given the offset kNoLoad, past the end of every resource.
+#pragma once
+
+#include "common.hpp"
+#include "ffn_internal.h"
+
+namespace fp4g {
+
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kNoLoad = 0x80000000u;   // resources hold less than 2^31 bytes
+
+// The element types of the operands.
+struct I8 { static constexpr int BYTES = 1; typedef v16i acc32; typedef v4i acc16; };
+struct BF { static constexpr int BYTES = 2; typedef v16f acc32; typedef v4f acc16; };
+
+// A raw buffer of `bytes` bytes at p (clamped to be non-negative); p and bytes must be
+// wave-uniform.  LDS copies of 16 bytes per lane from it: lane i of the wave fetches
+// p + off and writes 16 bytes at l + 16 * i.
+#if defined(__HIP_DEVICE_COMPILE__)
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes > 0 ? bytes : 0, 0x00020000);
+}
+__device__ __forceinline__ void lds_buffer16(rsrc_t r, lds_void* l, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, off, 0, 0, 0);
+}
+// As lds_buffer16, with the nontemporal policy, for data read once.
+__device__ __forceinline__ void lds_buffer16_nt(rsrc_t r, lds_void* l, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, off, 0, 0, 2);
+}
+__device__ __forceinline__ v2i lds_read_tr16(const uint8_t* p) {
+  return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                     (__attribute__((address_space(3))) v4s*)p));
+}
+#else
+struct rsrc_t {};
+__device__ __forceinline__ rsrc_t make_rsrc(const void*, int) { return {}; }
+__device__ __forceinline__ void lds_buffer16(rsrc_t, lds_void*, uint32_t) {}
+__device__ __forceinline__ void lds_buffer16_nt(rsrc_t, lds_void*, uint32_t) {}
+__device__ __forceinline__ v2i lds_read_tr16(const uint8_t*) { return {}; }
+#endif
+
+// 32x32 products of 16 bytes of K per lane (32 int8 or 16 bf16 K elements per instruction),
+// and 16x16 products of 16 bytes per lane (64 or 32 K elements).  Lane l holds row l % R of
+// its operand in K slot l / R; equal slots of the two operands meet.
+__device__ __forceinline__ v16i mfma32(v4i a, v4i b, v16i c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+__device__ __forceinline__ v16f mfma32(v4i a, v4i b, v16f c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+__device__ __forceinline__ v4i mfma16(v4i a, v4i b, v4i c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+#else
+  return c;
+#endif
+}
+
+// The activations of a gated block, in fp32.  With s(z) = 1 / (1 + e^-z):
+//   silu       x s(x)
+//   gelu       x (1 + erf(x / sqrt 2)) / 2
+//   gelu_tanh  x s(2 sqrt(2/pi) (x + 0.044715 x^3)), which is x (1 + tanh(..)) / 2
+// e^-z is one hardware 2^x of the fp32 product z log2(e) and the quotient one hardware
+// reciprocal: a few fp32 steps of relative error for |z| < 100, and past that s is 0 or 1
+// to more than fp32 precision.  The cubic is evaluated at |x| <= 32, where s has long been
+// 0 or 1: a larger x would overflow it and make 0 * inf of the derivative.
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+__device__ __forceinline__ float cubic_arg(float x, float* slope) {
+  constexpr float c = 1.5957691216057308f, q = 0.044715f;       // 2 sqrt(2/pi)
+  const float t = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f), t2 = t * t;
+  *slope = c * (1.0f + 3.0f * q * t2);
+  return c * t * (1.0f + q * t2);
+}
+__device__ __forceinline__ float act_of(int act, float x) {
+  if (act == FP4G_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+  float z = x, slope;
+  if (act == FP4G_ACT_GELU_TANH) z = cubic_arg(x, &slope);
+  return x * sigmoid(z);
+}
+// act(x) and its derivative.
+__device__ __forceinline__ void act_grad(int act, float x, float* a, float* da) {
+  if (act == FP4G_ACT_GELU) {
+    const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
+    const float t = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f);
+    *a = x * cdf;
+    *da = cdf + t * __expf(-0.5f * t * t) * 0.3989422804014327f;
+    return;
+  }
+  float z = x, slope = 1.0f;
+  if (act == FP4G_ACT_GELU_TANH) z = cubic_arg(x, &slope);
+  const float s = sigmoid(z);
+  *a = x * s;
+  *da = s + x * s * (1.0f - s) * slope;
+}
+
+// The elementwise end of a product: element (m, n) from its sums g (and u when GATED).
+template <class T, bool GATED>
+struct Finish {
+  typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
+  const DenseArgs& a;
+  __device__ __forceinline__ float row(int m) const {
+    if constexpr (std::is_same<T, I8>::value) return a.sa[m];
+    return 1.0f;
+  }
+  // The sums as values: int8 sums are whole (exact in int32) and rounded once here to fp32,
+  // then scaled by the row's and the column's scale.
+  __device__ __forceinline__ float value(sum_t v, float sm, int n, int which) const {
+    if constexpr (std::is_same<T, I8>::value) return (float)v * sm * a.sb[which][n];
+    return v;
+  }
+};
+
+}  // namespace fp4g

@@ -1,0 +1,80 @@
+// The elementwise step of the gated block's backward pass for gfx950: from dH (bf16) and the
+// kept fp32 products G and U,
+//   dG = dH * U * act'(G),   dU = dH * act(G),
+// rounded once to bf16, the operands of the gradients' products.  Rows are `pitch` elements
+// apart (a multiple of 64) with zeros past N, so the products' K stages of dX are whole and
+// every operand row is 16-byte aligned whatever N is.
+//
+// HBM-bound: 14 bytes an element (2 + 4 + 4 read, 2 + 2 written).  A lane takes 8 columns of
+// a row: one 16-byte load of dH, two each of G and U, two 16-byte stores.
+#include <algorithm>
+
+#include "dense.hpp"
+
+namespace fp4g {
+namespace {
+
+// VEC: N % 8 == 0, so that every group of 8 is whole and its loads are aligned.
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+gate_grad_kernel(int64_t M, int N, int pitch, const uint16_t* __restrict__ dH, const float* __restrict__ G,
+                 const float* __restrict__ U, int act, uint8_t* __restrict__ dG, uint8_t* __restrict__ dU) {
+  const int groups = pitch / 8;
+  const int64_t total = M * groups;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += (int64_t)gridDim.x * 256) {
+    const int64_t m = x / groups;
+    const int n = (int)(x - m * groups) * 8;
+    const int64_t at = m * N + n;
+    float h[8], g[8], u[8];
+    if constexpr (VEC) {
+      if (n < N) {
+        const v4i w = *reinterpret_cast<const v4i*>(dH + at);
+        const v4f g0 = *reinterpret_cast<const v4f*>(G + at), g1 = *reinterpret_cast<const v4f*>(G + at + 4);
+        const v4f u0 = *reinterpret_cast<const v4f*>(U + at), u1 = *reinterpret_cast<const v4f*>(U + at + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[e] = __builtin_bit_cast(float, e & 1 ? (uint32_t)w[e / 2] & 0xffff0000u : (uint32_t)w[e / 2] << 16);
+          g[e] = e < 4 ? g0[e & 3] : g1[e & 3];
+          u[e] = e < 4 ? u0[e & 3] : u1[e & 3];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = g[e] = u[e] = 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool in = n + e < N;
+        h[e] = in ? __builtin_bit_cast(float, (uint32_t)dH[at + e] << 16) : 0.0f;
+        g[e] = in ? G[at + e] : 0.0f;
+        u[e] = in ? U[at + e] : 0.0f;
+      }
+    }
+    uint32_t wg[4], wu[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      float a0, d0, a1, d1;
+      act_grad(act, g[e], &a0, &d0);
+      act_grad(act, g[e + 1], &a1, &d1);
+      wg[e / 2] = pack_bf16x2(h[e] * u[e] * d0, h[e + 1] * u[e + 1] * d1);
+      wu[e / 2] = pack_bf16x2(h[e] * a0, h[e + 1] * a1);
+    }
+    const int64_t to = (m * pitch + n) * 2;
+    *reinterpret_cast<v4i*>(dG + to) = v4i{(int)wg[0], (int)wg[1], (int)wg[2], (int)wg[3]};
+    *reinterpret_cast<v4i*>(dU + to) = v4i{(int)wu[0], (int)wu[1], (int)wu[2], (int)wu[3]};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_gate_grad(int64_t M, int64_t N, int64_t pitch, const void* dH, const float* G, const float* U, int act,
+                            void* dG, void* dU, hipStream_t s) {
+  const int64_t units = ceil_div(M * (pitch / 8), 256);
+  const unsigned grid = (unsigned)std::min<int64_t>(units, device_cus() * 16);
+  auto* kernel = N % 8 == 0 ? gate_grad_kernel<true> : gate_grad_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, M, (int)N, (int)pitch, static_cast<const uint16_t*>(dH), G, U,
+                     act, static_cast<uint8_t*>(dG), static_cast<uint8_t*>(dU));
+  return hipGetLastError();
+}
+
+}  // namespace fp4g
