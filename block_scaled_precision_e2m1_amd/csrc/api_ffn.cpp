@@ -63,14 +63,14 @@ fp4g_status finish(hipError_t e) { return e == hipSuccess ? FP4G_OK : FP4G_EHIP;
 
 // The plan of L products with `gates` weights each, given room for its partial sums.
 DensePlan plan(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT, size_t room) {
-  const int64_t per = L * gates * M * N * 4;
+  const int64_t per = L * gates * M * fp4g::partial_pitch(N) * 4;
   const int64_t cap = per > 0 ? (int64_t)(room / (size_t)per) : 1;
   return fp4g::dense_plan(M, gates * N, L, KT, cap > 1 ? cap : 1);
 }
 constexpr size_t kAnyRoom = ~(size_t)0 >> 1;
 size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT) {
   const int S = plan(M, N, gates, L, KT, kAnyRoom).S;
-  return S > 1 ? (size_t)(L * S * gates * M * N * 4) : 0;
+  return S > 1 ? (size_t)(L * S * gates * M * fp4g::partial_pitch(N) * 4) : 0;
 }
 int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
 

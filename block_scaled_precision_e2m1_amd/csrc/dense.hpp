@@ -125,21 +125,53 @@ __device__ __forceinline__ void act_grad(int act, float x, float* a, float* da) 
   *da = s + x * s * (1.0f - s) * slope;
 }
 
-// The elementwise end of a product: element (m, n) from its sums g (and u when GATED).
-template <class T, bool GATED>
-struct Finish {
-  typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
-  const DenseArgs& a;
-  __device__ __forceinline__ float row(int m) const {
-    if constexpr (std::is_same<T, I8>::value) return a.sa[m];
-    return 1.0f;
+// y = act(y) * u; the activation is uniform, so one of the three loops runs.
+template <int V>
+__device__ __forceinline__ void gate(int act, float (&y)[V], const float (&u)[V]) {
+  if (act == FP4G_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = act_of(FP4G_ACT_SILU, y[e]) * u[e];
+  } else if (act == FP4G_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = act_of(FP4G_ACT_GELU, y[e]) * u[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = act_of(FP4G_ACT_GELU_TANH, y[e]) * u[e];
   }
-  // The sums as values: int8 sums are whole (exact in int32) and rounded once here to fp32,
-  // then scaled by the row's and the column's scale.
-  __device__ __forceinline__ float value(sum_t v, float sm, int n, int which) const {
-    if constexpr (std::is_same<T, I8>::value) return (float)v * sm * a.sb[which][n];
-    return v;
+}
+
+// V results to D[at ..], of which the first `left` exist.  A whole group is one vector store
+// at any alignment: rows of an odd length start anywhere, and the hardware splits only the
+// stores that cross a line.
+template <bool BF16, int V>
+__device__ __forceinline__ void store_cols(void* D, int64_t at, int left, const float (&y)[V]) {
+  static_assert(V == 4 || (V == 8 && BF16), "16 bytes at most");
+  typedef v4i v4i_any __attribute__((aligned(2)));
+  typedef v2i v2i_any __attribute__((aligned(2)));
+  typedef v4f v4f_any __attribute__((aligned(4)));
+  if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(D) + at;
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int e = 0; e < V; e += 2) w[e / 2] = pack_bf16x2(y[e], y[e + 1]);
+    if (left >= V) {
+      if constexpr (V == 8) *reinterpret_cast<v4i_any*>(p) = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      else *reinterpret_cast<v2i_any*>(p) = v2i{(int)w[0], (int)w[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < left) p[e] = (uint16_t)(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
+    }
+  } else {
+    float* p = static_cast<float*>(D) + at;
+    if (left >= V) {
+      *reinterpret_cast<v4f_any*>(p) = v4f{y[0], y[1], y[2], y[3]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < left) p[e] = y[e];
+    }
   }
-};
+}
 
 }  // namespace fp4g

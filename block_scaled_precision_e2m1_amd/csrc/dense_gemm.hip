@@ -32,10 +32,10 @@
 //     wave's own registers' worth of sums and g and u never travel.
 //   * The end goes through the wave's share of the (then idle) ring in strips of 32 rows:
 //     sums are written as the instruction leaves them (a lane owns 4 consecutive columns)
-//     and read back along rows, so results leave as 16 bytes a lane, whole lines a row.
-//     The scales and the activation are applied on that way back, in a rolled loop: with
-//     three activations in line for each of a wave's sums the code would not fit the
-//     instruction cache.
+//     and read back along rows, so results leave as 16 bytes a lane, whole lines a row,
+//     whatever the row's alignment (the hardware takes unaligned vector stores).  The
+//     activation is applied on that way back, in a rolled loop: with three activations in
+//     line for each of a wave's sums the code would not fit the instruction cache.
 //   * Work items are numbered so that the tiles one XCD runs at once share A and B panels in
 //     its L2.  With too few tiles to fill the chip, K is cut into S slices, whose sums are
 //     added in slice order by a second kernel (no atomics: results repeat bit for bit).
@@ -266,7 +266,6 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
     for (int q = 0; q < LH; ++q) issue_one(C::STAGES - 1, q);
   };
 
-  const Finish<T, C::GATED> fin{a};
   // Persistent: at most one workgroup per CU (times its occupancy) walks the items.
   for (int work = blockIdx.x; work < total; work += gridDim.x) {
     setup(work);
@@ -298,19 +297,32 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
         for (int r = q; r < FR; r += NQ) read_frag(ks + 1, 0, 0, r);
       });
     }
+    // ---- the end ----
+    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
+    // A lane writes row r32 of every strip and reads column group `col` of it: the scales of
+    // both are fetched here once, under the wait for the ring.
+    constexpr int ELEM = SPLIT || !BF16 || SAVE ? 4 : 2, V = 16 / ELEM, LPR = C::WOUT / V;
+    static_assert(64 % LPR == 0, "a lane keeps its columns");
+    constexpr bool SCALED = !SPLIT && std::is_same<T, I8>::value;
+    typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
+    const int col = lane % LPR * V, n = nw + col;
+    float sm[FI], sc[C::GATED ? 2 : 1][V];
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int i = 0; i < FI; ++i) sm[i] = a.sa[min(mw + i * 32 + r32, a.M - 1)];
+#pragma unroll
+      for (int w = 0; w < (C::GATED ? 2 : 1); ++w)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sc[w][e] = a.sb[w][min(n + e, a.N - 1)];
+    }
     // No copy may still be landing when the ring is reused, and no wave may still read it.
     wait_vmcnt<0>();
     barrier_lds();
-
-    // ---- the end ----
     uint8_t* strip = smem + wave * (32 * C::STRIP);
-    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
-    const int64_t MN = (int64_t)a.M * a.N;
-    constexpr int ELEM = SPLIT || !BF16 ? 4 : 2, VEC = 16 / ELEM;
-    const bool wide = a.N % VEC == 0;
 #pragma unroll
     for (int i = 0; i < FI; ++i) {
       // In: lane (hi, r32) holds row r32, columns j*32 + 8*g + 4*hi + 0..3 of block row i.
+      // The row's scale goes into the 16 bytes past its sums.
 #pragma unroll
       for (int j = 0; j < FJ; ++j)
 #pragma unroll
@@ -320,51 +332,49 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
           *reinterpret_cast<e4*>(strip + r32 * C::STRIP + (j * 32 + 8 * g + 4 * hi) * 4) =
               e4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
         }
+      if constexpr (SCALED) *reinterpret_cast<float*>(strip + r32 * C::STRIP + C::WN * 4) = sm[i];
       // Out: V columns a lane, along rows.
-      auto rows_out = [&](auto v_c) {
-        constexpr int V = decltype(v_c)::value, LPR = C::WOUT / V;
-        for (int x = lane; x < 32 * LPR; x += 64) {
-          const int row = x / LPR, col = x % LPR * V;
-          const int m = mw + i * 32 + row, n = nw + col;
-          if (m >= a.M || n >= a.N) continue;
-          typedef typename Finish<T, C::GATED>::sum_t sum_t;
-          const sum_t* s = reinterpret_cast<const sum_t*>(strip + row * C::STRIP) + col;
-          const int64_t at = (int64_t)m * a.N + n;
-          if constexpr (SPLIT) {
+      const int rows = min(a.M - (mw + i * 32), 32);
+#pragma unroll 1
+      for (int row = lane / LPR; row < rows; row += 64 / LPR) {
+        const sum_t* g = reinterpret_cast<const sum_t*>(strip + row * C::STRIP) + col;
+        const int64_t m = mw + i * 32 + row;
+        if constexpr (SPLIT) {
+          const int64_t pitch = partial_pitch(a.N);
+          if (n < pitch) {
 #pragma unroll
             for (int w = 0; w < (C::GATED ? 2 : 1); ++w) {
-              sum_t* p = reinterpret_cast<sum_t*>(a.P) +
-                         (((int64_t)it.l * a.S + it.s) * (C::GATED ? 2 : 1) + w) * MN + at;
-              if constexpr (V == 4) *reinterpret_cast<v4i*>(p) = *reinterpret_cast<const v4i*>(s + w * C::WOUT);
-              else *p = s[w * C::WOUT];
-            }
-          } else {
-            const float sm = fin.row(m);
-            float y[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              y[e] = fin.value(s[e], sm, n + e, 0);
-              if constexpr (C::GATED) {
-                const float u = fin.value(s[C::WOUT + e], sm, n + e, 1);
-                if constexpr (SAVE) {
-                  a.G[at + e] = y[e];
-                  a.U[at + e] = u;
-                }
-                y[e] = act_of(a.act, y[e]) * u;
-              }
-            }
-            void* D = a.D[it.l];
-            if constexpr (V == 1) {
-              store_out<BF16>(D, at, y[0]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < V; e += 4) store_out4<BF16>(D, at + e, 4, y[e], y[e + 1], y[e + 2], y[e + 3]);
+              const int64_t plane = ((int64_t)it.l * a.S + it.s) * (C::GATED ? 2 : 1) + w;
+              *reinterpret_cast<v4i*>(static_cast<int*>(a.P) + (plane * a.M + m) * pitch + n) =
+                  *reinterpret_cast<const v4i*>(g + w * C::WOUT);
             }
           }
+        } else if (n < a.N) {
+          // int8 sums are exact in 32 bits and are rounded to fp32 here.
+          float y[V], u[V], rs = 1.0f;
+          if constexpr (SCALED) rs = *reinterpret_cast<const float*>(strip + row * C::STRIP + C::WN * 4);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            y[e] = (float)g[e];
+            if constexpr (SCALED) y[e] = y[e] * rs * sc[0][e];
+          }
+          const int64_t at = m * a.N + n;
+          const int left = a.N - n;
+          if constexpr (C::GATED) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              u[e] = (float)g[C::WOUT + e];
+              if constexpr (SCALED) u[e] = u[e] * rs * sc[1][e];
+            }
+            if constexpr (SAVE) {
+              store_cols<false>(a.G, at, left, y);
+              store_cols<false>(a.U, at, left, u);
+            }
+            gate(a.act, y, u);
+          }
+          store_cols<BF16>(a.D[it.l], at, left, y);
         }
-      };
-      if (wide) rows_out(std::integral_constant<int, VEC>{});
-      else rows_out(std::integral_constant<int, 1>{});
+      }
     }
     // No wave may start the next item's copies while another still reads its strips.
     barrier_lds();
@@ -373,61 +383,51 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
 
 // The end of a split product: sums of the S slices in slice order, then what the unsplit
 // kernel does with its sums.  HBM-bound: S (times 2 when gated) 32-bit values in, one out.
-template <class T, bool GATED, bool BF16, bool SAVE, int V>
+// Rows of partial sums are padded to whole groups of 4, one group a lane.
+template <class T, bool GATED, bool BF16, bool SAVE>
 __global__ void __launch_bounds__(256) dense_reduce_kernel(const DenseArgs a) {
-  typedef typename Finish<T, GATED>::sum_t sum_t;
-  typedef sum_t sumv __attribute__((ext_vector_type(V == 1 ? 2 : V)));
-  const Finish<T, GATED> fin{a};
-  const int64_t MN = (int64_t)a.M * a.N, per = MN / V;
+  typedef typename std::conditional<std::is_same<T, I8>::value, v4i, v4f>::type sum4;
   constexpr int W = GATED ? 2 : 1;
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < per * a.L; x += (int64_t)gridDim.x * 256) {
-    const int l = (int)(x / per);
-    const int64_t at = (x - l * per) * V;
-    const sum_t* p = reinterpret_cast<const sum_t*>(a.P) + (int64_t)l * a.S * W * MN + at;
-    sum_t s[W][V];
+  const uint32_t groups = (uint32_t)(partial_pitch(a.N) / 4), per = (uint32_t)a.M * groups;
+  for (uint32_t x = blockIdx.x * 256 + threadIdx.x; x < per * a.L; x += gridDim.x * 256) {
+    const uint32_t l = x / per, in = x - l * per, m = in / groups, n = (in - m * groups) * 4;
+    const sum4* p = static_cast<const sum4*>(a.P) + (int64_t)l * a.S * W * per + in;
+    sum4 s[W];
 #pragma unroll
-    for (int w = 0; w < W; ++w)
+    for (int w = 0; w < W; ++w) s[w] = p[(int64_t)w * per];
+#pragma unroll 4
+    for (int k = 1; k < a.S; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[w][e] = 0;
-    for (int k = 0; k < a.S; ++k)
+      for (int w = 0; w < W; ++w) s[w] += p[((int64_t)k * W + w) * per];
+    float y[4], u[4];
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const sum_t* q = p + ((int64_t)k * W + w) * MN;
-        if constexpr (V == 1) {
-          s[w][0] += *q;
-        } else {
-          const sumv t = *reinterpret_cast<const sumv*>(q);
-#pragma unroll
-          for (int e = 0; e < V; ++e) s[w][e] += t[e];
-        }
-      }
-    const int m = (int)(at / a.N), n = (int)(at - (int64_t)m * a.N);
-    const float sm = fin.row(m);
-    float y[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      y[e] = fin.value(s[0][e], sm, n + e, 0);
-      if constexpr (GATED) {
-        const float u = fin.value(s[W - 1][e], sm, n + e, 1);
-        if constexpr (SAVE) {
-          a.G[at + e] = y[e];
-          a.U[at + e] = u;
-        }
-        y[e] = act_of(a.act, y[e]) * u;
+    for (int e = 0; e < 4; ++e) {
+      y[e] = (float)s[0][e];
+      u[e] = (float)s[W - 1][e];
+      if constexpr (std::is_same<T, I8>::value) {
+        const int c = min((int)n + e, a.N - 1);
+        y[e] = y[e] * a.sa[m] * a.sb[0][c];
+        if constexpr (GATED) u[e] = u[e] * a.sa[m] * a.sb[1][c];
       }
     }
-    if constexpr (V == 1) store_out<BF16>(a.D[l], at, y[0]);
-    else store_out4<BF16>(a.D[l], at, 4, y[0], y[1], y[2], y[3]);
+    const int64_t at = (int64_t)m * a.N + n;
+    const int left = a.N - (int)n;
+    if constexpr (GATED) {
+      if constexpr (SAVE) {
+        store_cols<false>(a.G, at, left, y);
+        store_cols<false>(a.U, at, left, u);
+      }
+      gate(a.act, y, u);
+    }
+    store_cols<BF16>(a.D[l], at, left, y);
   }
 }
 
 template <class T, bool GATED, bool BF16, bool SAVE>
 hipError_t launch_reduce(const DenseArgs& a, hipStream_t s) {
-  const bool wide = a.N % 4 == 0;
-  const int64_t units = ceil_div((int64_t)a.M * a.N / (wide ? 4 : 1) * a.L, 256);
+  const int64_t units = ceil_div(a.L * a.M * (partial_pitch(a.N) / 4), 256);
   const unsigned grid = (unsigned)std::min<int64_t>(units, device_cus() * 8);
-  if (wide) hipLaunchKernelGGL((dense_reduce_kernel<T, GATED, BF16, SAVE, 4>), dim3(grid), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((dense_reduce_kernel<T, GATED, BF16, SAVE, 1>), dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((dense_reduce_kernel<T, GATED, BF16, SAVE>), dim3(grid), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -468,7 +468,7 @@ DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t 
   for (const auto& c : tiles) {
     const int64_t items = L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
     for (int64_t S = 1; S <= std::min<int64_t>({cap, KT, kMaxSplits}); ++S) {
-      if (S > 1 && KT / S < 4) break;
+      if (S > 1 && (KT / S < 4 || L * rows * (cols + 8) >= (int64_t)1 << 31)) break;   // 32-bit sums' indexes
       const int64_t slots = cus * c.per_cu;
       double t = (double)ceil_div(items * S, slots) * (ceil_div(KT, S) * c.stage_us + 2.0);
       if (S > 1) t += 3.0 + (double)(L * rows * cols) * 4.0 * (S + 1) / 4.0e6;

@@ -22,9 +22,16 @@ struct DenseArgs {
   void* D[2] = {nullptr, nullptr};
   float* G = nullptr;                         // gated: both products, where they are kept
   float* U = nullptr;
-  void* P = nullptr;                          // [L][S][gates][M][N] 32-bit partial sums
+  void* P = nullptr;                          // [L][S][gates][M][partial_pitch(N)] 32-bit partial sums
   int act = 0;
 };
+
+// Rows of partial sums are whole groups of 4.
+inline
+#if defined(__HIPCC__)
+__host__ __device__
+#endif
+int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
 enum DenseTile { kTile256, kTile128, kTile64 };
 struct DensePlan { DenseTile tile; int S; };

@@ -6,7 +6,9 @@
 // every operand row is 16-byte aligned whatever N is.
 //
 // HBM-bound: 14 bytes an element (2 + 4 + 4 read, 2 + 2 written).  A lane takes 8 columns of
-// a row: one 16-byte load of dH, two each of G and U, two 16-byte stores.
+// a row: one 16-byte load of dH, two each of G and U, two 16-byte stores.  The loads take
+// rows of any length, whose groups start at any element (the hardware takes unaligned vector
+// loads); only the group that holds a row's end is read element by element.
 #include <algorithm>
 
 #include "dense.hpp"
@@ -14,11 +16,11 @@
 namespace fp4g {
 namespace {
 
-// VEC: N % 8 == 0, so that every group of 8 is whole and its loads are aligned.
-template <bool VEC>
 __global__ void __launch_bounds__(256)
 gate_grad_kernel(int64_t M, int N, int pitch, const uint16_t* __restrict__ dH, const float* __restrict__ G,
                  const float* __restrict__ U, int act, uint8_t* __restrict__ dG, uint8_t* __restrict__ dU) {
+  typedef v4i v4i_any __attribute__((aligned(2)));
+  typedef v4f v4f_any __attribute__((aligned(4)));
   const int groups = pitch / 8;
   const int64_t total = M * groups;
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += (int64_t)gridDim.x * 256) {
@@ -26,20 +28,15 @@ gate_grad_kernel(int64_t M, int N, int pitch, const uint16_t* __restrict__ dH, c
     const int n = (int)(x - m * groups) * 8;
     const int64_t at = m * N + n;
     float h[8], g[8], u[8];
-    if constexpr (VEC) {
-      if (n < N) {
-        const v4i w = *reinterpret_cast<const v4i*>(dH + at);
-        const v4f g0 = *reinterpret_cast<const v4f*>(G + at), g1 = *reinterpret_cast<const v4f*>(G + at + 4);
-        const v4f u0 = *reinterpret_cast<const v4f*>(U + at), u1 = *reinterpret_cast<const v4f*>(U + at + 4);
+    if (n + 8 <= N) {
+      const v4i w = *reinterpret_cast<const v4i_any*>(dH + at);
+      const v4f g0 = *reinterpret_cast<const v4f_any*>(G + at), g1 = *reinterpret_cast<const v4f_any*>(G + at + 4);
+      const v4f u0 = *reinterpret_cast<const v4f_any*>(U + at), u1 = *reinterpret_cast<const v4f_any*>(U + at + 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          h[e] = __builtin_bit_cast(float, e & 1 ? (uint32_t)w[e / 2] & 0xffff0000u : (uint32_t)w[e / 2] << 16);
-          g[e] = e < 4 ? g0[e & 3] : g1[e & 3];
-          u[e] = e < 4 ? u0[e & 3] : u1[e & 3];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = g[e] = u[e] = 0.0f;
+      for (int e = 0; e < 8; ++e) {
+        h[e] = __builtin_bit_cast(float, e & 1 ? (uint32_t)w[e / 2] & 0xffff0000u : (uint32_t)w[e / 2] << 16);
+        g[e] = e < 4 ? g0[e & 3] : g1[e & 3];
+        u[e] = e < 4 ? u0[e & 3] : u1[e & 3];
       }
     } else {
 #pragma unroll
@@ -71,8 +68,7 @@ hipError_t launch_gate_grad(int64_t M, int64_t N, int64_t pitch, const void* dH,
                             void* dG, void* dU, hipStream_t s) {
   const int64_t units = ceil_div(M * (pitch / 8), 256);
   const unsigned grid = (unsigned)std::min<int64_t>(units, device_cus() * 16);
-  auto* kernel = N % 8 == 0 ? gate_grad_kernel<true> : gate_grad_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, M, (int)N, (int)pitch, static_cast<const uint16_t*>(dH), G, U,
+  hipLaunchKernelGGL(gate_grad_kernel, dim3(grid), dim3(256), 0, s, M, (int)N, (int)pitch, static_cast<const uint16_t*>(dH), G, U,
                      act, static_cast<uint8_t*>(dG), static_cast<uint8_t*>(dU));
   return hipGetLastError();
 }
