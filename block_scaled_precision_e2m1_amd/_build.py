@@ -61,13 +61,44 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(compile_one, sources()))
     tmp = LIB + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname,libfp4gemm.so", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB)
     build_probe(cc)
     return LIB
+
+
+BINDING_SRC = os.path.join(HERE, "binding", "ffn_binding.cpp")
+BINDING = os.path.join(HERE, "_ffn_binding.so")
+
+
+def build_binding() -> str:
+    """The feed-forward operators' Python binding: host code against torch's headers, which
+    finds libfp4gemm.so next to itself.  Needs the library, so it is linked after it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler: the Python binding cannot be built")
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [BINDING_SRC, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    for path in cpp_extension.library_paths():
+        cmd += ["-L" + path]
+    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 PROBE_SRC = os.path.join(HERE, "probe", "peak_probe.hip")
@@ -88,3 +119,4 @@ def build_probe(cc=None) -> str:
 
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
+    print(build_binding())
