@@ -61,24 +61,38 @@ bool known_out(int t) { return t == FP4G_OUT_F32 || t == FP4G_OUT_BF16; }
 
 fp4g_status finish(hipError_t e) { return e == hipSuccess ? FP4G_OK : FP4G_EHIP; }
 
-// The plan of L products with `gates` weights each, given room for its partial sums.
-DensePlan plan(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT, size_t room) {
+// How many slices of partial sums of L products with `gates` weights each fit into `room` bytes.
+int64_t slices(int64_t M, int64_t N, int64_t gates, int64_t L, size_t room) {
   const int64_t per = L * gates * M * fp4g::partial_pitch(N) * 4;
   const int64_t cap = per > 0 ? (int64_t)(room / (size_t)per) : 1;
-  return fp4g::dense_plan(M, gates * N, L, KT, cap > 1 ? cap : 1);
+  return cap > 1 ? cap : 1;
 }
 constexpr size_t kAnyRoom = ~(size_t)0 >> 1;
-size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, int64_t KT) {
-  const int S = plan(M, N, gates, L, KT, kAnyRoom).S;
-  return S > 1 ? (size_t)(L * S * gates * M * fp4g::partial_pitch(N) * 4) : 0;
+size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, const DensePlan& p) {
+  return p.S > 1 ? (size_t)(L * p.S * gates * M * fp4g::partial_pitch(N) * 4) : 0;
 }
 int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
+
+// The plan of a scaled or gated product, given room for its partial sums.
+DensePlan product_plan(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t room) {
+  const int64_t cap = slices(M, N, gates, 1, room);
+  if (fp4g::gemv_takes(M, N, K * elem, gates))
+    return DensePlan{fp4g::kGemv, fp4g::gemv_splits(M, N, K * elem, gates, cap)};
+  return fp4g::dense_plan(M, gates * N, 1, stages(K, elem), cap);
+}
+// The plans of dX (one product over both gradients' K) and of dWg and dWu.
+DensePlan input_grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
+  return fp4g::dense_plan(M, K, 1, 2 * stages(N, 2), slices(M, K, 1, 1, room));
+}
+DensePlan weight_grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
+  return fp4g::dense_plan(N, K, 2, stages(M, 2), slices(N, K, 1, 2, room));
+}
 
 fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t* bytes) {
   const fp4g_status st = check_sizes(M, N, K, elem);
   if (st != FP4G_OK) return st;
   if (!bytes) return FP4G_EINVAL;
-  *bytes = M == 0 || N == 0 || K == 0 ? 0 : partial_bytes(M, N, gates, 1, stages(K, elem));
+  *bytes = M == 0 || N == 0 || K == 0 ? 0 : partial_bytes(M, N, gates, 1, product_plan(M, N, K, elem, gates, kAnyRoom));
   return FP4G_OK;
 }
 
@@ -129,12 +143,12 @@ fp4g_status w8a8_gemm(int64_t M, int64_t N, int64_t K, const void* A, const floa
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (!some) return finish(zero(D, M * N, bf16, s));
-  const DensePlan p = plan(M, N, 1, 1, stages(K, 1), workspace_bytes);
+  const DensePlan p = product_plan(M, N, K, 1, 1, workspace_bytes);
   DenseArgs a;
   a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S;
   a.A[0] = static_cast<const uint8_t*>(A), a.B[0] = static_cast<const uint8_t*>(B);
-  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sb, a.D[0] = D, a.P = workspace;
-  return finish(fp4g::launch_w8a8(a, p.tile, bf16, s));
+  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sb, a.D[0] = D, a.P = workspace, a.bf16_out = bf16;
+  return finish(fp4g::launch_w8a8(a, p.tile, s));
 }
 
 fp4g_status w8a8_gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -155,13 +169,13 @@ fp4g_status w8a8_gated_gemm(int64_t M, int64_t N, int64_t K, const void* A, cons
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (!some) return finish(zero(D, M * N, bf16, s));
-  const DensePlan p = plan(M, N, 2, 1, stages(K, 1), workspace_bytes);
+  const DensePlan p = product_plan(M, N, K, 1, 2, workspace_bytes);
   DenseArgs a;
   a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S, a.act = act;
   a.A[0] = static_cast<const uint8_t*>(A);
   a.B[0] = static_cast<const uint8_t*>(Bg), a.B[1] = static_cast<const uint8_t*>(Bu);
-  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sg, a.sb[1] = su, a.D[0] = D, a.P = workspace;
-  return finish(fp4g::launch_w8a8_gated(a, p.tile, bf16, s));
+  a.lda = a.ldb = K, a.sa = sa, a.sb[0] = sg, a.sb[1] = su, a.D[0] = D, a.P = workspace, a.bf16_out = bf16;
+  return finish(fp4g::launch_w8a8_gated(a, p.tile, s));
 }
 
 fp4g_status gated_gemm_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -185,7 +199,7 @@ fp4g_status gated_gemm(int64_t M, int64_t N, int64_t K, const void* X, const voi
     if (e == hipSuccess && G) e = zero(U, M * N, false, s);
     return finish(e);
   }
-  const DensePlan p = plan(M, N, 2, 1, stages(K, 2), workspace_bytes);
+  const DensePlan p = product_plan(M, N, K, 2, 2, workspace_bytes);
   DenseArgs a;
   a.M = (int)M, a.N = (int)N, a.K = (int)K, a.S = p.S, a.act = act;
   a.A[0] = static_cast<const uint8_t*>(X);
@@ -203,7 +217,8 @@ fp4g_status gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K, 
   *bytes = *least = 0;
   if (M == 0 || N == 0 || K == 0) return FP4G_OK;
   *least = (size_t)(4 * M * pitch);
-  const size_t x = partial_bytes(M, K, 1, 1, 2 * stages(N, 2)), w = partial_bytes(N, K, 1, 2, stages(M, 2));
+  const size_t x = partial_bytes(M, K, 1, 1, input_grad_plan(M, N, K, kAnyRoom));
+  const size_t w = partial_bytes(N, K, 1, 2, weight_grad_plan(M, N, K, kAnyRoom));
   *bytes = *least + (x > w ? x : w);
   return FP4G_OK;
 }
@@ -239,7 +254,7 @@ fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH,
   hipError_t e = fp4g::launch_gate_grad(M, N, pitch, dH, G, U, act, dG, dU, s);
   if (e != hipSuccess) return FP4G_EHIP;
   {
-    const DensePlan p = plan(M, K, 1, 1, 2 * stages(N, 2), room);
+    const DensePlan p = input_grad_plan(M, N, K, room);
     DenseArgs a;
     a.M = (int)M, a.N = (int)K, a.K = (int)N, a.S = p.S;
     a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;
@@ -248,7 +263,7 @@ fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH,
     e = fp4g::launch_grad_input(a, p.tile, s);
     if (e != hipSuccess) return FP4G_EHIP;
   }
-  const DensePlan p = plan(N, K, 1, 2, stages(M, 2), room);
+  const DensePlan p = weight_grad_plan(M, N, K, room);
   DenseArgs a;
   a.M = (int)N, a.N = (int)K, a.K = (int)M, a.L = 2, a.S = p.S;
   a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;

@@ -39,6 +39,10 @@ __device__ __forceinline__ void lds_buffer16(rsrc_t r, lds_void* l, uint32_t off
 __device__ __forceinline__ void lds_buffer16_nt(rsrc_t r, lds_void* l, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, off, 0, 0, 2);
 }
+// 16 bytes a lane into registers, zeros past the end.
+__device__ __forceinline__ v4i load_buffer16(rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
 // __restrict__ matters: the alias scope it leaves on the inlined read is what tells the compiler
 // that the read needs no wait of its own for the copies in flight.  Without one it puts
 // vmcnt(0) before every read of this kind, which drains the ring: the two products of the
@@ -53,6 +57,7 @@ struct rsrc_t {};
 __device__ __forceinline__ rsrc_t make_rsrc(const void*, int) { return {}; }
 __device__ __forceinline__ void lds_buffer16(rsrc_t, lds_void*, uint32_t) {}
 __device__ __forceinline__ void lds_buffer16_nt(rsrc_t, lds_void*, uint32_t) {}
+__device__ __forceinline__ v4i load_buffer16(rsrc_t, uint32_t) { return {}; }
 __device__ __forceinline__ v2i lds_read_tr16(const uint8_t*) { return {}; }
 #endif
 

@@ -481,17 +481,26 @@ DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t 
   return best;
 }
 
-hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, bool bf16, hipStream_t s) {
-  return bf16 ? launch_cfg<I8, kScaled, false, false, 1, true, false>(a, tile, s)
+hipError_t launch_partial_sums(const DenseArgs& a, bool int8, bool gated, hipStream_t s) {
+  if (!int8) return a.G ? launch_reduce<BF, true, true, true>(a, s) : launch_reduce<BF, true, true, false>(a, s);
+  if (gated) return a.bf16_out ? launch_reduce<I8, true, true, false>(a, s) : launch_reduce<I8, true, false, false>(a, s);
+  return a.bf16_out ? launch_reduce<I8, false, true, false>(a, s) : launch_reduce<I8, false, false, false>(a, s);
+}
+
+hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, hipStream_t s) {
+  if (tile == kGemv) return launch_gemv_w8a8(a, s);
+  return a.bf16_out ? launch_cfg<I8, kScaled, false, false, 1, true, false>(a, tile, s)
               : launch_cfg<I8, kScaled, false, false, 1, false, false>(a, tile, s);
 }
 
-hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, bool bf16, hipStream_t s) {
-  return bf16 ? launch_cfg<I8, kGated, false, false, 1, true, false>(a, tile, s)
+hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {
+  if (tile == kGemv) return launch_gemv_w8a8_gated(a, s);
+  return a.bf16_out ? launch_cfg<I8, kGated, false, false, 1, true, false>(a, tile, s)
               : launch_cfg<I8, kGated, false, false, 1, false, false>(a, tile, s);
 }
 
 hipError_t launch_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {
+  if (tile == kGemv) return launch_gemv_gated(a, s);
   return a.G ? launch_cfg<BF, kGated, false, false, 1, true, true>(a, tile, s)
              : launch_cfg<BF, kGated, false, false, 1, true, false>(a, tile, s);
 }

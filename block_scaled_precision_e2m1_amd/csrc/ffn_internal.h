@@ -24,6 +24,7 @@ struct DenseArgs {
   float* U = nullptr;
   void* P = nullptr;                          // [L][S][gates][M][partial_pitch(N)] 32-bit partial sums
   int act = 0;
+  bool bf16_out = true;                       // the type of D
 };
 
 // Rows of partial sums are whole groups of 4.
@@ -33,16 +34,26 @@ __host__ __device__
 #endif
 int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
-enum DenseTile { kTile256, kTile128, kTile64 };
+enum DenseTile { kTile256, kTile128, kTile64, kGemv };
 struct DensePlan { DenseTile tile; int S; };
 
 // Tile and K split for L products of rows x cols sums (gated: cols counts both weights'
 // columns) over KT stages of 128 bytes of K; at most `cap` slices.
 DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap);
 
-hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, bool bf16, hipStream_t s);
-hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, bool bf16, hipStream_t s);
+// Whether a product of M tokens with `gates` weights of N rows of KB bytes goes to the kernels
+// for few tokens (dense_gemv.hip), and its K split there, of at most `cap` slices.
+bool gemv_takes(int64_t M, int64_t N, int64_t KB, int64_t gates);
+int gemv_splits(int64_t M, int64_t N, int64_t KB, int64_t gates, int64_t cap);
+
+hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, hipStream_t s);
+hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, hipStream_t s);
 hipError_t launch_gated(const DenseArgs& a, DenseTile tile, hipStream_t s);
+hipError_t launch_gemv_w8a8(const DenseArgs& a, hipStream_t s);
+hipError_t launch_gemv_w8a8_gated(const DenseArgs& a, hipStream_t s);
+hipError_t launch_gemv_gated(const DenseArgs& a, hipStream_t s);
+// Adds the slices of a.P and finishes the product.
+hipError_t launch_partial_sums(const DenseArgs& a, bool int8, bool gated, hipStream_t s);
 hipError_t launch_grad_input(const DenseArgs& a, DenseTile tile, hipStream_t s);
 hipError_t launch_grad_weights(const DenseArgs& a, DenseTile tile, hipStream_t s);
 

@@ -155,6 +155,46 @@ def test_w8a8_gemm(m, n, k, out):
         within(d, want, bound + 1e-40, f"w8a8_gemm {m}x{n}x{k}")
 
 
+# Every token packing (up to 4, 8, 16, 32, 64) at weights that stream past the caches (32 MB
+# and more) and at few rows with K long enough for a split; the last group of rows is ragged.
+FEW = [(m, n, k) for m in (1, 3, 4, 5, 8, 9, 16, 18, 32, 33, 47, 64) for n, k in ((8201, 4112), (70, 16400))]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_few_tokens(m, n, k):
+    print(f"case few tokens {m}x{n}x{k}", flush=True)
+    a, sa, bg, sg, bu, su = int8_inputs(m, n, k, 21, 2)
+    g = (a.double() @ bg.double().t()) * sa.double()[:, None] * sg.double()
+    u = (a.double() @ bu.double().t()) * sa.double()[:, None] * su.double()
+    want = activation(g, "silu")[0] * u
+    bound = gated_bound(g, 3 * H32 * g.abs(), u, 3 * H32 * u.abs(), "silu", 0) + 1e-30
+    for space in (None, torch.empty(0, dtype=torch.uint8, device=DEV)):
+        one = fp4.w8a8_gemm(a, sa, bg, sg, out_dtype=torch.float32, workspace=space)
+        both = fp4.w8a8_gated_gemm(a, sa, bg, sg, bu, su, out_dtype=torch.float32, workspace=space)
+        torch.cuda.synchronize(DEV)
+        within(one, g, 3 * H32 * g.abs() * 1.01 + 1e-40, "w8a8_gemm")
+        within(both, want, bound, "w8a8_gated_gemm")
+
+
+@pytest.mark.parametrize("m", [1, 3, 4, 7, 8, 15, 30, 64])
+def test_few_tokens_keep_non_finite_values_apart(m):
+    """Packed tokens share an instruction: a spoiled one must reach neither its neighbours nor,
+    through rows past N and tokens past M, anything else."""
+    for n, k in ((70, 1032), (2051, 4104)):
+        print(f"case few tokens, non-finite {m}x{n}x{k}", flush=True)
+        x, wg, wu, _ = bf16_inputs(m, n, k, 22)
+        clean = fp4.gated_gemm(x, wg, wu)
+        bad = m // 2
+        x[bad, k - 1] = math.nan
+        wu[n - 1, 3] = math.inf
+        h, g, u = fp4.gated_gemm(x, wg, wu, save=True)
+        torch.cuda.synchronize(DEV)
+        rows = [i for i in range(m) if i != bad]
+        assert torch.isnan(h[bad]).all() and torch.isnan(g[bad]).all() and torch.isnan(u[bad]).all()
+        assert torch.equal(h[rows][:, :n - 1], clean[rows][:, :n - 1])
+        assert not torch.isfinite(u[rows][:, n - 1]).any()
+
+
 def test_w8a8_gemm_largest_sums():
     """Sums at the ends of 32 bits: K = 131056 of -128 * -128 and -128 * 127."""
     k = (1 << 17) - 16
