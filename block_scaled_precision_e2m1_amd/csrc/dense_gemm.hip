@@ -11,6 +11,10 @@
 //   * One workgroup of 4 waves (2 x 2) per BM x BN tile; a wave owns WM x WN.  At 256 x 256
 //     a wave's 128 x 128 sums fill 256 AGPRs and each fragment read from LDS feeds four
 //     matrix instructions, which halves the LDS traffic of a 64 x 64 wave tile.
+//   * Small products have a CU or so to a tile and few matrix instructions a stage, and are
+//     bound by the latency of one wave's instructions.  Their tiles get two groups of waves
+//     (KG = 2), each multiplying half of every stage's quarters into sums of its own, which
+//     the end adds: twice the waves to hide latency behind, at the same LDS reads a product.
 //   * A K stage is 128 bytes of every row of A and of B (a cache line; 128 int8 or 64 bf16
 //     elements).  Stages live in a ring of STAGES slots, filled by buffer copies straight
 //     to LDS whose resources end with the operand's tile (dense.hpp): every ragged edge
@@ -56,12 +60,17 @@ __device__ __forceinline__ int unit_swz(int k) { return PITCH >= 256 ? k & 3 : (
 
 enum Form { kScaled, kGated, kPlain };
 
-template <class T_, int FORM_, int BM_, int BN_, int WM_, int WN_, int STAGES_, bool ACOL_, bool BCOL_, int NSEG_>
+// KG groups of waves share a tile: group g multiplies quarters 4g/KG .. of every stage.  OCC
+// workgroups share a CU.
+template <class T_, int FORM_, int BM_, int BN_, int WM_, int WN_, int KG_, int STAGES_, int OCC_, bool ACOL_, bool BCOL_,
+          int NSEG_>
 struct TileCfg {
   typedef T_ T;
-  static constexpr int FORM = FORM_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, NSEG = NSEG_;
+  static constexpr int FORM = FORM_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KG = KG_, STAGES = STAGES_, OCC = OCC_;
+  static constexpr int NSEG = NSEG_;
   static constexpr bool ACOL = ACOL_, BCOL = BCOL_, GATED = FORM_ == kGated;
-  static constexpr int NW = (BM / WM) * (BN / WN), NWN = BN / WN;
+  static constexpr int NWN = BN / WN, NWT = (BM / WM) * NWN, NW = NWT * KG;    // waves: of a group, of the workgroup
+  static constexpr int QN = 4 / KG;                           // quarters of a stage a wave multiplies
   static constexpr int ROWB = 128, KE = ROWB / T::BYTES;      // bytes and elements of K per stage
   static constexpr int A_BYTES = BM * ROWB, STAGE = (BM + BN) * ROWB, LDS = STAGE * STAGES;
   static constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW, LOADS = IA + IB;   // 1 KB copies per wave per stage
@@ -71,8 +80,9 @@ struct TileCfg {
   static_assert(!(ACOL || BCOL) || T::BYTES == 2, "column operands are bf16");
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "copies per wave");
   static_assert(!GATED || BN / NW <= WN / 2, "each wave copies rows of one weight");
-  static_assert(NW * 32 * STRIP <= LDS && LDS <= 160 * 1024, "LDS");
+  static_assert(NW * 32 * STRIP <= LDS && LDS * OCC <= 160 * 1024, "LDS");
   static_assert(STAGES >= 2 && (STAGES - 1) * LOADS < 64, "vmcnt range");
+  static_assert(KG == 1 || KG == 2, "two quarters a wave at least");
 };
 
 struct Item { int l, s, tm, tn; };
@@ -99,55 +109,19 @@ __device__ __forceinline__ Item item_of(int wg, int total, int S, int tiles_m, i
 }
 
 template <class C, bool BF16, bool SAVE, bool SPLIT>
-__global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs a) {
+__global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_kernel(const DenseArgs a) {
   typedef typename C::T T;
-  constexpr int FI = C::FI, FJ = C::FJ;
+  constexpr int FI = C::FI, FJ = C::FJ, QN = C::QN;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / C::NWN, wn = wave % C::NWN;
+  const int kg = wave / C::NWT, wt = wave % C::NWT, wm = wt / C::NWN, wn = wt % C::NWN;
   const int hi = lane >> 5, r32 = lane & 31;
   const int tiles_m = (a.M + C::BM - 1) / C::BM, tiles_n = (a.N + C::OUTN - 1) / C::OUTN;
   const int total = a.L * tiles_m * tiles_n * a.S;
   const int KT1 = (a.K + C::KE - 1) / C::KE, KT = C::NSEG * KT1;
   const int lda = (int)a.lda, ldb = (int)a.ldb;
-
-  // ---- this lane's part of a copy: offsets from the tile's first byte ----
-  // Row operand, copy q of the wave: rows 8q' .. 8q'+7 (q' = wave * I + q), 8 lanes a row.
-  // Column operand: 1 KB of the stage's 64 K rows of BM (BN) columns.
-  uint32_t va[C::IA], vb[C::IB];
-  int ca[2], cb[2];          // row operands: the byte of K within the stage, even and odd copies
-#pragma unroll
-  for (int q = 0; q < C::IA; ++q) {
-    const int n = wave * C::IA + q;
-    if constexpr (C::ACOL) {
-      constexpr int PITCH = C::BM * 2;
-      const int p = 1024 * n + 16 * lane, k = p / PITCH, w = p % PITCH;
-      va[q] = (uint32_t)k * lda + (((w >> 6) ^ unit_swz<PITCH>(k)) << 6 | (w & 63));
-    } else {
-      const int row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
-      va[q] = (uint32_t)row * lda + c;
-      ca[n & 1] = c;
-    }
-  }
-  // Gated: the rows this wave copies belong to one of the weights; within the tile, row r
-  // of LDS is output column (r / WN) * WN/2 + r % (WN/2) of weight (r % WN) / (WN/2).
-  const int bwhich = C::GATED ? (wave * C::IB * 8) % C::WN / (C::WN / 2) : 0;
-#pragma unroll
-  for (int q = 0; q < C::IB; ++q) {
-    const int n = wave * C::IB + q;
-    if constexpr (C::BCOL) {
-      constexpr int PITCH = C::BN * 2;
-      const int p = 1024 * n + 16 * lane, k = p / PITCH, w = p % PITCH;
-      vb[q] = (uint32_t)k * ldb + (((w >> 6) ^ unit_swz<PITCH>(k)) << 6 | (w & 63));
-    } else {
-      const int row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
-      const int src = C::GATED ? row / C::WN * (C::WN / 2) + row % (C::WN / 2) : row;
-      vb[q] = (uint32_t)src * ldb + c;
-      cb[n & 1] = c;
-    }
-  }
 
   // ---- the current item ----
   Item it;
@@ -159,71 +133,130 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
     ks0 = (int)((int64_t)it.s * KT / a.S);
     KS = (int)((int64_t)(it.s + 1) * KT / a.S) - ks0;
   };
-  // Copy q (A's, then B's) of stage ks of the item into slot ks % STAGES.  A stage past the
-  // end of the slice has an empty resource: no traffic, zeros in a slot that is not used.
-  auto issue_one = [&](int ks, int q) {
-    uint8_t* base = smem + (ks % C::STAGES) * C::STAGE;
-    const int g = ks0 + ks;
-    const int seg = C::NSEG == 2 && g >= KT1 ? 1 : 0;
-    const int kk = g - seg * KT1;
-    const bool live = ks < KS;
-    if (q < C::IA) {
-      const uint8_t* src = a.A[C::NSEG == 2 ? seg : it.l];
-      if constexpr (C::ACOL) {
-        const int rows = min(a.K - kk * C::KE, C::KE);
-        const rsrc_t r = make_rsrc(src + (int64_t)kk * C::KE * lda + m0 * 2, live ? rows * lda - m0 * 2 : 0);
-        lds_buffer16(r, (lds_void*)(base + 1024 * (wave * C::IA + q)), va[q]);
-      } else {
-        const int rows = min(a.M - m0, C::BM), left = a.K * T::BYTES - kk * C::ROWB;
-        const rsrc_t r = make_rsrc(src + (int64_t)m0 * lda + kk * C::ROWB, live ? rows * lda - kk * C::ROWB : 0);
-        lds_buffer16(r, (lds_void*)(base + 1024 * (wave * C::IA + q)),
-                     ca[(wave * C::IA + q) & 1] < left ? va[q] : kNoLoad);
-      }
-    } else {
-      const int i = q - C::IA;
-      const uint8_t* src = a.B[C::NSEG == 2 ? seg : bwhich];
-      if constexpr (C::BCOL) {
-        const int rows = min(a.K - kk * C::KE, C::KE);
-        const rsrc_t r = make_rsrc(src + (int64_t)kk * C::KE * ldb + n0 * 2, live ? rows * ldb - n0 * 2 : 0);
-        lds_buffer16(r, (lds_void*)(base + C::A_BYTES + 1024 * (wave * C::IB + i)), vb[i]);
-      } else {
-        const int rows = min(a.N - n0, C::OUTN), left = a.K * T::BYTES - kk * C::ROWB;
-        const rsrc_t r = make_rsrc(src + (int64_t)n0 * ldb + kk * C::ROWB, live ? rows * ldb - kk * C::ROWB : 0);
-        lds_buffer16(r, (lds_void*)(base + C::A_BYTES + 1024 * (wave * C::IB + i)),
-                     cb[(wave * C::IB + i) & 1] < left ? vb[i] : kNoLoad);
-      }
+
+  // ---- copies ----
+  // The stage being copied, `ist` of the item's KS: where its rows start, how many bytes of the
+  // operand lie from there to the tile's end, this lane's offsets, its slot.  From one
+  // stage to the next only the starts move; stages before `plain` need no more than that,
+  // so that the scalar work of a stage stays small (it was half of a small tile's
+  // instructions when every copy formed its resource anew).
+  //   Row operand, copy q of the wave: rows 8n .. 8n+7 (n = wave * I + q), 8 lanes a row.
+  //   Column operand: 1 KB of the stage's 64 K rows of BM (BN) columns.
+  const uint8_t *pa = nullptr, *pb = nullptr;
+  int na = 0, nb = 0, ist = 0, plain = 0, wr = 0;
+  uint32_t va[C::IA], vb[C::IB];
+  // Gated: the rows this wave copies belong to one of the weights; within the tile, row r
+  // of LDS is output column (r / WN) * WN/2 + r % (WN/2) of weight (r % WN) / (WN/2).
+  const int bwhich = C::GATED ? (wave * C::IB * 8) % C::WN / (C::WN / 2) : 0;
+  // This lane's offset from the stage's start in copy n of a column operand of PITCH bytes a row.
+  auto col_offset = [&](auto pitch_c, int n, int ld) {
+    constexpr int PITCH = decltype(pitch_c)::value;
+    const int p = 1024 * n + 16 * lane, k = p / PITCH, w = p % PITCH;
+    return (uint32_t)k * ld + (((w >> 6) ^ unit_swz<PITCH>(k)) << 6 | (w & 63));
+  };
+  auto new_stage = [&]() {
+    if (ist >= KS) {   // past the slice: no traffic, zeros in a slot that is not used
+      na = nb = 0;
+      return;
     }
+    const int g = ks0 + ist, seg = C::NSEG == 2 && g >= KT1 ? 1 : 0, kk = g - seg * KT1;
+    const int left = a.K - kk * C::KE;
+    // The last stage of a segment may end inside a row, and the next segment starts afresh.
+    plain = kk + 1 >= KT1 ? ist + 1 : min(KS, ist + KT1 - 1 - kk);
+    const uint8_t* A = a.A[C::NSEG == 2 ? seg : it.l];
+    const uint8_t* B = a.B[C::NSEG == 2 ? seg : bwhich];
+    if constexpr (C::ACOL) {
+      pa = A + (int64_t)kk * C::KE * lda + m0 * 2;
+      na = min(left, C::KE) * lda - m0 * 2;
+    } else {
+      pa = A + (int64_t)m0 * lda + kk * C::ROWB;
+      na = min(a.M - m0, C::BM) * lda - kk * C::ROWB;
+    }
+#pragma unroll
+    for (int q = 0; q < C::IA; ++q) {
+      const int n = wave * C::IA + q, row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
+      if constexpr (C::ACOL) va[q] = col_offset(std::integral_constant<int, C::BM * 2>{}, n, lda);
+      else va[q] = c < left * T::BYTES ? (uint32_t)row * lda + c : kNoLoad;
+    }
+    if constexpr (C::BCOL) {
+      pb = B + (int64_t)kk * C::KE * ldb + n0 * 2;
+      nb = min(left, C::KE) * ldb - n0 * 2;
+    } else {
+      pb = B + (int64_t)n0 * ldb + kk * C::ROWB;
+      nb = min(a.N - n0, C::OUTN) * ldb - kk * C::ROWB;
+    }
+#pragma unroll
+    for (int q = 0; q < C::IB; ++q) {
+      const int n = wave * C::IB + q, row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
+      const int src = C::GATED ? row / C::WN * (C::WN / 2) + row % (C::WN / 2) : row;
+      if constexpr (C::BCOL) vb[q] = col_offset(std::integral_constant<int, C::BN * 2>{}, n, ldb);
+      else vb[q] = c < left * T::BYTES ? (uint32_t)src * ldb + c : kNoLoad;
+    }
+  };
+  auto next_stage = [&]() {
+    ++ist;
+    wr = wr + C::STAGE == C::LDS ? 0 : wr + C::STAGE;
+    if (ist < plain) {
+      pa += C::ACOL ? (int64_t)C::KE * lda : C::ROWB;
+      pb += C::BCOL ? (int64_t)C::KE * ldb : C::ROWB;
+      if constexpr (!C::ACOL) na -= C::ROWB;
+      if constexpr (!C::BCOL) nb -= C::ROWB;
+    } else {
+      new_stage();
+    }
+  };
+  // Copy q (A's, then B's) of the stage.
+  auto issue_one = [&](int q) {
+    if (q < C::IA) lds_buffer16(make_rsrc(pa, na), (lds_void*)(smem + wr + 1024 * (wave * C::IA + q)), va[q]);
+    else
+      lds_buffer16(make_rsrc(pb, nb), (lds_void*)(smem + wr + C::A_BYTES + 1024 * (wave * C::IB + q - C::IA)),
+                   vb[q - C::IA]);
   };
 
   // ---- fragments ----
+  // Of a row operand: block r's fragment of quarter j is at fo[j] + r * 32 rows.  Of a column
+  // operand: at fo[r] + j * 8 K rows; the 16 lanes of a group read K rows k, k+1, k+2, k+3
+  // (lane / 4) of 16 columns, and lane i of the group receives column i of all four.
   v4i fa[2][FI], fb[2][FJ];
-  // Column operand: the 16 lanes of a group read K rows k, k+1, k+2, k+3 (lane / 4) of 16
-  // columns; lane i of the group receives column i of all four.
+  constexpr int NFA = C::ACOL ? FI : QN, NFB = C::BCOL ? FJ : QN;
   const int ti = lane & 15, tq = ti >> 2, tb = ((lane >> 4) & 1) * 32 + (ti & 3) * 8;
-  auto read_col = [&](const uint8_t* tile, auto pitch_c, int blk, int kq) {
+  auto row_frag = [&](int row, int j) { return row * C::ROWB + (((4 * hi + kg * QN + j) ^ swz(r32)) << 4); };
+  auto col_frag = [&](auto pitch_c, int blk) {
     constexpr int PITCH = decltype(pitch_c)::value;
-    const uint8_t* p = tile + (32 * hi + 8 * kq + tq) * PITCH + ((blk ^ unit_swz<PITCH>(tq)) << 6) + tb;
-    const v2i lo = lds_read_tr16(p), up = lds_read_tr16(p + 4 * PITCH);
+    return (32 * hi + 8 * kg * QN + tq) * PITCH + ((blk ^ unit_swz<PITCH>(tq)) << 6) + tb;
+  };
+  int foa[NFA], fob[NFB], ca[NFA], cb[NFB];   // offsets within a slot, and with the slot's start
+#pragma unroll
+  for (int i = 0; i < NFA; ++i) {
+    if constexpr (C::ACOL) foa[i] = col_frag(std::integral_constant<int, C::BM * 2>{}, wm * FI + i);
+    else foa[i] = row_frag(wm * C::WM + r32, i);
+  }
+#pragma unroll
+  for (int i = 0; i < NFB; ++i) {
+    if constexpr (C::BCOL) fob[i] = C::A_BYTES + col_frag(std::integral_constant<int, C::BN * 2>{}, wn * FJ + i);
+    else fob[i] = C::A_BYTES + row_frag(wn * C::WN + r32, i);
+  }
+  int rd = 0;   // the slot being read
+  auto read_slot = [&]() {
+#pragma unroll
+    for (int i = 0; i < NFA; ++i) ca[i] = foa[i] + rd;
+#pragma unroll
+    for (int i = 0; i < NFB; ++i) cb[i] = fob[i] + rd;
+  };
+  auto read_col = [&](auto pitch_c, int at) {
+    constexpr int PITCH = decltype(pitch_c)::value;
+    const v2i lo = lds_read_tr16(smem + at), up = lds_read_tr16(smem + at + 4 * PITCH);
     return v4i{lo[0], lo[1], up[0], up[1]};
   };
-  auto read_frag = [&](int ks, int kq, int set, int r) {
-    const uint8_t* base = smem + (ks % C::STAGES) * C::STAGE;
-    const int c = 4 * hi + kq;
+  // Fragment r (A's, then B's) of quarter j of this wave.
+  auto read_frag = [&](int j, int r) {
     if (r < FI) {
-      if constexpr (C::ACOL) {
-        fa[set][r] = read_col(base, std::integral_constant<int, C::BM * 2>{}, wm * FI + r, kq);
-      } else {
-        const int row = wm * C::WM + r * 32 + r32;
-        fa[set][r] = *reinterpret_cast<const v4i*>(base + row * C::ROWB + ((c ^ swz(row)) << 4));
-      }
+      if constexpr (C::ACOL) fa[j & 1][r] = read_col(std::integral_constant<int, C::BM * 2>{}, ca[r] + j * (16 * C::BM));
+      else fa[j & 1][r] = *reinterpret_cast<const v4i*>(smem + ca[j] + r * (32 * C::ROWB));
     } else {
-      const int j = r - FI;
-      if constexpr (C::BCOL) {
-        fb[set][j] = read_col(base + C::A_BYTES, std::integral_constant<int, C::BN * 2>{}, wn * FJ + j, kq);
-      } else {
-        const int row = wn * C::WN + j * 32 + r32;
-        fb[set][j] = *reinterpret_cast<const v4i*>(base + C::A_BYTES + row * C::ROWB + ((c ^ swz(row)) << 4));
-      }
+      const int b = r - FI;
+      if constexpr (C::BCOL) fb[j & 1][b] = read_col(std::integral_constant<int, C::BN * 2>{}, cb[b] + j * (16 * C::BN));
+      else fb[j & 1][b] = *reinterpret_cast<const v4i*>(smem + cb[j] + b * (32 * C::ROWB));
     }
   };
 
@@ -245,56 +278,62 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
   // Copies 0 .. LH-1 of a stage go out under the last quarter of the stage STAGES before it
   // (right after the barrier that frees its slot), the rest under the following quarter 0.
   constexpr int LH = (C::LOADS + 1) / 2, FR = FI + FJ, NQ = FI * FJ;
-  auto mid_quarter = [&](int ks, auto kq_c) {
-    constexpr int KQ = decltype(kq_c)::value;
-    quarter(std::integral_constant<int, (KQ & 1)>{}, [&](int q) {
+  auto mid_quarter = [&](auto j_c) {
+    constexpr int J = decltype(j_c)::value;
+    quarter(std::integral_constant<int, (J & 1)>{}, [&](int q) {
 #pragma unroll
-      for (int r = q; r < FR; r += NQ) read_frag(ks, KQ + 1, (KQ + 1) & 1, r);
+      for (int r = q; r < FR; r += NQ) read_frag(J + 1, r);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (KQ == 0) {
+      if constexpr (J == 0) {
 #pragma unroll
-        for (int r = LH + q; r < C::LOADS; r += NQ) issue_one(ks + C::STAGES - 1, r);
+        for (int r = LH + q; r < C::LOADS; r += NQ) issue_one(r);
       }
     });
   };
   auto prologue = [&]() {
+    ist = wr = rd = 0;
+    new_stage();
 #pragma unroll
-    for (int p = 0; p < C::STAGES - 1; ++p)
+    for (int p = 0; p < C::STAGES - 1; ++p) {
 #pragma unroll
-      for (int q = 0; q < C::LOADS; ++q) issue_one(p, q);
+      for (int q = 0; q < C::LOADS; ++q) issue_one(q);
+      next_stage();
+    }
 #pragma unroll
-    for (int q = 0; q < LH; ++q) issue_one(C::STAGES - 1, q);
+    for (int q = 0; q < LH; ++q) issue_one(q);
   };
 
-  // Persistent: at most one workgroup per CU (times its occupancy) walks the items.
+  // Persistent: at most OCC workgroups per CU walk the items.
   for (int work = blockIdx.x; work < total; work += gridDim.x) {
     setup(work);
     prologue();
     // Stage 0 has landed once only the copies issued after it are in flight.
     wait_vmcnt<(C::STAGES - 2) * C::LOADS + LH>();
     barrier_lds();
+    read_slot();
 #pragma unroll
-    for (int r = 0; r < FR; ++r) read_frag(0, 0, 0, r);
+    for (int r = 0; r < FR; ++r) read_frag(0, r);
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
       for (int j = 0; j < FJ; ++j) acc[i][j] = typename T::acc32{};
 
     for (int ks = 0; ks < KS; ++ks) {
-      mid_quarter(ks, std::integral_constant<int, 0>{});
-      mid_quarter(ks, std::integral_constant<int, 1>{});
-      mid_quarter(ks, std::integral_constant<int, 2>{});
+      static_for<0, QN - 1>([&](auto j) { mid_quarter(j); });
       // Stage ks+1 has landed once at most the STAGES-2 stages after it are in flight; the
       // barrier publishes it and says that every wave has read slot ks % STAGES to its end
       // (the last quarter's fragments are in registers: barrier_lds waits for LDS reads).
       wait_vmcnt<(C::STAGES - 2) * C::LOADS>();
       barrier_lds();
-      quarter(std::integral_constant<int, 1>{}, [&](int q) {
+      next_stage();
+      rd = rd + C::STAGE == C::LDS ? 0 : rd + C::STAGE;
+      read_slot();
+      quarter(std::integral_constant<int, (QN - 1) & 1>{}, [&](int q) {
 #pragma unroll
-        for (int r = q; r < LH; r += NQ) issue_one(ks + C::STAGES, r);
+        for (int r = q; r < LH; r += NQ) issue_one(r);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = q; r < FR; r += NQ) read_frag(ks + 1, 0, 0, r);
+        for (int r = q; r < FR; r += NQ) read_frag(0, r);
       });
     }
     // ---- the end ----
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
     // A lane writes row r32 of every strip and reads column group `col` of it: the scales of
     // both are fetched here once, under the wait for the ring.
     constexpr int ELEM = SPLIT || !BF16 || SAVE ? 4 : 2, V = 16 / ELEM, LPR = C::WOUT / V;
-    static_assert(64 % LPR == 0, "a lane keeps its columns");
+    static_assert(64 % LPR == 0 && C::STRIP % 16 == 0, "a lane keeps its columns");
     constexpr bool SCALED = !SPLIT && std::is_same<T, I8>::value;
     typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
     const int col = lane % LPR * V, n = nw + col;
@@ -319,8 +358,11 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
     wait_vmcnt<0>();
     barrier_lds();
     uint8_t* strip = smem + wave * (32 * C::STRIP);
+    const uint8_t* strips = smem + wt * (32 * C::STRIP);   // group 0's; the other group's is GROUP further
+    constexpr int GROUP = C::NWT * 32 * C::STRIP, ROWS = 32 / C::KG;
 #pragma unroll
     for (int i = 0; i < FI; ++i) {
+      if (C::KG > 1 && i > 0) barrier_lds();
       // In: lane (hi, r32) holds row r32, columns j*32 + 8*g + 4*hi + 0..3 of block row i.
       // The row's scale goes into the 16 bytes past its sums.
 #pragma unroll
@@ -333,11 +375,22 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
               e4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
         }
       if constexpr (SCALED) *reinterpret_cast<float*>(strip + r32 * C::STRIP + C::WN * 4) = sm[i];
-      // Out: V columns a lane, along rows.
-      const int rows = min(a.M - (mw + i * 32), 32);
+      if constexpr (C::KG > 1) barrier_lds();
+      // Out: V columns a lane, along rows; with two groups each takes half of the rows and adds
+      // both groups' sums.
+      const int rows = min(a.M - (mw + i * 32), ROWS * (kg + 1));
 #pragma unroll 1
-      for (int row = lane / LPR; row < rows; row += 64 / LPR) {
-        const sum_t* g = reinterpret_cast<const sum_t*>(strip + row * C::STRIP) + col;
+      for (int row = ROWS * kg + lane / LPR; row < rows; row += 64 / LPR) {
+        typedef sum_t sumv __attribute__((ext_vector_type(4)));
+        sum_t g[(C::GATED ? 2 : 1) * V];
+#pragma unroll
+        for (int x = 0; x < (C::GATED ? 2 : 1) * V; x += 4) {
+          const sumv* p = reinterpret_cast<const sumv*>(strips + row * C::STRIP + (x / V * C::WOUT + col + x % V) * 4);
+          sumv v = *p;
+          if constexpr (C::KG > 1) v += p[GROUP / 16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[x + e] = v[e];
+        }
         const int64_t m = mw + i * 32 + row;
         if constexpr (SPLIT) {
           const int64_t pitch = partial_pitch(a.N);
@@ -345,14 +398,14 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
 #pragma unroll
             for (int w = 0; w < (C::GATED ? 2 : 1); ++w) {
               const int64_t plane = ((int64_t)it.l * a.S + it.s) * (C::GATED ? 2 : 1) + w;
-              *reinterpret_cast<v4i*>(static_cast<int*>(a.P) + (plane * a.M + m) * pitch + n) =
-                  *reinterpret_cast<const v4i*>(g + w * C::WOUT);
+              *reinterpret_cast<sumv*>(static_cast<sum_t*>(a.P) + (plane * a.M + m) * pitch + n) =
+                  sumv{g[w * V], g[w * V + 1], g[w * V + 2], g[w * V + 3]};
             }
           }
         } else if (n < a.N) {
           // int8 sums are exact in 32 bits and are rounded to fp32 here.
           float y[V], u[V], rs = 1.0f;
-          if constexpr (SCALED) rs = *reinterpret_cast<const float*>(strip + row * C::STRIP + C::WN * 4);
+          if constexpr (SCALED) rs = *reinterpret_cast<const float*>(strips + row * C::STRIP + C::WN * 4);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             y[e] = (float)g[e];
@@ -363,7 +416,7 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemm_kernel(const DenseArgs 
           if constexpr (C::GATED) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              u[e] = (float)g[C::WOUT + e];
+              u[e] = (float)g[V + e];
               if constexpr (SCALED) u[e] = u[e] * rs * sc[1][e];
             }
             if constexpr (SAVE) {
@@ -432,10 +485,10 @@ hipError_t launch_reduce(const DenseArgs& a, hipStream_t s) {
 }
 
 template <class C, bool BF16, bool SAVE>
-hipError_t launch_tiles(const DenseArgs& a, int per_cu, hipStream_t s) {
+hipError_t launch_tiles(const DenseArgs& a, hipStream_t s) {
   const int64_t items = a.L * ceil_div(a.M, C::BM) * ceil_div(a.N, C::OUTN) * a.S;
   if (items > INT32_MAX) return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)std::min<int64_t>(items, device_cus() * per_cu);
+  const unsigned grid = (unsigned)std::min<int64_t>(items, device_cus() * C::OCC);
   if (a.S > 1) {
     hipLaunchKernelGGL((dense_gemm_kernel<C, false, false, true>), dim3(grid), dim3(C::NW * 64), 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -449,29 +502,52 @@ hipError_t launch_tiles(const DenseArgs& a, int per_cu, hipStream_t s) {
 template <class T, int FORM, bool ACOL, bool BCOL, int NSEG, bool BF16, bool SAVE>
 hipError_t launch_cfg(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   switch (tile) {
-    case kTile256: return launch_tiles<TileCfg<T, FORM, 256, 256, 128, 128, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, 1, s);
-    case kTile128: return launch_tiles<TileCfg<T, FORM, 128, 128, 64, 64, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, 2, s);
-    default: return launch_tiles<TileCfg<T, FORM, 64, 128, 32, 64, 3, ACOL, BCOL, NSEG>, BF16, SAVE>(a, 2, s);
+    case kTile256: return launch_tiles<TileCfg<T, FORM, 256, 256, 128, 128, 1, 2, 1, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile128: return launch_tiles<TileCfg<T, FORM, 128, 128, 64, 64, 1, 2, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile128Deep: return launch_tiles<TileCfg<T, FORM, 128, 128, 64, 64, 2, 4, 1, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile64x128: return launch_tiles<TileCfg<T, FORM, 64, 128, 32, 64, 1, 3, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile64Deep: return launch_tiles<TileCfg<T, FORM, 64, 64, 32, 32, 2, 5, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile64: return launch_tiles<TileCfg<T, FORM, 64, 64, 32, 64, 2, 3, 3, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kGemv: break;
   }
+  return hipErrorInvalidConfiguration;
 }
 
 }  // namespace
 
 // Tile and K split of a product with `rows` x `cols` sums (gated: cols = 2 N), L of them,
-// each a sum of KT stages.
+// each a sum of KT stages: the pair with the least modelled time.  A round of items, n to a
+// CU, takes us[n-1] for each stage and `item` for its start and end; a split adds a launch
+// and the partial sums' way through memory.  The figures are fitted to the measured times of
+// 33 sizes of all five products, M = 20 .. 8192 (every tile, S = 1, 2, 4, 8); on those the
+// pair it picks is the fastest measured or within 4% of it.  What the tiles are for, in us:
+//   int8 8192^3: 256^2 477, 128^2 593, 64 x 128 731, 64^2 907
+//   int8 2048 x 4096 x 4096: 128^2 44.2, 256^2 58.8, 64 x 128 53.0
+//   int8 200 x 14336 x 4096: 128^2 of two groups 27.1, 128^2 38.0, 64 x 128 30.8
+//   int8 1003 x 1117 x 1040: 64 x 128 9.8, 128^2 13.7, 64^2 10.2
+//   int8 128 x 4096 x 4096: 64^2 of 5 stages 12.4, 64^2 of 3 stages 13.4, 64 x 128 16.7
+//   int8 100 x 1000 x 1024: 64^2 of 3 stages 6.3, of 5 stages 6.8, 64 x 128 7.9
 DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap) {
+  struct Tile { DenseTile t; int64_t bm, bn, occ; double us[3], item; };
+  static const Tile tiles[] = {{kTile256, 256, 256, 1, {1.69}, 4.6},
+                               {kTile128, 128, 128, 2, {0.81, 1.12}, 2.0},
+                               {kTile128Deep, 128, 128, 1, {0.53}, 3.6},
+                               {kTile64x128, 64, 128, 2, {0.40, 0.72}, 2.5},
+                               {kTile64Deep, 64, 64, 2, {0.24, 0.505}, 2.2},
+                               {kTile64, 64, 64, 3, {0.28, 0.56, 0.69}, 1.8}};
   const int64_t cus = device_cus();
-  struct { DenseTile t; int64_t bm, bn, per_cu; double stage_us; } const tiles[] = {
-      {kTile256, 256, 256, 1, 1.4}, {kTile128, 128, 128, 2, 0.75}, {kTile64, 64, 128, 2, 0.5}};
   DensePlan best{kTile64, 1};
   double best_t = 1e30;
-  for (const auto& c : tiles) {
-    const int64_t items = L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
-    for (int64_t S = 1; S <= std::min<int64_t>({cap, KT, kMaxSplits}); ++S) {
-      if (S > 1 && (KT / S < 4 || L * rows * (cols + 8) >= (int64_t)1 << 31)) break;   // 32-bit sums' indexes
-      const int64_t slots = cus * c.per_cu;
-      double t = (double)ceil_div(items * S, slots) * (ceil_div(KT, S) * c.stage_us + 2.0);
-      if (S > 1) t += 3.0 + (double)(L * rows * cols) * 4.0 * (S + 1) / 4.0e6;
+  for (const Tile& c : tiles) {
+    const int64_t items1 = L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
+    for (int64_t S = 1; S <= std::min<int64_t>(cap, kMaxSplits); S *= 2) {
+      // At least 4 stages a slice; the reduction's indexes are 32 bits.
+      if (S > 1 && (KT / S < 4 || L * rows * (cols + 8) >= (int64_t)1 << 31)) break;
+      const int64_t items = items1 * S, full = items / (cus * c.occ), rest = items % (cus * c.occ);
+      const double stages = (double)ceil_div(KT, S);
+      double t = (double)full * (stages * c.us[c.occ - 1] + c.item);
+      if (rest) t += stages * c.us[ceil_div(rest, cus) - 1] + c.item;
+      if (S > 1) t += 2.6 + (double)(L * rows * cols) * (double)(2 * S + 1) * 4.0 / 6.4e6;
       if (t < best_t) {
         best_t = t;
         best = DensePlan{c.t, (int)S};

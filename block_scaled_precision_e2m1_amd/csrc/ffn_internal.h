@@ -34,7 +34,7 @@ __host__ __device__
 #endif
 int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
-enum DenseTile { kTile256, kTile128, kTile64, kGemv };
+enum DenseTile { kTile256, kTile128, kTile128Deep, kTile64x128, kTile64Deep, kTile64, kGemv };
 struct DensePlan { DenseTile tile; int S; };
 
 // Tile and K split for L products of rows x cols sums (gated: cols counts both weights'
