@@ -89,22 +89,37 @@ struct Item { int l, s, tm, tn; };
 
 // Work item `wg` of `total`: consecutive ids go to the 8 XCDs in turn, so they are regrouped
 // to give each XCD a contiguous run, in which the slices of one tile are neighbours and the
-// tiles go in groups of 8 tile rows, column by column.
-__device__ __forceinline__ Item item_of(int wg, int total, int S, int tiles_m, int tiles_n) {
+// tiles go in groups of 8 tile rows, column by column.  Divisions take hundreds of cycles
+// before a workgroup's first copy, so those that a small product does not need are skipped.
+__device__ __forceinline__ Item item_of(int wg, int total, int S, int L, int tiles_m, int tiles_n) {
   // Runs of equal length; the first total % 8 of them take one more item.
   const int q = total >> 3, rem = total & 7, x = wg & 7;
-  int lin = x * q + min(x, rem) + (wg >> 3);
-  Item it;
-  it.s = lin % S;
-  lin /= S;
-  const int T = tiles_m * tiles_n;
-  it.l = lin / T;
-  const int t = lin - it.l * T;
+  uint32_t lin = x * q + min(x, rem) + (wg >> 3);
+  Item it{0, 0, 0, 0};
+  if (S > 1) {
+    it.s = lin % (uint32_t)S;
+    lin /= (uint32_t)S;
+  }
+  if (L > 1) {
+    const uint32_t T = tiles_m * tiles_n;
+    it.l = lin / T;
+    lin -= it.l * T;
+  }
   constexpr int G = 8;
-  const int group = t / (G * tiles_n), first = group * G, size = min(G, tiles_m - first);
-  const int in = t - group * G * tiles_n;
-  it.tm = first + in % size;
-  it.tn = in / size;
+  int first = 0, size = tiles_m;
+  if (tiles_m > G) {
+    const uint32_t group = lin / (uint32_t)(G * tiles_n);
+    first = group * G;
+    size = min(G, tiles_m - first);
+    lin -= first * tiles_n;
+  }
+  if (size == G) {
+    it.tm = first + lin % G;
+    it.tn = lin / G;
+  } else {
+    it.tn = lin / (uint32_t)size;
+    it.tm = first + lin - it.tn * size;
+  }
   return it;
 }
 
@@ -127,11 +142,15 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
   Item it;
   int m0 = 0, n0 = 0, ks0 = 0, KS = 0;
   auto setup = [&](int work) {
-    it = item_of(work, total, a.S, tiles_m, tiles_n);
+    it = item_of(work, total, a.S, a.L, tiles_m, tiles_n);
     m0 = it.tm * C::BM;
     n0 = it.tn * C::OUTN;
-    ks0 = (int)((int64_t)it.s * KT / a.S);
-    KS = (int)((int64_t)(it.s + 1) * KT / a.S) - ks0;
+    ks0 = 0;
+    KS = KT;
+    if (SPLIT) {   // S slices, S <= 16 and KT < 2^20
+      ks0 = (uint32_t)(it.s * KT) / (uint32_t)a.S;
+      KS = (uint32_t)((it.s + 1) * KT) / (uint32_t)a.S - ks0;
+    }
   };
 
   // ---- copies ----
@@ -248,8 +267,10 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
     const v2i lo = lds_read_tr16(smem + at), up = lds_read_tr16(smem + at + 4 * PITCH);
     return v4i{lo[0], lo[1], up[0], up[1]};
   };
-  // Fragment r (A's, then B's) of quarter j of this wave.
-  auto read_frag = [&](int j, int r) {
+  // Fragment x of quarter j of this wave, in the order the matrix instructions want them: the
+  // first of B and of A, then the rest of B's, then of A's.
+  auto read_frag = [&](int j, int x) {
+    const int r = x == 1 ? 0 : x > FJ ? x - FJ : x == 0 ? FI : FI + x - 1;
     if (r < FI) {
       if constexpr (C::ACOL) fa[j & 1][r] = read_col(std::integral_constant<int, C::BM * 2>{}, ca[r] + j * (16 * C::BM));
       else fa[j & 1][r] = *reinterpret_cast<const v4i*>(smem + ca[j] + r * (32 * C::ROWB));
@@ -275,19 +296,32 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // Copies 0 .. LH-1 of a stage go out under the last quarter of the stage STAGES before it
-  // (right after the barrier that frees its slot), the rest under the following quarter 0.
-  constexpr int LH = (C::LOADS + 1) / 2, FR = FI + FJ, NQ = FI * FJ;
+  // When the memory instructions of a stage go out.  The fragments of the next quarter are
+  // read evenly over a quarter's NQ matrix instructions, and a stage's copies evenly over
+  // two quarters: the last one of the stage STAGES before it (after the barrier that frees
+  // its slot) and the next stage's first.  Bursts of either stall the waves that issue them:
+  // at 8192 x 14336 x 4096 the backward products take 1508 and 1585 us with one of each after
+  // every matrix instruction until they are out, 1458 and 1541 us spread.  Copies spread
+  // over three quarters land too late (1550 and 1555 us), in one they crowd (1604, 1681).
+  constexpr int FR = FI + FJ, NQ = FI * FJ;
+  constexpr int LH = (C::LOADS + 1) / 2;   // copies in the last quarter
+  auto copies = [&](auto part_c, int q) {   // part 0: the last quarter, 1: quarter 0
+    constexpr int PART = decltype(part_c)::value;
+#pragma unroll
+    for (int c = 0; c < C::LOADS; ++c)
+      if (2 * c * NQ / C::LOADS == PART * NQ + q) issue_one(c);
+  };
+  auto reads = [&](int j, int q) {
+#pragma unroll
+    for (int r = 0; r < FR; ++r)
+      if (r * NQ / FR == q) read_frag(j, r);
+  };
   auto mid_quarter = [&](auto j_c) {
     constexpr int J = decltype(j_c)::value;
     quarter(std::integral_constant<int, (J & 1)>{}, [&](int q) {
-#pragma unroll
-      for (int r = q; r < FR; r += NQ) read_frag(J + 1, r);
+      reads(J + 1, q);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (J == 0) {
-#pragma unroll
-        for (int r = LH + q; r < C::LOADS; r += NQ) issue_one(r);
-      }
+      if constexpr (J == 0) copies(std::integral_constant<int, 1>{}, q);
     });
   };
   auto prologue = [&]() {
@@ -306,6 +340,24 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
   // Persistent: at most OCC workgroups per CU walk the items.
   for (int work = blockIdx.x; work < total; work += gridDim.x) {
     setup(work);
+    // A lane writes row r32 of every strip of the wave's sums and reads column group `col` of it:
+    // it fetches the scales of both here, so that the end does not wait for them.
+    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
+    constexpr int ELEM = SPLIT || !BF16 || SAVE ? 4 : 2, V = 16 / ELEM, LPR = C::WOUT / V;
+    static_assert(64 % LPR == 0 && C::STRIP % 16 == 0, "a lane keeps its columns");
+    constexpr bool SCALED = !SPLIT && std::is_same<T, I8>::value;
+    typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
+    const int col = lane % LPR * V, n = nw + col;
+    float sm[FI], sc[C::GATED ? 2 : 1][V];
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int i = 0; i < FI; ++i) sm[i] = a.sa[min(mw + i * 32 + r32, a.M - 1)];
+#pragma unroll
+      for (int w = 0; w < (C::GATED ? 2 : 1); ++w)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sc[w][e] = a.sb[w][min(n + e, a.N - 1)];
+    }
+    __builtin_amdgcn_sched_barrier(0);   // before the copies: the counted waits below skip none of those
     prologue();
     // Stage 0 has landed once only the copies issued after it are in flight.
     wait_vmcnt<(C::STAGES - 2) * C::LOADS + LH>();
@@ -329,31 +381,12 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
       rd = rd + C::STAGE == C::LDS ? 0 : rd + C::STAGE;
       read_slot();
       quarter(std::integral_constant<int, (QN - 1) & 1>{}, [&](int q) {
-#pragma unroll
-        for (int r = q; r < LH; r += NQ) issue_one(r);
+        copies(std::integral_constant<int, 0>{}, q);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int r = q; r < FR; r += NQ) read_frag(0, r);
+        reads(0, q);
       });
     }
     // ---- the end ----
-    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
-    // A lane writes row r32 of every strip and reads column group `col` of it: the scales of
-    // both are fetched here once, under the wait for the ring.
-    constexpr int ELEM = SPLIT || !BF16 || SAVE ? 4 : 2, V = 16 / ELEM, LPR = C::WOUT / V;
-    static_assert(64 % LPR == 0 && C::STRIP % 16 == 0, "a lane keeps its columns");
-    constexpr bool SCALED = !SPLIT && std::is_same<T, I8>::value;
-    typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
-    const int col = lane % LPR * V, n = nw + col;
-    float sm[FI], sc[C::GATED ? 2 : 1][V];
-    if constexpr (SCALED) {
-#pragma unroll
-      for (int i = 0; i < FI; ++i) sm[i] = a.sa[min(mw + i * 32 + r32, a.M - 1)];
-#pragma unroll
-      for (int w = 0; w < (C::GATED ? 2 : 1); ++w)
-#pragma unroll
-        for (int e = 0; e < V; ++e) sc[w][e] = a.sb[w][min(n + e, a.N - 1)];
-    }
     // No copy may still be landing when the ring is reused, and no wave may still read it.
     wait_vmcnt<0>();
     barrier_lds();

@@ -121,6 +121,22 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
 #pragma unroll
       for (int j = 0; j < C::P; ++j) acc[b][t][j] = acc_t{};
 
+  // The output items of this wave (token tile, row group) and the scales of its lanes there,
+  // fetched here so that the end does not wait for them.
+  constexpr int OUT = C::TT * C::RG, MY = (OUT + C::NW - 1) / C::NW;
+  float sm[MY], sc[MY][C::GATES][4];
+  if constexpr (std::is_same<T, I8>::value) {
+#pragma unroll
+    for (int x = 0; x < MY; ++x) {
+      const int item = min(wave + x * C::NW, OUT - 1);
+      sm[x] = a.sa[min(C::TOK * (item % C::TT) + r, a.M - 1)];
+#pragma unroll
+      for (int g = 0; g < C::GATES; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[x][g][e] = a.sb[g][min(n0 + 16 * (item / C::TT) + 4 * s + e, a.N - 1)];
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
   static_for<0, C::D>([&](auto d) { issue(first + decltype(d)::value, d); });
   for (int i = first; i < last; i += C::D) {
     static_for<0, C::D>([&](auto d_c) {
@@ -155,7 +171,10 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
       for (int j = 0; j < C::P; ++j)
         part[(((wave * C::NB + b) * C::TT + t) * C::P + j) * 64 + lane] = acc[b][t][j];
   barrier_lds();
-  for (int item = wave; item < C::TT * C::RG; item += C::NW) {
+#pragma unroll
+  for (int x = 0; x < MY; ++x) {
+    const int item = wave + x * C::NW;
+    if (item >= OUT) break;
     const int tile = item % C::TT, rg = item / C::TT;
     const int m = C::TOK * tile + r, n = n0 + 16 * rg + 4 * s, left = a.N - n;
     if (r >= C::TOK || m >= a.M || n >= a.N) continue;
@@ -182,7 +201,7 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         y[g][e] = (float)sum[g][e];
-        if constexpr (std::is_same<T, I8>::value) y[g][e] = y[g][e] * a.sa[m] * a.sb[g][min(n + e, a.N - 1)];
+        if constexpr (std::is_same<T, I8>::value) y[g][e] = y[g][e] * sm[x] * sc[x][g][e];
       }
     const int64_t at = (int64_t)m * a.N + n;
     if constexpr (C::GATES == 2) {
