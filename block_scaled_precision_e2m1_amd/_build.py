@@ -93,7 +93,7 @@ def build_binding() -> str:
     cmd += [BINDING_SRC, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
     for path in cpp_extension.library_paths():
         cmd += ["-L" + path]
-    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_python"]
+    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stdout}{r.stderr}")

@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 
 #include <cstring>
@@ -89,7 +90,7 @@ struct Unlocked {
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
   const Unlocked u;
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+  return at::Tensor(at::detail::empty_cuda(shape, dtype, device, std::nullopt));   // what at::empty ends in
 }
 at::Tensor result(PyObject* out, const char* name, at::ScalarType dtype, at::IntArrayRef shape, at::Device device) {
   return out == Py_None ? empty(shape, dtype, device) : need(out, name, dtype, shape, device);

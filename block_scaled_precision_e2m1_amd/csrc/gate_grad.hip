@@ -29,9 +29,9 @@ gate_grad_kernel(int64_t M, int N, int pitch, const uint16_t* __restrict__ dH, c
     const int64_t at = m * N + n;
     float h[8], g[8], u[8];
     if (n + 8 <= N) {
-      const v4i w = *reinterpret_cast<const v4i_any*>(dH + at);
-      const v4f g0 = *reinterpret_cast<const v4f_any*>(G + at), g1 = *reinterpret_cast<const v4f_any*>(G + at + 4);
-      const v4f u0 = *reinterpret_cast<const v4f_any*>(U + at), u1 = *reinterpret_cast<const v4f_any*>(U + at + 4);
+      const v4i w = __builtin_nontemporal_load(reinterpret_cast<const v4i_any*>(dH + at));
+      const v4f g0 = __builtin_nontemporal_load(reinterpret_cast<const v4f_any*>(G + at)), g1 = __builtin_nontemporal_load(reinterpret_cast<const v4f_any*>(G + at + 4));
+      const v4f u0 = __builtin_nontemporal_load(reinterpret_cast<const v4f_any*>(U + at)), u1 = __builtin_nontemporal_load(reinterpret_cast<const v4f_any*>(U + at + 4));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         h[e] = __builtin_bit_cast(float, e & 1 ? (uint32_t)w[e / 2] & 0xffff0000u : (uint32_t)w[e / 2] << 16);
