@@ -77,15 +77,12 @@ int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
 DensePlan product_plan(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t room) {
   const int64_t cap = slices(M, N, gates, 1, room);
   if (fp4g::gemv_takes(M, N, K * elem, gates))
-    return DensePlan{fp4g::kGemv, fp4g::gemv_splits(M, N, K * elem, gates, cap)};
+    return DensePlan{fp4g::kGemv, fp4g::gemv_splits(M, N, K * elem, gates, cap), 0.0};
   return fp4g::dense_plan(M, gates * N, 1, stages(K, elem), cap);
 }
-// The plans of dX (one product over both gradients' K) and of dWg and dWu.
-DensePlan input_grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
-  return fp4g::dense_plan(M, K, 1, 2 * stages(N, 2), slices(M, K, 1, 1, room));
-}
-DensePlan weight_grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
-  return fp4g::dense_plan(N, K, 2, stages(M, 2), slices(N, K, 1, 2, room));
+// dX (one product over both gradients' K) and dWg and dWu; their partial sums share the room.
+fp4g::GradPlan grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
+  return fp4g::grad_plan(M, N, K, slices(M, K, 1, 1, room), slices(N, K, 1, 2, room));
 }
 
 fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t* bytes) {
@@ -217,8 +214,8 @@ fp4g_status gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K, 
   *bytes = *least = 0;
   if (M == 0 || N == 0 || K == 0) return FP4G_OK;
   *least = (size_t)(4 * M * pitch);
-  const size_t x = partial_bytes(M, K, 1, 1, input_grad_plan(M, N, K, kAnyRoom));
-  const size_t w = partial_bytes(N, K, 1, 2, weight_grad_plan(M, N, K, kAnyRoom));
+  const fp4g::GradPlan p = grad_plan(M, N, K, kAnyRoom);
+  const size_t x = partial_bytes(M, K, 1, 1, p.x), w = partial_bytes(N, K, 1, 2, p.w);
   *bytes = *least + (x > w ? x : w);
   return FP4G_OK;
 }
@@ -253,23 +250,17 @@ fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH,
   const size_t room = workspace_bytes - least;
   hipError_t e = fp4g::launch_gate_grad(M, N, pitch, dH, G, U, act, dG, dU, s);
   if (e != hipSuccess) return FP4G_EHIP;
-  {
-    const DensePlan p = input_grad_plan(M, N, K, room);
-    DenseArgs a;
-    a.M = (int)M, a.N = (int)K, a.K = (int)N, a.S = p.S;
-    a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;
-    a.B[0] = static_cast<const uint8_t*>(Wg), a.B[1] = static_cast<const uint8_t*>(Wu), a.ldb = K * 2;
-    a.D[0] = dX, a.P = P;
-    e = fp4g::launch_grad_input(a, p.tile, s);
-    if (e != hipSuccess) return FP4G_EHIP;
-  }
-  const DensePlan p = weight_grad_plan(M, N, K, room);
-  DenseArgs a;
-  a.M = (int)N, a.N = (int)K, a.K = (int)M, a.L = 2, a.S = p.S;
-  a.A[0] = dG, a.A[1] = dU, a.lda = pitch * 2;
-  a.B[0] = static_cast<const uint8_t*>(X), a.ldb = K * 2;
-  a.D[0] = dWg, a.D[1] = dWu, a.P = P;
-  return finish(fp4g::launch_grad_weights(a, p.tile, s));
+  const fp4g::GradPlan p = grad_plan(M, N, K, room);
+  DenseArgs x, w;
+  x.M = (int)M, x.N = (int)K, x.K = (int)N, x.S = p.x.S;
+  x.A[0] = dG, x.A[1] = dU, x.lda = pitch * 2;
+  x.B[0] = static_cast<const uint8_t*>(Wg), x.B[1] = static_cast<const uint8_t*>(Wu), x.ldb = K * 2;
+  x.D[0] = dX, x.P = P;
+  w.M = (int)N, w.N = (int)K, w.K = (int)M, w.L = 2, w.S = p.w.S;
+  w.A[0] = dG, w.A[1] = dU, w.lda = pitch * 2;
+  w.B[0] = static_cast<const uint8_t*>(X), w.ldb = K * 2;
+  w.D[0] = dWg, w.D[1] = dWu, w.P = P;
+  return finish(fp4g::launch_grads(x, w, p, s));
 }
 
 }  // extern "C"

@@ -46,6 +46,7 @@
 #include <algorithm>
 
 #include "dense.hpp"
+#include "launch.hpp"
 
 namespace fp4g {
 namespace {
@@ -123,11 +124,11 @@ __device__ __forceinline__ Item item_of(int wg, int total, int S, int L, int til
   return it;
 }
 
+// The items `block`, `block` + `grid`, .. of a product, by one workgroup.
 template <class C, bool BF16, bool SAVE, bool SPLIT>
-__global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_kernel(const DenseArgs a) {
+__device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int grid, uint8_t* smem) {
   typedef typename C::T T;
   constexpr int FI = C::FI, FJ = C::FJ, QN = C::QN;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
   };
 
   // Persistent: at most OCC workgroups per CU walk the items.
-  for (int work = blockIdx.x; work < total; work += gridDim.x) {
+  for (int work = block; work < total; work += grid) {
     setup(work);
     // A lane writes row r32 of every strip of the wave's sums and reads column group `col` of it:
     // it fetches the scales of both here, so that the end does not wait for them.
@@ -467,6 +468,25 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_ker
   }
 }
 
+template <class C, bool BF16, bool SAVE, bool SPLIT>
+__global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) dense_gemm_kernel(const DenseArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
+  dense_gemm<C, BF16, SAVE, SPLIT>(a, blockIdx.x, gridDim.x, smem);
+}
+
+// Both backward products in one launch: workgroups 0 .. split-1 take the items of x (dX), the
+// others those of w (dWg and dWu).  They need the same operands and neither fills the GPU
+// where they are small.
+template <class CX, class CW, bool SPLITX>
+__global__ void __launch_bounds__(CX::NW * 64, CX::NW * CX::OCC / 4)
+dense_grads_kernel(const DenseArgs x, const DenseArgs w, int split) {
+  static_assert(CX::NW == CW::NW && CX::LDS == CW::LDS && CX::OCC == CW::OCC, "one launch shape");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[CX::LDS];
+  const int b = blockIdx.x;
+  if (b < split) dense_gemm<CX, true, false, SPLITX>(x, b, split, smem);
+  else dense_gemm<CW, true, false, false>(w, b - split, gridDim.x - split, smem);
+}
+
 // The end of a split product: sums of the S slices in slice order, then what the unsplit
 // kernel does with its sums.  HBM-bound: S (times 2 when gated) 32-bit values in, one out.
 // Rows of partial sums are padded to whole groups of 4, one group a lane.
@@ -513,8 +533,7 @@ template <class T, bool GATED, bool BF16, bool SAVE>
 hipError_t launch_reduce(const DenseArgs& a, hipStream_t s) {
   const int64_t units = ceil_div(a.L * a.M * (partial_pitch(a.N) / 4), 256);
   const unsigned grid = (unsigned)std::min<int64_t>(units, device_cus() * 8);
-  hipLaunchKernelGGL((dense_reduce_kernel<T, GATED, BF16, SAVE>), dim3(grid), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return launch(dense_reduce_kernel<T, GATED, BF16, SAVE>, grid, 256, s, a);
 }
 
 template <class C, bool BF16, bool SAVE>
@@ -523,27 +542,73 @@ hipError_t launch_tiles(const DenseArgs& a, hipStream_t s) {
   if (items > INT32_MAX) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)std::min<int64_t>(items, device_cus() * C::OCC);
   if (a.S > 1) {
-    hipLaunchKernelGGL((dense_gemm_kernel<C, false, false, true>), dim3(grid), dim3(C::NW * 64), 0, s, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch(dense_gemm_kernel<C, false, false, true>, grid, C::NW * 64, s, a);
     if (e != hipSuccess) return e;
     return launch_reduce<typename C::T, C::GATED, BF16, SAVE>(a, s);
   }
-  hipLaunchKernelGGL((dense_gemm_kernel<C, BF16, SAVE, false>), dim3(grid), dim3(C::NW * 64), 0, s, a);
-  return hipGetLastError();
+  return launch(dense_gemm_kernel<C, BF16, SAVE, false>, grid, C::NW * 64, s, a);
 }
 
-template <class T, int FORM, bool ACOL, bool BCOL, int NSEG, bool BF16, bool SAVE>
+// The tiles by name, for one form of product.
+template <class T, int FORM, bool ACOL, bool BCOL, int NSEG>
+struct Tiles {
+  template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC>
+  using Cfg = TileCfg<T, FORM, BM, BN, WM, WN, KG, STAGES, OCC, ACOL, BCOL, NSEG>;
+  typedef Cfg<256, 256, 128, 128, 1, 2, 1> t256;
+  typedef Cfg<128, 128, 64, 64, 1, 2, 2> t128;
+  typedef Cfg<128, 128, 64, 64, 2, 4, 1> t128_deep;
+  typedef Cfg<64, 128, 32, 64, 1, 3, 2> t64x128;
+  typedef Cfg<64, 64, 32, 32, 2, 5, 2> t64_deep;
+  typedef Cfg<64, 64, 32, 64, 2, 3, 3> t64;
+};
+typedef Tiles<BF, kPlain, false, true, 2> GradInput;    // dX = [dG dU] [Wg; Wu]: A rows hold K, B rows are K
+typedef Tiles<BF, kPlain, true, true, 1> GradWeights;   // dWg = dG^T X, dWu = dU^T X: both operands' rows are K
+
+template <class S, bool BF16, bool SAVE>
 hipError_t launch_cfg(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   switch (tile) {
-    case kTile256: return launch_tiles<TileCfg<T, FORM, 256, 256, 128, 128, 1, 2, 1, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
-    case kTile128: return launch_tiles<TileCfg<T, FORM, 128, 128, 64, 64, 1, 2, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
-    case kTile128Deep: return launch_tiles<TileCfg<T, FORM, 128, 128, 64, 64, 2, 4, 1, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
-    case kTile64x128: return launch_tiles<TileCfg<T, FORM, 64, 128, 32, 64, 1, 3, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
-    case kTile64Deep: return launch_tiles<TileCfg<T, FORM, 64, 64, 32, 32, 2, 5, 2, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
-    case kTile64: return launch_tiles<TileCfg<T, FORM, 64, 64, 32, 64, 2, 3, 3, ACOL, BCOL, NSEG>, BF16, SAVE>(a, s);
+    case kTile256: return launch_tiles<typename S::t256, BF16, SAVE>(a, s);
+    case kTile128: return launch_tiles<typename S::t128, BF16, SAVE>(a, s);
+    case kTile128Deep: return launch_tiles<typename S::t128_deep, BF16, SAVE>(a, s);
+    case kTile64x128: return launch_tiles<typename S::t64x128, BF16, SAVE>(a, s);
+    case kTile64Deep: return launch_tiles<typename S::t64_deep, BF16, SAVE>(a, s);
+    case kTile64: return launch_tiles<typename S::t64, BF16, SAVE>(a, s);
     case kGemv: break;
   }
   return hipErrorInvalidConfiguration;
+}
+
+template <class CX, class CW>
+hipError_t launch_both(const DenseArgs& x, const DenseArgs& w, hipStream_t s) {
+  const int64_t slots = device_cus() * CX::OCC;
+  const int64_t nx = x.S * ceil_div(x.M, CX::BM) * ceil_div(x.N, CX::OUTN);
+  const int64_t nw = w.L * ceil_div(w.M, CW::BM) * ceil_div(w.N, CW::OUTN);
+  if (nx > INT32_MAX || nw > INT32_MAX) return hipErrorInvalidConfiguration;
+  // A multiple of 8 workgroups for x, so that the others' ids keep their XCDs.
+  const int split = (int)(ceil_div(std::min(nx, slots), 8) * 8);
+  const unsigned grid = (unsigned)(split + std::min(nw, slots));
+  if (x.S == 1) return launch(dense_grads_kernel<CX, CW, false>, grid, CX::NW * 64, s, x, w, split);
+  const hipError_t e = launch(dense_grads_kernel<CX, CW, true>, grid, CX::NW * 64, s, x, w, split);
+  return e != hipSuccess ? e : launch_reduce<BF, false, true, false>(x, s);
+}
+
+struct Tile { DenseTile t; int64_t bm, bn, occ; double us[3], item; };
+const Tile kTiles[] = {{kTile256, 256, 256, 1, {1.69}, 4.6},
+                       {kTile128, 128, 128, 2, {0.81, 1.12}, 2.0},
+                       {kTile128Deep, 128, 128, 1, {0.53}, 3.6},
+                       {kTile64x128, 64, 128, 2, {0.40, 0.72}, 2.5},
+                       {kTile64Deep, 64, 64, 2, {0.24, 0.505}, 2.2},
+                       {kTile64, 64, 64, 3, {0.28, 0.56, 0.69}, 1.8}};
+
+int64_t items_of(const Tile& c, int64_t rows, int64_t cols, int64_t L) {
+  return L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
+}
+double split_us(int64_t rows, int64_t cols, int64_t L, int64_t S) {
+  return S > 1 ? 2.6 + (double)(L * rows * cols) * (double)(2 * S + 1) * 4.0 / 6.4e6 : 0.0;
+}
+// A slice holds at least 4 stages; the reduction's indexes are 32 bits.
+bool can_split(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t S, int64_t cap) {
+  return S == 1 || (S <= std::min<int64_t>(cap, kMaxSplits) && KT / S >= 4 && L * rows * (cols + 8) < (int64_t)1 << 31);
 }
 
 }  // namespace
@@ -561,29 +626,37 @@ hipError_t launch_cfg(const DenseArgs& a, DenseTile tile, hipStream_t s) {
 //   int8 128 x 4096 x 4096: 64^2 of 5 stages 12.4, 64^2 of 3 stages 13.4, 64 x 128 16.7
 //   int8 100 x 1000 x 1024: 64^2 of 3 stages 6.3, of 5 stages 6.8, 64 x 128 7.9
 DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap) {
-  struct Tile { DenseTile t; int64_t bm, bn, occ; double us[3], item; };
-  static const Tile tiles[] = {{kTile256, 256, 256, 1, {1.69}, 4.6},
-                               {kTile128, 128, 128, 2, {0.81, 1.12}, 2.0},
-                               {kTile128Deep, 128, 128, 1, {0.53}, 3.6},
-                               {kTile64x128, 64, 128, 2, {0.40, 0.72}, 2.5},
-                               {kTile64Deep, 64, 64, 2, {0.24, 0.505}, 2.2},
-                               {kTile64, 64, 64, 3, {0.28, 0.56, 0.69}, 1.8}};
   const int64_t cus = device_cus();
-  DensePlan best{kTile64, 1};
-  double best_t = 1e30;
-  for (const Tile& c : tiles) {
-    const int64_t items1 = L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
-    for (int64_t S = 1; S <= std::min<int64_t>(cap, kMaxSplits); S *= 2) {
-      // At least 4 stages a slice; the reduction's indexes are 32 bits.
-      if (S > 1 && (KT / S < 4 || L * rows * (cols + 8) >= (int64_t)1 << 31)) break;
-      const int64_t items = items1 * S, full = items / (cus * c.occ), rest = items % (cus * c.occ);
+  DensePlan best{kTile64, 1, 1e30};
+  for (const Tile& c : kTiles)
+    for (int64_t S = 1; can_split(rows, cols, L, KT, S, cap); S *= 2) {
+      const int64_t items = items_of(c, rows, cols, L) * S, full = items / (cus * c.occ), rest = items % (cus * c.occ);
       const double stages = (double)ceil_div(KT, S);
-      double t = (double)full * (stages * c.us[c.occ - 1] + c.item);
+      double t = split_us(rows, cols, L, S) + (double)full * (stages * c.us[c.occ - 1] + c.item);
       if (rest) t += stages * c.us[ceil_div(rest, cus) - 1] + c.item;
-      if (S > 1) t += 2.6 + (double)(L * rows * cols) * (double)(2 * S + 1) * 4.0 / 6.4e6;
+      if (t < best.us) best = DensePlan{c.t, (int)S, t};
+    }
+  return best;
+}
+
+// Both backward products in one launch, dX with S slices: the chip's throughput over all their
+// items, or the longest item, whichever is more.  Taken where that beats the two launches
+// and the microsecond or two between them.
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int64_t cap_x, int64_t cap_w) {
+  const int64_t cus = device_cus(), KX = 2 * ceil_div(N, 64), KW = ceil_div(M, 64);
+  GradPlan best{dense_plan(M, K, 1, KX, cap_x), dense_plan(N, K, 2, KW, cap_w), false};
+  double best_t = best.x.us + best.w.us + 1.5;
+  for (const Tile& c : kTiles) {
+    if (c.t != kTile64 && c.t != kTile64Deep && c.t != kTile64x128) continue;
+    for (int64_t S = 1; can_split(M, K, 1, KX, S, cap_x); S *= 2) {
+      const int64_t nx = items_of(c, M, K, 1) * S, nw = items_of(c, N, K, 2);
+      const double sx = (double)ceil_div(KX, S), sw = (double)KW, us = c.us[c.occ - 1];
+      const double all = ((double)nx * (sx * us + c.item) + (double)nw * (sw * us + c.item)) / (double)(cus * c.occ);
+      const double one = std::max(sx, sw) * c.us[std::min<int64_t>(c.occ, ceil_div(nx + nw, cus)) - 1] + c.item;
+      const double t = std::max(all, one) + split_us(M, K, 1, S);
       if (t < best_t) {
         best_t = t;
-        best = DensePlan{c.t, (int)S};
+        best = GradPlan{{c.t, (int)S, t}, {c.t, 1, t}, true};
       }
     }
   }
@@ -598,30 +671,33 @@ hipError_t launch_partial_sums(const DenseArgs& a, bool int8, bool gated, hipStr
 
 hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   if (tile == kGemv) return launch_gemv_w8a8(a, s);
-  return a.bf16_out ? launch_cfg<I8, kScaled, false, false, 1, true, false>(a, tile, s)
-              : launch_cfg<I8, kScaled, false, false, 1, false, false>(a, tile, s);
+  return a.bf16_out ? launch_cfg<Tiles<I8, kScaled, false, false, 1>, true, false>(a, tile, s)
+              : launch_cfg<Tiles<I8, kScaled, false, false, 1>, false, false>(a, tile, s);
 }
 
 hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   if (tile == kGemv) return launch_gemv_w8a8_gated(a, s);
-  return a.bf16_out ? launch_cfg<I8, kGated, false, false, 1, true, false>(a, tile, s)
-              : launch_cfg<I8, kGated, false, false, 1, false, false>(a, tile, s);
+  return a.bf16_out ? launch_cfg<Tiles<I8, kGated, false, false, 1>, true, false>(a, tile, s)
+              : launch_cfg<Tiles<I8, kGated, false, false, 1>, false, false>(a, tile, s);
 }
 
 hipError_t launch_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   if (tile == kGemv) return launch_gemv_gated(a, s);
-  return a.G ? launch_cfg<BF, kGated, false, false, 1, true, true>(a, tile, s)
-             : launch_cfg<BF, kGated, false, false, 1, true, false>(a, tile, s);
+  return a.G ? launch_cfg<Tiles<BF, kGated, false, false, 1>, true, true>(a, tile, s)
+             : launch_cfg<Tiles<BF, kGated, false, false, 1>, true, false>(a, tile, s);
 }
 
-// dX = [dG dU] [Wg; Wu]: A rows hold K, B rows are K.
-hipError_t launch_grad_input(const DenseArgs& a, DenseTile tile, hipStream_t s) {
-  return launch_cfg<BF, kPlain, false, true, 2, true, false>(a, tile, s);
-}
-
-// dWg = dG^T X and dWu = dU^T X: the rows of both operands are K.
-hipError_t launch_grad_weights(const DenseArgs& a, DenseTile tile, hipStream_t s) {
-  return launch_cfg<BF, kPlain, true, true, 1, true, false>(a, tile, s);
+hipError_t launch_grads(const DenseArgs& x, const DenseArgs& w, const GradPlan& p, hipStream_t s) {
+  if (!p.merged) {
+    const hipError_t e = launch_cfg<GradInput, true, false>(x, p.x.tile, s);
+    return e != hipSuccess ? e : launch_cfg<GradWeights, true, false>(w, p.w.tile, s);
+  }
+  switch (p.x.tile) {
+    case kTile64x128: return launch_both<GradInput::t64x128, GradWeights::t64x128>(x, w, s);
+    case kTile64Deep: return launch_both<GradInput::t64_deep, GradWeights::t64_deep>(x, w, s);
+    case kTile64: return launch_both<GradInput::t64, GradWeights::t64>(x, w, s);
+    default: return hipErrorInvalidConfiguration;
+  }
 }
 
 }  // namespace fp4g

@@ -31,6 +31,7 @@
 #include <algorithm>
 
 #include "dense.hpp"
+#include "launch.hpp"
 
 namespace fp4g {
 namespace {
@@ -59,11 +60,16 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
   __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
   const int lane = threadIdx.x & 63, r = lane & 15, s = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (16 * C::RG);
+  const int slice = a.S > 1 ? blockIdx.x % (uint32_t)a.S : 0, group = a.S > 1 ? blockIdx.x / (uint32_t)a.S : blockIdx.x;
+  const int n0 = group * (16 * C::RG);
   const int KB = a.K * T::BYTES, ld = (int)a.ldb;
   const int rounds = ((KB + C::SW - 1) / C::SW + C::NW - 1) / C::NW;
-  // Slice blockIdx.y of the K split: rounds first .. last - 1 of NW chunks.
-  const int first = (int)((int64_t)blockIdx.y * rounds / a.S), last = (int)((int64_t)(blockIdx.y + 1) * rounds / a.S);
+  // A slice of the K split: rounds first .. last - 1 of NW chunks (S <= 16, rounds < 2^14).
+  int first = 0, last = rounds;
+  if (a.S > 1) {
+    first = (uint32_t)(slice * rounds) / (uint32_t)a.S;
+    last = (uint32_t)((slice + 1) * rounds) / (uint32_t)a.S;
+  }
 
   // Block b: rows n0 + 16 * (b / GATES) .. of weight b % GATES.
   rsrc_t rw[C::NB];
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
       const int64_t pitch = partial_pitch(a.N);
 #pragma unroll
       for (int g = 0; g < C::GATES; ++g)
-        static_cast<acc_t*>(a.P)[((((int64_t)blockIdx.y * C::GATES + g) * a.M + m) * pitch + n) / 4] = sum[g];
+        static_cast<acc_t*>(a.P)[((((int64_t)slice * C::GATES + g) * a.M + m) * pitch + n) / 4] = sum[g];
       continue;
     }
     float y[C::GATES][4];
@@ -218,8 +224,7 @@ __global__ void __launch_bounds__(C::NW * 64) dense_gemv_kernel(const DenseArgs 
 
 template <class C>
 hipError_t launch_gemv(const DenseArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((dense_gemv_kernel<C>), dim3((unsigned)ceil_div(a.N, 16 * C::RG), a.S), dim3(C::NW * 64), 0, s, a);
-  return hipGetLastError();
+  return launch(dense_gemv_kernel<C>, ceil_div(a.N, 16 * C::RG) * a.S, C::NW * 64, s, a);
 }
 
 // Weights of 32 MB and more stream past the caches (the eight L2s hold that much together):

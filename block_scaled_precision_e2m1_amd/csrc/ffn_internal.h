@@ -35,7 +35,8 @@ __host__ __device__
 int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
 enum DenseTile { kTile256, kTile128, kTile128Deep, kTile64x128, kTile64Deep, kTile64, kGemv };
-struct DensePlan { DenseTile tile; int S; };
+struct DensePlan { DenseTile tile; int S; double us; };   // us: the modelled time
+struct GradPlan { DensePlan x, w; bool merged; };         // dX; dWg and dWu; in one launch
 
 // Tile and K split for L products of rows x cols sums (gated: cols counts both weights'
 // columns) over KT stages of 128 bytes of K; at most `cap` slices.
@@ -54,8 +55,9 @@ hipError_t launch_gemv_w8a8_gated(const DenseArgs& a, hipStream_t s);
 hipError_t launch_gemv_gated(const DenseArgs& a, hipStream_t s);
 // Adds the slices of a.P and finishes the product.
 hipError_t launch_partial_sums(const DenseArgs& a, bool int8, bool gated, hipStream_t s);
-hipError_t launch_grad_input(const DenseArgs& a, DenseTile tile, hipStream_t s);
-hipError_t launch_grad_weights(const DenseArgs& a, DenseTile tile, hipStream_t s);
+// The backward products of an M x N gated product of K inputs, at most cap_x and cap_w slices.
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int64_t cap_x, int64_t cap_w);
+hipError_t launch_grads(const DenseArgs& x, const DenseArgs& w, const GradPlan& p, hipStream_t s);
 
 // dG = dH U act'(G), dU = dH act(G) as bf16 rows of `pitch` elements, zero past N.
 hipError_t launch_gate_grad(int64_t M, int64_t N, int64_t pitch, const void* dH, const float* G, const float* U, int act,

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "dense.hpp"
+#include "launch.hpp"
 
 namespace fp4g {
 namespace {
@@ -24,7 +25,8 @@ gate_grad_kernel(int64_t M, int N, int pitch, const uint16_t* __restrict__ dH, c
   const int groups = pitch / 8;
   const int64_t total = M * groups;
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < total; x += (int64_t)gridDim.x * 256) {
-    const int64_t m = x / groups;
+    // 32-bit division where it will do: the 64-bit one is a hundred instructions.
+    const int64_t m = total <= UINT32_MAX ? (uint32_t)x / (uint32_t)groups : x / groups;
     const int n = (int)(x - m * groups) * 8;
     const int64_t at = m * N + n;
     float h[8], g[8], u[8];
@@ -68,9 +70,8 @@ hipError_t launch_gate_grad(int64_t M, int64_t N, int64_t pitch, const void* dH,
                             void* dG, void* dU, hipStream_t s) {
   const int64_t units = ceil_div(M * (pitch / 8), 256);
   const unsigned grid = (unsigned)std::min<int64_t>(units, device_cus() * 16);
-  hipLaunchKernelGGL(gate_grad_kernel, dim3(grid), dim3(256), 0, s, M, (int)N, (int)pitch, static_cast<const uint16_t*>(dH), G, U,
-                     act, static_cast<uint8_t*>(dG), static_cast<uint8_t*>(dU));
-  return hipGetLastError();
+  return launch(gate_grad_kernel, grid, 256, s, M, (int)N, (int)pitch, static_cast<const uint16_t*>(dH), G, U, act,
+                static_cast<uint8_t*>(dG), static_cast<uint8_t*>(dU));
 }
 
 }  // namespace fp4g

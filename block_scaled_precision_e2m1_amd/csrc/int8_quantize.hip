@@ -13,6 +13,7 @@
 
 #include "common.hpp"
 #include "ffn_internal.h"
+#include "launch.hpp"
 
 namespace fp4g {
 namespace {
@@ -147,27 +148,25 @@ int8_quantize_long_kernel(int K, const uint8_t* __restrict__ X, uint8_t* __restr
 }
 
 template <bool BF16, int W, int C>
-hipError_t launch(int64_t rows, int64_t K, const void* X, void* codes, float* scales, hipStream_t s) {
+hipError_t launch_rows(int64_t rows, int64_t K, const void* X, void* codes, float* scales, hipStream_t s) {
   constexpr int NW = W < 4 ? 4 : W;
-  hipLaunchKernelGGL((int8_quantize_kernel<BF16, W, C>), dim3((unsigned)ceil_div(rows, NW / W)), dim3(NW * 64), 0, s,
-                     rows, (int)K, static_cast<const uint8_t*>(X), static_cast<uint8_t*>(codes), scales);
-  return hipGetLastError();
+  return launch(int8_quantize_kernel<BF16, W, C>, ceil_div(rows, NW / W), NW * 64, s, rows, (int)K,
+                static_cast<const uint8_t*>(X), static_cast<uint8_t*>(codes), scales);
 }
 
 template <bool BF16>
 hipError_t launch_type(int64_t rows, int64_t K, const void* X, void* codes, float* scales, hipStream_t s) {
   const int64_t loads = ceil_div(K / Unit<BF16>::EPU, 64);   // 1 KB loads a row
-  if (loads <= 1) return launch<BF16, 1, 1>(rows, K, X, codes, scales, s);
-  if (loads <= 2) return launch<BF16, 1, 2>(rows, K, X, codes, scales, s);
-  if (loads <= 4) return launch<BF16, 1, 4>(rows, K, X, codes, scales, s);
-  if (loads <= 8) return launch<BF16, 4, 2>(rows, K, X, codes, scales, s);
-  if (loads <= 16) return launch<BF16, 4, 4>(rows, K, X, codes, scales, s);
-  if (loads <= 32) return launch<BF16, 4, 8>(rows, K, X, codes, scales, s);
-  if (loads <= 64) return launch<BF16, 16, 4>(rows, K, X, codes, scales, s);
-  if (loads <= 128) return launch<BF16, 16, 8>(rows, K, X, codes, scales, s);
-  hipLaunchKernelGGL((int8_quantize_long_kernel<BF16>), dim3((unsigned)rows), dim3(1024), 0, s, (int)K,
-                     static_cast<const uint8_t*>(X), static_cast<uint8_t*>(codes), scales);
-  return hipGetLastError();
+  if (loads <= 1) return launch_rows<BF16, 1, 1>(rows, K, X, codes, scales, s);
+  if (loads <= 2) return launch_rows<BF16, 1, 2>(rows, K, X, codes, scales, s);
+  if (loads <= 4) return launch_rows<BF16, 1, 4>(rows, K, X, codes, scales, s);
+  if (loads <= 8) return launch_rows<BF16, 4, 2>(rows, K, X, codes, scales, s);
+  if (loads <= 16) return launch_rows<BF16, 4, 4>(rows, K, X, codes, scales, s);
+  if (loads <= 32) return launch_rows<BF16, 4, 8>(rows, K, X, codes, scales, s);
+  if (loads <= 64) return launch_rows<BF16, 16, 4>(rows, K, X, codes, scales, s);
+  if (loads <= 128) return launch_rows<BF16, 16, 8>(rows, K, X, codes, scales, s);
+  return launch(int8_quantize_long_kernel<BF16>, rows, 1024, s, (int)K, static_cast<const uint8_t*>(X),
+                static_cast<uint8_t*>(codes), scales);
 }
 
 }  // namespace

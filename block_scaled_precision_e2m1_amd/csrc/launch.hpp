@@ -1,0 +1,27 @@
+// Kernel launches of the feed-forward operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <tuple>
+#include <utility>
+
+namespace fp4g {
+
+// Launches k(args...), converted to its parameter types.  The runtime's own entry point: the
+// triple-chevron macro keeps the launch shape in thread-local state on the way to it, which
+// takes 0.2 of a launch's 2.4 us of host time.
+template <class... P, class... A>
+inline hipError_t launch(void (*k)(P...), int64_t grid, int block, hipStream_t s, A&&... args) {
+  std::tuple<typename std::remove_const<P>::type...> held(std::forward<A>(args)...);
+  return std::apply(
+      [&](auto&... a) {
+        void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&a))...};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((unsigned)grid), dim3((unsigned)block), ptrs, 0, s);
+        if (e != hipSuccess) (void)hipGetLastError();
+        return e;
+      },
+      held);
+}
+
+}  // namespace fp4g
