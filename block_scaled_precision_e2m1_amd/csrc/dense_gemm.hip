@@ -629,7 +629,8 @@ DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t 
   const int64_t cus = device_cus();
   DensePlan best{kTile64, 1, 1e30};
   for (const Tile& c : kTiles)
-    for (int64_t S = 1; can_split(rows, cols, L, KT, S, cap); S *= 2) {
+    for (int64_t S : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (!can_split(rows, cols, L, KT, S, cap)) break;
       const int64_t items = items_of(c, rows, cols, L) * S, full = items / (cus * c.occ), rest = items % (cus * c.occ);
       const double stages = (double)ceil_div(KT, S);
       double t = split_us(rows, cols, L, S) + (double)full * (stages * c.us[c.occ - 1] + c.item);

@@ -227,19 +227,22 @@ hipError_t launch_gemv(const DenseArgs& a, hipStream_t s) {
   return launch(dense_gemv_kernel<C>, ceil_div(a.N, 16 * C::RG) * a.S, C::NW * 64, s, a);
 }
 
-// Weights of 32 MB and more stream past the caches (the eight L2s hold that much together):
-// nontemporal copies, two row groups a workgroup, which halves the tokens' reads, and two
-// waves.  Against one group: 14336 x 4096 int8, 16 and 32 tokens, 16.8 -> 14.4 and 23.7 ->
-// 18.4 us; bf16 gated, 16 and 32 tokens, 45.8 -> 46.3 and 57.9 -> 52.3 us.  Smaller
-// weights may stay in the caches and need the workgroups: one row group, and four waves
-// where the tokens leave LDS and registers for them (gated bf16 1024 x 1024, 1 token: 5.2
-// against 5.8 us with two; 64 tokens, int8 1000 x 1024: 6.9 against 5.4 us).
+// Weights of 32 MB and more stream past the caches (the eight L2s hold that much together).
+// With enough rows for two CUs in three they take nontemporal copies, two row groups a
+// workgroup, which halves the tokens' reads, and two waves.  Against one group: 14336 x 4096
+// int8, 16 and 32 tokens, 16.8 -> 14.4 and 23.7 -> 18.4 us; bf16 gated, 16 and 32 tokens,
+// 45.8 -> 46.3 and 57.9 -> 52.3 us; 6000 x 2000 bf16 gated, 30 tokens, 18.8 -> 16.3 us; but
+// with fewer rows (4096 x 8192 int8 gated, 16 tokens) 16.2 -> 20.1 us.  Smaller weights may
+// stay in the caches and need the workgroups too: one row group, and four waves where the
+// tokens leave LDS and registers for them (gated bf16 1024 x 1024, 1 token: 5.2 against 5.8
+// us with two; 64 tokens, int8 1000 x 1024: 6.9 against 5.4 us).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 bool streams(int64_t N, int64_t KB, int64_t gates) { return gates * N * KB >= kStreamBytes; }
+bool wide(int64_t N, int64_t KB, int64_t gates) { return streams(N, KB, gates) && ceil_div(N, 32) * 3 >= device_cus() * 2; }
 
 template <class T, int GATES, int TT, int P>
 hipError_t launch_tokens(const DenseArgs& a, hipStream_t s) {
-  if (streams(a.N, a.ldb, GATES)) {
+  if (wide(a.N, a.ldb, GATES)) {
     if constexpr (TT <= 2) return launch_gemv<GemvCfg<T, GATES, 2, 2, 256, 2, TT, P, true>>(a, s);
     return hipErrorInvalidConfiguration;   // gemv_takes refuses these
   }
@@ -270,7 +273,7 @@ bool gemv_takes(int64_t M, int64_t N, int64_t KB, int64_t gates) {
 // The K split: a workgroup reads its weights and all the tokens at about 50 KB a us, the chip
 // 4.8 MB a us; a split adds a launch and the partial sums.
 int gemv_splits(int64_t M, int64_t N, int64_t KB, int64_t gates, int64_t cap) {
-  const double rows = streams(N, KB, gates) ? 32.0 : 16.0, cus = (double)device_cus();
+  const double rows = wide(N, KB, gates) ? 32.0 : 16.0, cus = (double)device_cus();
   const double groups = (double)ceil_div(N, (int64_t)rows), own = (gates * rows + (double)M) * (double)KB;
   const int64_t rounds = ceil_div(KB, M <= 16 ? 1024 : 512);
   int best = 1;
