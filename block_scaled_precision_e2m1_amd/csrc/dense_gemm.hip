@@ -16,7 +16,8 @@
 //     (KG = 2), each multiplying half of every stage's quarters into sums of its own, which
 //     the end adds: twice the waves to hide latency behind, at the same LDS reads a product.
 //   * A K stage is 128 bytes of every row of A and of B (a cache line; 128 int8 or 64 bf16
-//     elements).  Stages live in a ring of STAGES slots, filled by buffer copies straight
+//     elements), or 256 for the two "long" tiles, which halves the barriers where few tiles
+//     walk a long K with a CU to themselves.  Stages live in a ring of STAGES slots, filled by buffer copies straight
 //     to LDS whose resources end with the operand's tile (dense.hpp): every ragged edge
 //     reads zeros.
 //   * Operand forms.  A "row" operand has K contiguous: 16-byte chunk c of row r sits at
@@ -25,8 +26,9 @@
 //     strided: the stage is 64 K rows of the tile's columns, and ds_read_b64_tr_b16 turns
 //     4 K rows x 16 columns into the fragment's order.  Its 64-byte units are XORed with
 //     the K row's low bits, so that the four rows one read touches lie in different banks.
-//   * K slots.  In quarter q of a stage, slot h (lane / 32) holds chunk 4h + q of a row, which
-//     is K elements 32h + 8q .. +7 for bf16: column operands read exactly those K rows.
+//   * K slots.  In quarter q of a stage ("quarters" are 32 bytes of K: 4 in a stage of 128
+//     bytes), slot h (lane / 32) holds chunk 4h + q of a row, which is K elements
+//     32h + 8q .. +7 for bf16: column operands read exactly those K rows.
 //   * The schedule is the one measured for the MXFP4 tiles (mxfp4_gemm.hip): the next
 //     quarter's fragments are read under this quarter's 16 matrix instructions, and the
 //     copies of a later stage are issued between them, in a pinned order; one barrier a
@@ -51,7 +53,8 @@
 namespace fp4g {
 namespace {
 
-__device__ __forceinline__ int swz(int r) { return ((r >> 1) & 7) ^ ((r & 1) << 2); }
+template <int ROWB>
+__device__ __forceinline__ int swz(int r) { return ROWB == 128 ? ((r >> 1) & 7) ^ ((r & 1) << 2) : r & 15; }
 
 // Column operands: the 64-byte unit u of K row k sits at unit u ^ unit_swz(k) of its LDS row, so
 // the four rows k .. k+3 (k % 4 == 0) of one unit lie in different banks: rows of 256 and 512
@@ -61,26 +64,27 @@ __device__ __forceinline__ int unit_swz(int k) { return PITCH >= 256 ? k & 3 : (
 
 enum Form { kScaled, kGated, kPlain };
 
-// KG groups of waves share a tile: group g multiplies quarters 4g/KG .. of every stage.  OCC
-// workgroups share a CU.
-template <class T_, int FORM_, int BM_, int BN_, int WM_, int WN_, int KG_, int STAGES_, int OCC_, bool ACOL_, bool BCOL_,
-          int NSEG_>
+// KG groups of waves share a tile: group g multiplies quarters QN g .. of every stage, which
+// is ROWB bytes of K.  OCC workgroups share a CU.
+template <class T_, int FORM_, int BM_, int BN_, int WM_, int WN_, int KG_, int ROWB_, int STAGES_, int OCC_,
+          bool ACOL_, bool BCOL_, int NSEG_>
 struct TileCfg {
   typedef T_ T;
   static constexpr int FORM = FORM_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, KG = KG_, STAGES = STAGES_, OCC = OCC_;
   static constexpr int NSEG = NSEG_;
   static constexpr bool ACOL = ACOL_, BCOL = BCOL_, GATED = FORM_ == kGated;
   static constexpr int NWN = BN / WN, NWT = (BM / WM) * NWN, NW = NWT * KG;    // waves: of a group, of the workgroup
-  static constexpr int QN = 4 / KG;                           // quarters of a stage a wave multiplies
-  static constexpr int ROWB = 128, KE = ROWB / T::BYTES;      // bytes and elements of K per stage
+  static constexpr int QN = ROWB_ / 32 / KG;                  // quarters of a stage a wave multiplies
+  static constexpr int ROWB = ROWB_, KE = ROWB / T::BYTES;      // bytes and elements of K per stage
+  static constexpr int RPC = 1024 / ROWB, CPR = ROWB / 16;    // rows a copy, chunks a row
   static constexpr int A_BYTES = BM * ROWB, STAGE = (BM + BN) * ROWB, LDS = STAGE * STAGES;
-  static constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW, LOADS = IA + IB;   // 1 KB copies per wave per stage
+  static constexpr int IA = BM * ROWB / 1024 / NW, IB = BN * ROWB / 1024 / NW, LOADS = IA + IB;   // 1 KB copies per wave per stage
   static constexpr int FI = WM / 32, FJ = WN / 32;
   static constexpr int OUTN = GATED ? BN / 2 : BN, WOUT = GATED ? WN / 2 : WN;   // output columns: tile, wave
   static constexpr int STRIP = WN * 4 + 16;                   // LDS pitch of a row of a wave's sums
   static_assert(!(ACOL || BCOL) || T::BYTES == 2, "column operands are bf16");
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "copies per wave");
-  static_assert(!GATED || BN / NW <= WN / 2, "each wave copies rows of one weight");
+  static_assert(IA * NW * 1024 == A_BYTES && IB * NW * 1024 == BN * ROWB, "copies per wave");
+  static_assert(!GATED || (IB * RPC <= WN / 2 && WN / 2 % (IB * RPC) == 0), "each wave copies rows of one weight");
   static_assert(NW * 32 * STRIP <= LDS && LDS * OCC <= 160 * 1024, "LDS");
   static_assert(STAGES >= 2 && (STAGES - 1) * LOADS < 64, "vmcnt range");
   static_assert(KG == 1 || KG == 2, "two quarters a wave at least");
@@ -167,7 +171,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   uint32_t va[C::IA], vb[C::IB];
   // Gated: the rows this wave copies belong to one of the weights; within the tile, row r
   // of LDS is output column (r / WN) * WN/2 + r % (WN/2) of weight (r % WN) / (WN/2).
-  const int bwhich = C::GATED ? (wave * C::IB * 8) % C::WN / (C::WN / 2) : 0;
+  const int bwhich = C::GATED ? (wave * C::IB * C::RPC) % C::WN / (C::WN / 2) : 0;
   // This lane's offset from the stage's start in copy n of a column operand of PITCH bytes a row.
   auto col_offset = [&](auto pitch_c, int n, int ld) {
     constexpr int PITCH = decltype(pitch_c)::value;
@@ -194,7 +198,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
     }
 #pragma unroll
     for (int q = 0; q < C::IA; ++q) {
-      const int n = wave * C::IA + q, row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
+      const int n = wave * C::IA + q, row = n * C::RPC + lane / C::CPR, c = ((lane % C::CPR) ^ swz<C::ROWB>(row)) * 16;
       if constexpr (C::ACOL) va[q] = col_offset(std::integral_constant<int, C::BM * 2>{}, n, lda);
       else va[q] = c < left * T::BYTES ? (uint32_t)row * lda + c : kNoLoad;
     }
@@ -207,7 +211,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
     }
 #pragma unroll
     for (int q = 0; q < C::IB; ++q) {
-      const int n = wave * C::IB + q, row = 8 * n + (lane >> 3), c = ((lane & 7) ^ swz(row)) * 16;
+      const int n = wave * C::IB + q, row = n * C::RPC + lane / C::CPR, c = ((lane % C::CPR) ^ swz<C::ROWB>(row)) * 16;
       const int src = C::GATED ? row / C::WN * (C::WN / 2) + row % (C::WN / 2) : row;
       if constexpr (C::BCOL) vb[q] = col_offset(std::integral_constant<int, C::BN * 2>{}, n, ldb);
       else vb[q] = c < left * T::BYTES ? (uint32_t)src * ldb + c : kNoLoad;
@@ -240,10 +244,10 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   v4i fa[2][FI], fb[2][FJ];
   constexpr int NFA = C::ACOL ? FI : QN, NFB = C::BCOL ? FJ : QN;
   const int ti = lane & 15, tq = ti >> 2, tb = ((lane >> 4) & 1) * 32 + (ti & 3) * 8;
-  auto row_frag = [&](int row, int j) { return row * C::ROWB + (((4 * hi + kg * QN + j) ^ swz(r32)) << 4); };
+  auto row_frag = [&](int row, int j) { return row * C::ROWB + (((C::CPR / 2 * hi + kg * QN + j) ^ swz<C::ROWB>(r32)) << 4); };
   auto col_frag = [&](auto pitch_c, int blk) {
     constexpr int PITCH = decltype(pitch_c)::value;
-    return (32 * hi + 8 * kg * QN + tq) * PITCH + ((blk ^ unit_swz<PITCH>(tq)) << 6) + tb;
+    return (C::KE / 2 * hi + 8 * kg * QN + tq) * PITCH + ((blk ^ unit_swz<PITCH>(tq)) << 6) + tb;
   };
   int foa[NFA], fob[NFB], ca[NFA], cb[NFB];   // offsets within a slot, and with the slot's start
 #pragma unroll
@@ -304,13 +308,12 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   // at 8192 x 14336 x 4096 the backward products take 1508 and 1585 us with one of each after
   // every matrix instruction until they are out, 1458 and 1541 us spread.  Copies spread
   // over three quarters land too late (1550 and 1555 us), in one they crowd (1604, 1681).
-  constexpr int FR = FI + FJ, NQ = FI * FJ;
-  constexpr int LH = (C::LOADS + 1) / 2;   // copies in the last quarter
-  auto copies = [&](auto part_c, int q) {   // part 0: the last quarter, 1: quarter 0
-    constexpr int PART = decltype(part_c)::value;
+  constexpr int FR = FI + FJ, NQ = FI * FJ, SPAN = QN > 4 ? QN / 2 : 2;
+  constexpr int LH = (C::LOADS + SPAN - 1) / SPAN;   // copies in the last quarter
+  auto copies = [&](int part, int q) {   // part 0: the last quarter, 1 ..: quarters 0 ..
 #pragma unroll
     for (int c = 0; c < C::LOADS; ++c)
-      if (2 * c * NQ / C::LOADS == PART * NQ + q) issue_one(c);
+      if (SPAN * c * NQ / C::LOADS == part * NQ + q) issue_one(c);
   };
   auto reads = [&](int j, int q) {
 #pragma unroll
@@ -322,7 +325,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
     quarter(std::integral_constant<int, (J & 1)>{}, [&](int q) {
       reads(J + 1, q);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (J == 0) copies(std::integral_constant<int, 1>{}, q);
+      if constexpr (J + 1 < SPAN) copies(J + 1, q);
     });
   };
   auto prologue = [&]() {
@@ -382,7 +385,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
       rd = rd + C::STAGE == C::LDS ? 0 : rd + C::STAGE;
       read_slot();
       quarter(std::integral_constant<int, (QN - 1) & 1>{}, [&](int q) {
-        copies(std::integral_constant<int, 0>{}, q);
+        copies(0, q);
         __builtin_amdgcn_sched_barrier(0);
         reads(0, q);
       });
@@ -552,14 +555,16 @@ hipError_t launch_tiles(const DenseArgs& a, hipStream_t s) {
 // The tiles by name, for one form of product.
 template <class T, int FORM, bool ACOL, bool BCOL, int NSEG>
 struct Tiles {
-  template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC>
-  using Cfg = TileCfg<T, FORM, BM, BN, WM, WN, KG, STAGES, OCC, ACOL, BCOL, NSEG>;
+  template <int BM, int BN, int WM, int WN, int KG, int STAGES, int OCC, int ROWB = 128>
+  using Cfg = TileCfg<T, FORM, BM, BN, WM, WN, KG, ROWB, STAGES, OCC, ACOL, BCOL, NSEG>;
   typedef Cfg<256, 256, 128, 128, 1, 2, 1> t256;
   typedef Cfg<128, 128, 64, 64, 1, 2, 2> t128;
   typedef Cfg<128, 128, 64, 64, 2, 4, 1> t128_deep;
   typedef Cfg<64, 128, 32, 64, 1, 3, 2> t64x128;
   typedef Cfg<64, 64, 32, 32, 2, 5, 2> t64_deep;
   typedef Cfg<64, 64, 32, 64, 2, 3, 3> t64;
+  typedef Cfg<64, 128, 32, 64, 1, 3, 1, 256> t64x128_long;
+  typedef Cfg<64, 64, 32, 32, 2, 4, 1, 256> t64_long;
 };
 typedef Tiles<BF, kPlain, false, true, 2> GradInput;    // dX = [dG dU] [Wg; Wu]: A rows hold K, B rows are K
 typedef Tiles<BF, kPlain, true, true, 1> GradWeights;   // dWg = dG^T X, dWu = dU^T X: both operands' rows are K
@@ -573,6 +578,8 @@ hipError_t launch_cfg(const DenseArgs& a, DenseTile tile, hipStream_t s) {
     case kTile64x128: return launch_tiles<typename S::t64x128, BF16, SAVE>(a, s);
     case kTile64Deep: return launch_tiles<typename S::t64_deep, BF16, SAVE>(a, s);
     case kTile64: return launch_tiles<typename S::t64, BF16, SAVE>(a, s);
+    case kTile64x128Long: return launch_tiles<typename S::t64x128_long, BF16, SAVE>(a, s);
+    case kTile64Long: return launch_tiles<typename S::t64_long, BF16, SAVE>(a, s);
     case kGemv: break;
   }
   return hipErrorInvalidConfiguration;
@@ -593,18 +600,20 @@ hipError_t launch_both(const DenseArgs& x, const DenseArgs& w, hipStream_t s) {
 }
 
 struct Tile { DenseTile t; int64_t bm, bn, occ; double us[3], item; };
-const Tile kTiles[] = {{kTile256, 256, 256, 1, {1.69}, 4.6},
-                       {kTile128, 128, 128, 2, {0.81, 1.12}, 2.0},
-                       {kTile128Deep, 128, 128, 1, {0.53}, 3.6},
-                       {kTile64x128, 64, 128, 2, {0.40, 0.72}, 2.5},
-                       {kTile64Deep, 64, 64, 2, {0.24, 0.505}, 2.2},
-                       {kTile64, 64, 64, 3, {0.28, 0.56, 0.69}, 1.8}};
+const Tile kTiles[] = {{kTile256, 256, 256, 1, {1.84}, 5.1},
+                       {kTile128, 128, 128, 2, {0.86, 1.20}, 2.0},
+                       {kTile128Deep, 128, 128, 1, {0.56}, 3.7},
+                       {kTile64x128, 64, 128, 2, {0.36, 0.73}, 2.5},
+                       {kTile64Deep, 64, 64, 2, {0.24, 0.50}, 2.4},
+                       {kTile64, 64, 64, 3, {0.275, 0.51, 0.68}, 2.1},
+                       {kTile64x128Long, 64, 128, 1, {0.326}, 3.2},
+                       {kTile64Long, 64, 64, 1, {0.211}, 2.9}};
 
 int64_t items_of(const Tile& c, int64_t rows, int64_t cols, int64_t L) {
   return L * ceil_div(rows, c.bm) * ceil_div(cols, c.bn);
 }
 double split_us(int64_t rows, int64_t cols, int64_t L, int64_t S) {
-  return S > 1 ? 2.6 + (double)(L * rows * cols) * (double)(2 * S + 1) * 4.0 / 6.4e6 : 0.0;
+  return S > 1 ? 2.7 + (double)(L * rows * cols) * (double)(2 * S + 1) * 4.0 / 6.7e6 : 0.0;
 }
 // A slice holds at least 4 stages; the reduction's indexes are 32 bits.
 bool can_split(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t S, int64_t cap) {
@@ -614,17 +623,20 @@ bool can_split(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t S, int
 }  // namespace
 
 // Tile and K split of a product with `rows` x `cols` sums (gated: cols = 2 N), L of them,
-// each a sum of KT stages: the pair with the least modelled time.  A round of items, n to a
-// CU, takes us[n-1] for each stage and `item` for its start and end; a split adds a launch
-// and the partial sums' way through memory.  The figures are fitted to the measured times of
-// 33 sizes of all five products, M = 20 .. 8192 (every tile, S = 1, 2, 4, 8); on those the
-// pair it picks is the fastest measured or within 4% of it.  What the tiles are for, in us:
+// each a sum of KT stages of 128 bytes: the pair with the least modelled time.  A round of
+// items, n to a CU, takes us[n-1] for each stage and `item` for its start and end; a split
+// adds a launch and the partial sums' way through memory.  The figures are fitted to the
+// measured times of 33 sizes of all five products, M = 20 .. 8192 (every tile, S = 1, 2, 4,
+// 8); on those the pair it picks is the fastest measured or within 3% of it.  What the tiles
+// are for, in us:
 //   int8 8192^3: 256^2 477, 128^2 593, 64 x 128 731, 64^2 907
 //   int8 2048 x 4096 x 4096: 128^2 44.2, 256^2 58.8, 64 x 128 53.0
-//   int8 200 x 14336 x 4096: 128^2 of two groups 27.1, 128^2 38.0, 64 x 128 30.8
-//   int8 1003 x 1117 x 1040: 64 x 128 9.8, 128^2 13.7, 64^2 10.2
-//   int8 128 x 4096 x 4096: 64^2 of 5 stages 12.4, 64^2 of 3 stages 13.4, 64 x 128 16.7
-//   int8 100 x 1000 x 1024: 64^2 of 3 stages 6.3, of 5 stages 6.8, 64 x 128 7.9
+//   int8 200 x 14336 x 4096: 128^2 of two groups 26.8, 128^2 38.0, 64 x 128 30.6
+//   int8 1003 x 1117 x 1040: 64 x 128 9.1, 128^2 13.7, 64^2 9.8
+//   int8 256 x 8192 x 8192: 64 x 128 with 256-byte stages 32.9, with 128-byte stages 37.1
+//   int8 128 x 4096 x 4096: 64^2 with 256-byte stages 11.0, with 5 of 128 bytes 12.7, 64 x 128 16.7
+//   int8 100 x 1000 x 1024: 64^2 of 3 stages 6.2, of 5 stages 6.6, 64 x 128 7.3
+//   bf16 gated 128 x 4096 x 2048: 64^2 of 5 stages 15.5, of 3 stages 18.3
 DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap) {
   const int64_t cus = device_cus();
   DensePlan best{kTile64, 1, 1e30};

@@ -34,7 +34,9 @@ __host__ __device__
 #endif
 int64_t partial_pitch(int64_t N) { return (N + 3) / 4 * 4; }
 
-enum DenseTile { kTile256, kTile128, kTile128Deep, kTile64x128, kTile64Deep, kTile64, kGemv };
+enum DenseTile {
+  kTile256, kTile128, kTile128Deep, kTile64x128, kTile64Deep, kTile64, kTile64x128Long, kTile64Long, kGemv
+};
 struct DensePlan { DenseTile tile; int S; double us; };   // us: the modelled time
 struct GradPlan { DensePlan x, w; bool merged; };         // dX; dWg and dWu; in one launch
 
