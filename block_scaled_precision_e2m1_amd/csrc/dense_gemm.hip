@@ -78,7 +78,8 @@ struct TileCfg {
   static constexpr int ROWB = ROWB_, KE = ROWB / T::BYTES;      // bytes and elements of K per stage
   static constexpr int RPC = 1024 / ROWB, CPR = ROWB / 16;    // rows a copy, chunks a row
   static constexpr int A_BYTES = BM * ROWB, STAGE = (BM + BN) * ROWB, LDS = STAGE * STAGES;
-  static constexpr int IA = BM * ROWB / 1024 / NW, IB = BN * ROWB / 1024 / NW, LOADS = IA + IB;   // 1 KB copies per wave per stage
+  // 1 KB copies of a wave in a stage.
+  static constexpr int IA = BM * ROWB / 1024 / NW, IB = BN * ROWB / 1024 / NW, LOADS = IA + IB;
   static constexpr int FI = WM / 32, FJ = WN / 32;
   static constexpr int OUTN = GATED ? BN / 2 : BN, WOUT = GATED ? WN / 2 : WN;   // output columns: tile, wave
   static constexpr int STRIP = WN * 4 + 16;                   // LDS pitch of a row of a wave's sums
@@ -244,7 +245,9 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   v4i fa[2][FI], fb[2][FJ];
   constexpr int NFA = C::ACOL ? FI : QN, NFB = C::BCOL ? FJ : QN;
   const int ti = lane & 15, tq = ti >> 2, tb = ((lane >> 4) & 1) * 32 + (ti & 3) * 8;
-  auto row_frag = [&](int row, int j) { return row * C::ROWB + (((C::CPR / 2 * hi + kg * QN + j) ^ swz<C::ROWB>(r32)) << 4); };
+  auto row_frag = [&](int row, int j) {
+    return row * C::ROWB + (((C::CPR / 2 * hi + kg * QN + j) ^ swz<C::ROWB>(r32)) << 4);
+  };
   auto col_frag = [&](auto pitch_c, int blk) {
     constexpr int PITCH = decltype(pitch_c)::value;
     return (C::KE / 2 * hi + 8 * kg * QN + tq) * PITCH + ((blk ^ unit_swz<PITCH>(tq)) << 6) + tb;
@@ -277,11 +280,13 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   auto read_frag = [&](int j, int x) {
     const int r = x == 1 ? 0 : x > FJ ? x - FJ : x == 0 ? FI : FI + x - 1;
     if (r < FI) {
-      if constexpr (C::ACOL) fa[j & 1][r] = read_col(std::integral_constant<int, C::BM * 2>{}, ca[r] + j * (16 * C::BM));
+      if constexpr (C::ACOL)
+        fa[j & 1][r] = read_col(std::integral_constant<int, C::BM * 2>{}, ca[r] + j * (16 * C::BM));
       else fa[j & 1][r] = *reinterpret_cast<const v4i*>(smem + ca[j] + r * (32 * C::ROWB));
     } else {
       const int b = r - FI;
-      if constexpr (C::BCOL) fb[j & 1][b] = read_col(std::integral_constant<int, C::BN * 2>{}, cb[b] + j * (16 * C::BN));
+      if constexpr (C::BCOL)
+        fb[j & 1][b] = read_col(std::integral_constant<int, C::BN * 2>{}, cb[b] + j * (16 * C::BN));
       else fb[j & 1][b] = *reinterpret_cast<const v4i*>(smem + cb[j] + b * (32 * C::ROWB));
     }
   };
@@ -417,7 +422,8 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
       // both groups' sums.  A batch of rows is read before the first is used: one wave a SIMD
       // would wait for LDS at every row (int8 8192^3 475.9 -> 469.2 us, dX at 8192 x 14336 x
       // 4096 1461 -> 1447 us).
-      constexpr int RPI = 64 / LPR, ITERS = RPI < ROWS ? ROWS / RPI : 1, BATCH = ITERS < (C::GATED ? 2 : 4) ? ITERS : C::GATED ? 2 : 4;
+      constexpr int RPI = 64 / LPR, ITERS = RPI < ROWS ? ROWS / RPI : 1;
+      constexpr int MOST = C::GATED ? 2 : 4, BATCH = ITERS < MOST ? ITERS : MOST;
       static_assert(ITERS % BATCH == 0, "whole batches");
       typedef sum_t sumv __attribute__((ext_vector_type(4)));
       constexpr int W = C::GATED ? 2 : 1;
@@ -430,7 +436,8 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
           const int row = ROWS * kg + min((b + k) * RPI + lane / LPR, ROWS - 1);
 #pragma unroll
           for (int x = 0; x < W * V; x += 4) {
-            const sumv* p = reinterpret_cast<const sumv*>(strips + row * C::STRIP + (x / V * C::WOUT + col + x % V) * 4);
+            const uint8_t* at = strips + row * C::STRIP + (x / V * C::WOUT + col + x % V) * 4;
+            const sumv* p = reinterpret_cast<const sumv*>(at);
             sumv v = *p;
             if constexpr (C::KG > 1) v += p[GROUP / 16];
 #pragma unroll
@@ -692,20 +699,21 @@ GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int64_t cap_x, int64_t cap_w
 
 hipError_t launch_partial_sums(const DenseArgs& a, bool int8, bool gated, hipStream_t s) {
   if (!int8) return a.G ? launch_reduce<BF, true, true, true>(a, s) : launch_reduce<BF, true, true, false>(a, s);
-  if (gated) return a.bf16_out ? launch_reduce<I8, true, true, false>(a, s) : launch_reduce<I8, true, false, false>(a, s);
+  if (gated)
+    return a.bf16_out ? launch_reduce<I8, true, true, false>(a, s) : launch_reduce<I8, true, false, false>(a, s);
   return a.bf16_out ? launch_reduce<I8, false, true, false>(a, s) : launch_reduce<I8, false, false, false>(a, s);
 }
 
 hipError_t launch_w8a8(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   if (tile == kGemv) return launch_gemv_w8a8(a, s);
   return a.bf16_out ? launch_cfg<Tiles<I8, kScaled, false, false, 1>, true, false>(a, tile, s)
-              : launch_cfg<Tiles<I8, kScaled, false, false, 1>, false, false>(a, tile, s);
+                    : launch_cfg<Tiles<I8, kScaled, false, false, 1>, false, false>(a, tile, s);
 }
 
 hipError_t launch_w8a8_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {
   if (tile == kGemv) return launch_gemv_w8a8_gated(a, s);
   return a.bf16_out ? launch_cfg<Tiles<I8, kGated, false, false, 1>, true, false>(a, tile, s)
-              : launch_cfg<Tiles<I8, kGated, false, false, 1>, false, false>(a, tile, s);
+                    : launch_cfg<Tiles<I8, kGated, false, false, 1>, false, false>(a, tile, s);
 }
 
 hipError_t launch_gated(const DenseArgs& a, DenseTile tile, hipStream_t s) {

@@ -11,16 +11,17 @@
 //   * Few tokens are packed: a load of 16 rows x 64 bytes takes P steps of 16 / P tokens, and
 //     the P steps multiply it into sums of their own, of which only the columns of their
 //     own step mean anything; the end picks those.  So 1 to 4 tokens cost a quarter of the
-//     loads (N = 1000, K = 1024: no change; 14336 x 4096 int8, 8 tokens: 16.3 -> 15.1 us).
+//     loads, 5 to 8 half (14336 x 4096 int8, 8 tokens: 16.7 -> 15.1 us).
 //   * The 16-byte unit u of row r sits at unit u ^ r of its LDS row: rows are a multiple of
 //     256 bytes apart, so 16 rows of one unit would share four banks.
 //   * Ragged sizes: rows past N, K past a row's end and chunks past the last are zeros from
 //     the buffer resources (dense.hpp); tokens past M repeat the last one and are not stored.
 //   * The waves' partial tiles meet in LDS and are added in wave order (results repeat bit
 //     for bit); a lane then owns 4 consecutive columns of one token.
-//   * HBM-bound for large weights, bound by what one CU can pull (about 50 GB/s x 1000, the
-//     tokens' reads included) where N gives few workgroups: then K is cut into slices too,
-//     added by the reduction of dense_gemm.hip.
+//   * HBM-bound for large weights (14336 x 4096 int8, 8 tokens: 12.3 us, 4.8 TB/s; gated bf16,
+//     16 tokens: 46-49 us, 4.9 TB/s).  Where N gives few workgroups, bound by what one CU can
+//     pull, about 50 KB a us with the tokens' reads: then K is cut into slices too, added by
+//     the reduction of dense_gemm.hip.
 //
 // What was measured for the shape (cold weights, us).  The ring's bytes per workgroup matter
 // most: short rings let more workgroups share a CU, and their starts and ends overlap.
@@ -238,7 +239,9 @@ hipError_t launch_gemv(const DenseArgs& a, hipStream_t s) {
 // us with two; 64 tokens, int8 1000 x 1024: 6.9 against 5.4 us).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 bool streams(int64_t N, int64_t KB, int64_t gates) { return gates * N * KB >= kStreamBytes; }
-bool wide(int64_t N, int64_t KB, int64_t gates) { return streams(N, KB, gates) && ceil_div(N, 32) * 3 >= device_cus() * 2; }
+bool wide(int64_t N, int64_t KB, int64_t gates) {
+  return streams(N, KB, gates) && ceil_div(N, 32) * 3 >= device_cus() * 2;
+}
 
 template <class T, int GATES, int TT, int P>
 hipError_t launch_tokens(const DenseArgs& a, hipStream_t s) {

@@ -17,7 +17,8 @@ inline hipError_t launch(void (*k)(P...), int64_t grid, int block, hipStream_t s
   return std::apply(
       [&](auto&... a) {
         void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&a))...};
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((unsigned)grid), dim3((unsigned)block), ptrs, 0, s);
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(k), dim3((unsigned)grid),
+                                             dim3((unsigned)block), ptrs, 0, s);
         if (e != hipSuccess) (void)hipGetLastError();
         return e;
       },

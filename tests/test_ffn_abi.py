@@ -160,3 +160,15 @@ def test_python_checks_come_before_the_library():
         fp4.int8_quantize(None)
     with pytest.raises(TypeError):
         fp4.gated_gemm(cpu.half(), cpu, cpu) if torch.cuda.is_available() else fp4.gated_gemm(3, cpu, cpu)
+
+
+def test_binding_takes_every_argument_by_position():
+    """The compiled functions behind ffn.py: their names, and counts that are refused."""
+    native = fp4.ffn._binding()
+    for name, count in (("int8_quantize", 3), ("w8a8_gemm", 7), ("w8a8_gated_gemm", 10), ("gated_gemm", 7),
+                        ("gated_gemm_backward", 8)):
+        f = getattr(native, name)
+        with pytest.raises(TypeError, match="expected"):
+            f(*[None] * (count - 1))
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            f(*[None] * count)

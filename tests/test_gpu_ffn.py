@@ -358,6 +358,41 @@ def test_gradients_against_differences(act):
         assert abs((got[i].double() * d).sum().item() - slope) <= (bounds[i][1] * d.abs()).sum().item() + 1e-6 * abs(slope) + 1e-4
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in codes, results, kept sums and gradients: first, middle and last rows."""
+    m, n, k = 65600, 32800, 16
+    rows, cols = [0, 32769, m - 1], [0, 16400, n - 1]
+    print(f"case offsets past 32 bits: quantize {m}x{n}", flush=True)
+    x = torch.randn(m, n, generator=gen(31), device=DEV, dtype=torch.bfloat16)
+    c, s = fp4.int8_quantize(x)
+    torch.cuda.synchronize(DEV)
+    rc, rs = quantize_reference(x[rows])
+    assert torch.equal(s[rows], rs) and torch.equal(c[rows], rc)
+    del x, c, s
+    print(f"case offsets past 32 bits: w8a8_gemm {m}x{n}x{k}", flush=True)
+    a, sa, b, sb = int8_inputs(m, n, k, 32, 1)
+    d = fp4.w8a8_gemm(a, sa, b, sb)
+    torch.cuda.synchronize(DEV)
+    want = (a[rows].double() @ b.double().t()) * sa[rows].double()[:, None] * sb.double()
+    within(d[rows], want, want.abs() * (3 * H32 + HBF) * 1.01 + 1e-40, "w8a8_gemm")
+    del d
+    print(f"case offsets past 32 bits: gated_gemm and its gradients {m}x{n}x{k}", flush=True)
+    x, wg, wu, dh = bf16_inputs(m, n, k, 33)
+    h, g, u = fp4.gated_gemm(x, wg, wu, save=True)
+    torch.cuda.synchronize(DEV)
+    (wantg, eg), (wantu, eu) = sums(x[rows], wg), sums(x[rows], wu)
+    within(g[rows], wantg, eg + 1e-30, "G")
+    within(u[rows], wantu, eu + 1e-30, "U")
+    within(h[rows], activation(wantg, "silu")[0] * wantu, gated_bound(wantg, eg, wantu, eu, "silu", HBF) + 1e-30, "H")
+    dx, dwg, dwu = fp4.gated_gemm_backward(dh, x, wg, wu, g, u)
+    torch.cuda.synchronize(DEV)
+    want = gradient_reference(dh[rows], x[rows], wg, wu, g[rows], u[rows], "silu")
+    within(dx[rows], *want[0], "dX")
+    want = gradient_reference(dh[:, cols], x, wg[cols], wu[cols], g[:, cols], u[:, cols], "silu")
+    within(dwg[cols], *want[1], "dWg")
+    within(dwu[cols], *want[2], "dWu")
+
+
 def test_empty_products():
     z = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
     h, g, u = fp4.gated_gemm(z(3, 0), z(5, 0), z(5, 0), save=True)
