@@ -139,9 +139,10 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kg = wave / C::NWT, wt = wave % C::NWT, wm = wt / C::NWN, wn = wt % C::NWN;
   const int hi = lane >> 5, r32 = lane & 31;
-  const int tiles_m = (a.M + C::BM - 1) / C::BM, tiles_n = (a.N + C::OUTN - 1) / C::OUTN;
+  // Sizes reach 2^31 - 1: what passes them by part of a tile is formed unsigned.
+  const int tiles_m = ((uint32_t)a.M + C::BM - 1) / C::BM, tiles_n = ((uint32_t)a.N + C::OUTN - 1) / C::OUTN;
   const int total = a.L * tiles_m * tiles_n * a.S;
-  const int KT1 = (a.K + C::KE - 1) / C::KE, KT = C::NSEG * KT1;
+  const int KT1 = ((uint32_t)a.K + C::KE - 1) / C::KE, KT = C::NSEG * KT1;
   const int lda = (int)a.lda, ldb = (int)a.ldb;
 
   // ---- the current item ----
@@ -351,20 +352,21 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
     setup(work);
     // A lane writes row r32 of every strip of the wave's sums and reads column group `col` of it:
     // it fetches the scales of both here, so that the end does not wait for them.
-    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
+    const uint32_t mw = m0 + wm * C::WM, nw = n0 + wn * C::WOUT;
     constexpr int ELEM = SPLIT || !BF16 || SAVE ? 4 : 2, V = 16 / ELEM, LPR = C::WOUT / V;
     static_assert(64 % LPR == 0 && C::STRIP % 16 == 0, "a lane keeps its columns");
     constexpr bool SCALED = !SPLIT && std::is_same<T, I8>::value;
     typedef typename std::conditional<std::is_same<T, I8>::value, int, float>::type sum_t;
-    const int col = lane % LPR * V, n = nw + col;
+    const int col = lane % LPR * V;
+    const uint32_t n = nw + col;
     float sm[FI], sc[C::GATED ? 2 : 1][V];
     if constexpr (SCALED) {
 #pragma unroll
-      for (int i = 0; i < FI; ++i) sm[i] = a.sa[min(mw + i * 32 + r32, a.M - 1)];
+      for (int i = 0; i < FI; ++i) sm[i] = a.sa[min(mw + i * 32 + r32, a.M - 1u)];
 #pragma unroll
       for (int w = 0; w < (C::GATED ? 2 : 1); ++w)
 #pragma unroll
-        for (int e = 0; e < V; ++e) sc[w][e] = a.sb[w][min(n + e, a.N - 1)];
+        for (int e = 0; e < V; ++e) sc[w][e] = a.sb[w][min(n + e, a.N - 1u)];
     }
     __builtin_amdgcn_sched_barrier(0);   // before the copies: the counted waits below skip none of those
     prologue();
@@ -448,7 +450,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
           const int r = (b + k) * RPI + lane / LPR;
-          const int64_t m = mw + i * 32 + ROWS * kg + r;
+          const int64_t m = (int64_t)mw + i * 32 + ROWS * kg + r;
           if (RPI > ROWS && r >= ROWS) continue;   // more lanes than rows
           if constexpr (SPLIT) {
             const int64_t pitch = partial_pitch(a.N);
@@ -460,7 +462,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
                     sumv{g[k][w * V], g[k][w * V + 1], g[k][w * V + 2], g[k][w * V + 3]};
               }
             }
-          } else if (m < a.M && n < a.N) {
+          } else if (m < a.M && n < (uint32_t)a.N) {
             // int8 sums are exact in 32 bits and are rounded to fp32 here.
             float y[V], u[V];
 #pragma unroll
@@ -469,7 +471,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
               if constexpr (SCALED) y[e] = y[e] * rs[k] * sc[0][e];
             }
             const int64_t at = m * a.N + n;
-            const int left = a.N - n;
+            const int left = a.N - (int)n;
             if constexpr (C::GATED) {
 #pragma unroll
               for (int e = 0; e < V; ++e) {
@@ -563,7 +565,7 @@ hipError_t launch_reduce(const DenseArgs& a, hipStream_t s) {
 template <class C, bool BF16, bool SAVE>
 hipError_t launch_tiles(const DenseArgs& a, hipStream_t s) {
   const int64_t items = a.L * ceil_div(a.M, C::BM) * ceil_div(a.N, C::OUTN) * a.S;
-  if (items > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (items > INT32_MAX / 2) return hipErrorInvalidConfiguration;
   const unsigned grid = (unsigned)std::min<int64_t>(items, device_cus() * C::OCC);
   if (a.S > 1) {
     const hipError_t e = launch(dense_gemm_kernel<C, false, false, true>, grid, C::NW * 64, s, a);
@@ -611,7 +613,7 @@ hipError_t launch_both(const DenseArgs& x, const DenseArgs& w, hipStream_t s) {
   const int64_t slots = device_cus() * CX::OCC;
   const int64_t nx = x.S * ceil_div(x.M, CX::BM) * ceil_div(x.N, CX::OUTN);
   const int64_t nw = w.L * ceil_div(w.M, CW::BM) * ceil_div(w.N, CW::OUTN);
-  if (nx > INT32_MAX || nw > INT32_MAX) return hipErrorInvalidConfiguration;
+  if (nx > INT32_MAX / 2 || nw > INT32_MAX / 2) return hipErrorInvalidConfiguration;
   // A multiple of 8 workgroups for x, so that the others' ids keep their XCDs.
   const int split = (int)(ceil_div(std::min(nx, slots), 8) * 8);
   const unsigned grid = (unsigned)(split + std::min(nw, slots));

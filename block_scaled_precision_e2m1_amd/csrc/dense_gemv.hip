@@ -269,8 +269,9 @@ hipError_t launch_form(const DenseArgs& a, hipStream_t s) {
 // Up to 32 tokens, and up to 64 of weights that do not stream: with 64 tokens and 14336 x 4096
 // int8 gated weights the tiles take 32.4 us and this 37.1, with 1000 x 1024 8.5 and 8.5, and
 // ungated 64 x 1000 x 1024 8.3 and 5.4.
+// (A launch holds fewer than 2^32 threads: N below 2^27 leaves room for any split.)
 bool gemv_takes(int64_t M, int64_t N, int64_t KB, int64_t gates) {
-  return M <= (streams(N, KB, gates) ? 32 : 64);
+  return N < (int64_t)1 << 27 && M <= (streams(N, KB, gates) ? 32 : 64);
 }
 
 // The K split: a workgroup reads its weights and all the tokens at about 50 KB a us, the chip

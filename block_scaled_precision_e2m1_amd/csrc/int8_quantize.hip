@@ -150,8 +150,16 @@ int8_quantize_long_kernel(int K, const uint8_t* __restrict__ X, uint8_t* __restr
 template <bool BF16, int W, int C>
 hipError_t launch_rows(int64_t rows, int64_t K, const void* X, void* codes, float* scales, hipStream_t s) {
   constexpr int NW = W < 4 ? 4 : W;
-  return launch(int8_quantize_kernel<BF16, W, C>, ceil_div(rows, NW / W), NW * 64, s, rows, (int)K,
-                static_cast<const uint8_t*>(X), static_cast<uint8_t*>(codes), scales);
+  // A launch holds fewer than 2^32 threads, so very many short rows take several.
+  const int64_t most = ((int64_t)1 << 31) / (NW * 64) * (NW / W);
+  for (int64_t first = 0; first < rows; first += most) {
+    const int64_t n = std::min(rows - first, most);
+    const hipError_t e = launch(int8_quantize_kernel<BF16, W, C>, ceil_div(n, NW / W), NW * 64, s, n, (int)K,
+                                static_cast<const uint8_t*>(X) + first * K * (BF16 ? 2 : 4),
+                                static_cast<uint8_t*>(codes) + first * K, scales + first);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool BF16>

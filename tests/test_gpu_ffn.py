@@ -393,6 +393,29 @@ def test_offsets_past_32_bits():
     within(dwu[cols], *want[2], "dWu")
 
 
+def test_more_rows_than_a_launch_holds():
+    """2^26 and more rows of 16 for the quantizer, 2^27 and more channels for one token."""
+    rows = (1 << 26) + 5
+    print(f"case int8_quantize {rows}x16", flush=True)
+    x = torch.randn(rows, 16, generator=gen(34), device=DEV, dtype=torch.bfloat16)
+    c, s = fp4.int8_quantize(x)
+    torch.cuda.synchronize(DEV)
+    at = [0, (1 << 25) - 1, 1 << 25, (1 << 26) - 1, 1 << 26, rows - 1]
+    rc, rs = quantize_reference(x[at])
+    assert torch.equal(s[at], rs) and torch.equal(c[at], rc)
+    del x, c, s
+    n = (1 << 27) + 3
+    print(f"case w8a8_gemm 1x{n}x16", flush=True)
+    a, sa = codes(gen(35), 1, 16), scales(gen(36), 1, 0.03)
+    b = torch.randint(-127, 128, (n, 16), generator=gen(37), device=DEV, dtype=torch.int8)
+    sb = torch.rand(n, generator=gen(38), device=DEV) + 0.5
+    d = fp4.w8a8_gemm(a, sa, b, sb, out_dtype=torch.float32)
+    torch.cuda.synchronize(DEV)
+    at = [0, 1, 1 << 26, (1 << 27) - 1, n - 1]
+    want = (a.double() @ b[at].double().t()) * sa.double()[:, None] * sb[at].double()
+    within(d[:, at], want, want.abs() * 3 * H32 * 1.01 + 1e-40, "w8a8_gemm")
+
+
 def test_empty_products():
     z = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
     h, g, u = fp4.gated_gemm(z(3, 0), z(5, 0), z(5, 0), save=True)
