@@ -3,6 +3,7 @@
 // returns its status without touching the device.
 #include "ffn_internal.h"
 
+#include <algorithm>
 #include <initializer_list>
 
 namespace {
@@ -73,16 +74,43 @@ size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, const Dense
 }
 int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
 
-// The plan of a scaled or gated product, given room for its partial sums.
+// The last plan of this thread, by the sizes and the GPU's compute units: a call follows its
+// workspace query, and choosing among tiles and splits takes some tenths of a microsecond.
+template <class Plan>
+struct LastPlan {
+  int64_t key[6] = {-1, -1, -1, -1, -1, -1};
+  Plan plan{};
+  template <class F>
+  const Plan& get(int64_t a, int64_t b, int64_t c, int64_t d, int64_t e, F&& choose) {
+    const int64_t now[6] = {a, b, c, d, e, fp4g::device_cus()};
+    if (!std::equal(now, now + 6, key)) {
+      plan = choose();
+      std::copy(now, now + 6, key);
+    }
+    return plan;
+  }
+};
+
+// The plan of a scaled or gated product, given room for its partial sums: the best of all
+// where they fit, else the best with fewer slices.
 DensePlan product_plan(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t room) {
+  static thread_local LastPlan<DensePlan> last;
+  auto choose = [&](int64_t cap) {
+    if (fp4g::gemv_takes(M, N, K * elem, gates))
+      return DensePlan{fp4g::kGemv, fp4g::gemv_splits(M, N, K * elem, gates, cap), 0.0};
+    return fp4g::dense_plan(M, gates * N, 1, stages(K, elem), cap);
+  };
+  const DensePlan& p = last.get(M, N, K, elem, gates, [&] { return choose(fp4g::kMaxSplits); });
   const int64_t cap = slices(M, N, gates, 1, room);
-  if (fp4g::gemv_takes(M, N, K * elem, gates))
-    return DensePlan{fp4g::kGemv, fp4g::gemv_splits(M, N, K * elem, gates, cap), 0.0};
-  return fp4g::dense_plan(M, gates * N, 1, stages(K, elem), cap);
+  return p.S <= cap ? p : choose(cap);
 }
 // dX (one product over both gradients' K) and dWg and dWu; their partial sums share the room.
 fp4g::GradPlan grad_plan(int64_t M, int64_t N, int64_t K, size_t room) {
-  return fp4g::grad_plan(M, N, K, slices(M, K, 1, 1, room), slices(N, K, 1, 2, room));
+  static thread_local LastPlan<fp4g::GradPlan> last;
+  const fp4g::GradPlan& p =
+      last.get(M, N, K, 0, 0, [&] { return fp4g::grad_plan(M, N, K, fp4g::kMaxSplits, fp4g::kMaxSplits); });
+  const int64_t cap_x = slices(M, K, 1, 1, room), cap_w = slices(N, K, 1, 2, room);
+  return p.x.S <= cap_x && p.w.S <= cap_w ? p : fp4g::grad_plan(M, N, K, cap_x, cap_w);
 }
 
 fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t gates, size_t* bytes) {

@@ -148,7 +148,8 @@ __device__ __forceinline__ void gate(int act, float (&y)[V], const float (&u)[V]
 // V results to D[at ..], of which the first `left` exist.  A whole group is one vector store
 // at any alignment: rows of an odd length start anywhere, and the hardware splits only the
 // stores that cross a line.
-template <bool BF16, int V>
+// NT (fp32): past the caches.
+template <bool BF16, bool NT = false, int V>
 __device__ __forceinline__ void store_cols(void* D, int64_t at, int left, const float (&y)[V]) {
   static_assert(V == 4 || (V == 8 && BF16), "16 bytes at most");
   typedef v4i v4i_any __attribute__((aligned(2)));
@@ -170,7 +171,9 @@ __device__ __forceinline__ void store_cols(void* D, int64_t at, int left, const 
   } else {
     float* p = static_cast<float*>(D) + at;
     if (left >= V) {
-      *reinterpret_cast<v4f_any*>(p) = v4f{y[0], y[1], y[2], y[3]};
+      const v4f v{y[0], y[1], y[2], y[3]};
+      if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<v4f_any*>(p));
+      else *reinterpret_cast<v4f_any*>(p) = v;
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e)
