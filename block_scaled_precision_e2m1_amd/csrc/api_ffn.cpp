@@ -20,7 +20,7 @@ constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 16;
 
 struct Buffer {
   const void* p;
-  int64_t bytes;
+  uint64_t bytes;   // unsigned: a workspace may be said to hold any size_t
   uintptr_t align;
 };
 
@@ -33,8 +33,9 @@ fp4g_status check_buffers(std::initializer_list<Buffer> ins, std::initializer_li
     for (const Buffer& b : *list)
       if (b.bytes > 0 && reinterpret_cast<uintptr_t>(b.p) % b.align != 0) return FP4G_EALIGN;
   auto clash = [](const Buffer& a, const Buffer& b) {
+    // By the distance of the starts: an end may pass 2^64.
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
   };
   for (const Buffer* o = outs.begin(); o != outs.end(); ++o) {
     for (const Buffer& i : ins)
@@ -126,7 +127,7 @@ fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t
 int64_t grad_pitch(int64_t N) { return (N + 63) / 64 * 64; }
 
 // Buffers of zero elements are not there.
-Buffer buf(const void* p, int64_t bytes, uintptr_t align = 16) { return Buffer{p, bytes, align}; }
+Buffer buf(const void* p, uint64_t bytes, uintptr_t align = 16) { return Buffer{p, bytes, align}; }
 
 hipError_t zero(void* p, int64_t count, bool bf16, hipStream_t s) {
   return count > 0 ? fp4g::launch_zero_fill(p, count, bf16, s) : hipSuccess;
@@ -165,7 +166,7 @@ fp4g_status w8a8_gemm(int64_t M, int64_t N, int64_t K, const void* A, const floa
   if (M == 0 || N == 0) return FP4G_OK;
   const bool bf16 = d_type == FP4G_OUT_BF16, some = K > 0;
   st = check_buffers({buf(A, M * K), buf(sa, some ? M * 4 : 0, 4), buf(B, N * K), buf(sb, some ? N * 4 : 0, 4)},
-                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, (int64_t)workspace_bytes)});
+                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, workspace_bytes)});
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (!some) return finish(zero(D, M * N, bf16, s));
@@ -191,7 +192,7 @@ fp4g_status w8a8_gated_gemm(int64_t M, int64_t N, int64_t K, const void* A, cons
   const bool bf16 = d_type == FP4G_OUT_BF16, some = K > 0;
   st = check_buffers({buf(A, M * K), buf(sa, some ? M * 4 : 0, 4), buf(Bg, N * K), buf(sg, some ? N * 4 : 0, 4),
                       buf(Bu, N * K), buf(su, some ? N * 4 : 0, 4)},
-                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, (int64_t)workspace_bytes)});
+                     {buf(D, M * N * (bf16 ? 2 : 4)), buf(workspace, workspace_bytes)});
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (!some) return finish(zero(D, M * N, bf16, s));
@@ -216,7 +217,7 @@ fp4g_status gated_gemm(int64_t M, int64_t N, int64_t K, const void* X, const voi
   if (M == 0 || N == 0) return FP4G_OK;
   const int64_t kept = G ? M * N * 4 : 0;
   st = check_buffers({buf(X, M * K * 2), buf(Wg, N * K * 2), buf(Wu, N * K * 2)},
-                     {buf(H, M * N * 2), buf(G, kept), buf(U, kept), buf(workspace, (int64_t)workspace_bytes)});
+                     {buf(H, M * N * 2), buf(G, kept), buf(U, kept), buf(workspace, workspace_bytes)});
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (K == 0) {
@@ -262,7 +263,7 @@ fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH,
   st = check_buffers({buf(dH, M * N * 2), buf(X, some ? M * K * 2 : 0), buf(Wg, some ? N * K * 2 : 0),
                       buf(Wu, some ? N * K * 2 : 0), buf(G, M * N * 4), buf(U, M * N * 4)},
                      {buf(dX, M * K * 2), buf(dWg, N * K * 2), buf(dWu, N * K * 2),
-                      buf(workspace, some ? (int64_t)workspace_bytes : 0)});
+                      buf(workspace, some ? workspace_bytes : 0)});
   if (st != FP4G_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (!some) {
