@@ -132,3 +132,27 @@ def test_gated_gemm_backward(case):
         torch.cuda.synchronize(DEV)
         for what, a, b in zip(("dX", "dWg", "dWu"), got, want):
             assert torch.equal(a, b), f"{what}, {room} bytes of workspace"
+
+
+def test_gradients_of_rows_past_32_bit_offsets():
+    """dG and dU of 65600 x 32800 hold more than 2^31 elements in rows of 32832, so rows from 65409 on start past
+    them.  All but a few of those rows of dH and three earlier ones are zero: the gradients are sums of just these."""
+    m, n, k = 65600, 32800, 16
+    print(f"case gated_gemm_backward {m}x{n}x{k}, few rows", flush=True)
+    g = gen(45)
+    rows = torch.tensor([0, 1, 32769] + list(range(m - 100, m)), device=DEV)
+    x, wg, wu = (integers(g, r, k).bfloat16() for r in (m, n, n))
+    dh = torch.zeros(m, n, dtype=torch.bfloat16, device=DEV)
+    dh[rows] = integers(g, len(rows), n, 2).bfloat16()
+    kept = torch.full((m, n), 64.0, device=DEV)
+    u = torch.randint(-3, 4, (m, n), generator=g, device=DEV, dtype=torch.int8).float()
+    dx, dwg, dwu = fp4.gated_gemm_backward(dh, x, wg, wu, kept, u)
+    torch.cuda.synchronize(DEV)
+    wx, wdg, wdu = exact_gradients(dh[rows], x[rows], wg, wu, kept[rows], u[rows])
+    assert torch.equal(dx[rows], wx) and torch.equal(dwg, wdg) and torch.equal(dwu, wdu)
+    rest = torch.ones(m, dtype=torch.bool, device=DEV)
+    rest[rows] = False
+    assert not dx[rest].any()
+    # what a wrong offset would give: the last stage of 64 rows lost, or rows from the start in place of the last
+    assert not torch.equal(exact_gradients(dh[rows[:-64]], x[rows[:-64]], wg, wu, kept[rows[:-64]], u[rows[:-64]])[1], wdg)
+    assert not torch.equal(exact_gradients(dh[rows], x[:len(rows)], wg, wu, kept[rows], u[rows])[1], wdg)
