@@ -97,11 +97,22 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
 //   silu       x s(x)
 //   gelu       x (1 + erf(x / sqrt 2)) / 2
 //   gelu_tanh  x s(2 sqrt(2/pi) (x + 0.044715 x^3)), which is x (1 + tanh(..)) / 2
-// e^-z is one hardware 2^x of the fp32 product z log2(e) and the quotient one hardware
-// reciprocal: a few fp32 steps of relative error for |z| < 100, and past that s is 0 or 1
-// to more than fp32 precision.  The cubic is evaluated at |x| <= 32, where s has long been
-// 0 or 1: a larger x would overflow it and make 0 * inf of the derivative.
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// With e = e^-|z|, s(z) is 1 / (1 + e) for z >= 0 and e / (1 + e) below.  e is taken as the
+// square of e^(-|z|/2), whose two factors stay normal where e does not, and multiplies x in two
+// steps: x s(z) is a normal number down to z = -92, s itself only down to -87.
+// e^(-|z|/2) is one hardware 2^x of an fp32 product and the quotient one hardware reciprocal, so
+// the relative error of s and of x s is a few fp32 half steps (2^-24) for |z| < 2 and grows like
+// |z| from the rounding of the exponent: silu is off by 59 half steps at most in -60 .. -30 and
+// 111 at -92; gelu_tanh, whose z is rounded four times more, by 208 at x = -9 (z = -69).  That
+// is 2e-5 at worst, far below a bf16 half step of 4e-3.
+// The cubic is evaluated at |x| <= 32, where s has long been 0 or 1: a larger x would overflow
+// it and make 0 * inf of the derivative.
+struct Sigmoid { float h, r, q; };    // s(z) = h h r, 1 - s(z) = q
+__device__ __forceinline__ Sigmoid sigmoid(float z) {
+  const float f = __builtin_amdgcn_exp2f(__builtin_fabsf(z) * -0.72134752044448170f);   // log2(e) / 2
+  const float e = f * f, r = __builtin_amdgcn_rcpf(1.0f + e);
+  return Sigmoid{z < 0.0f ? f : 1.0f, r, z < 0.0f ? r : e * r};
+}
 __device__ __forceinline__ float cubic_arg(float x, float* slope) {
   constexpr float c = 1.5957691216057308f, q = 0.044715f;       // 2 sqrt(2/pi)
   const float t = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f), t2 = t * t;
@@ -112,7 +123,8 @@ __device__ __forceinline__ float act_of(int act, float x) {
   if (act == FP4G_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
   float z = x, slope;
   if (act == FP4G_ACT_GELU_TANH) z = cubic_arg(x, &slope);
-  return x * sigmoid(z);
+  const Sigmoid s = sigmoid(z);
+  return x * s.h * s.r * s.h;
 }
 // act(x) and its derivative.
 __device__ __forceinline__ void act_grad(int act, float x, float* a, float* da) {
@@ -125,9 +137,10 @@ __device__ __forceinline__ void act_grad(int act, float x, float* a, float* da) 
   }
   float z = x, slope = 1.0f;
   if (act == FP4G_ACT_GELU_TANH) z = cubic_arg(x, &slope);
-  const float s = sigmoid(z);
-  *a = x * s;
-  *da = s + x * s * (1.0f - s) * slope;
+  const Sigmoid s = sigmoid(z);
+  const float xh = x * s.h;
+  *a = xh * s.r * s.h;
+  *da = (s.h + xh * s.q * slope) * s.r * s.h;   // s + x s (1 - s) z'
 }
 
 // y = act(y) * u; the activation is uniform, so one of the three loops runs.
