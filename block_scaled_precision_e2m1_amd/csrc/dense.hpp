@@ -95,7 +95,7 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
 
 // The activations of a gated block, in fp32.  With s(z) = 1 / (1 + e^-z):
 //   silu       x s(x)
-//   gelu       x (1 + erf(x / sqrt 2)) / 2
+//   gelu       x erfc(-x / sqrt 2) / 2, which is x (1 + erf(x / sqrt 2)) / 2
 //   gelu_tanh  x s(2 sqrt(2/pi) (x + 0.044715 x^3)), which is x (1 + tanh(..)) / 2
 // With e = e^-|z|, s(z) is 1 / (1 + e) for z >= 0 and e / (1 + e) below.  e is taken as the
 // square of e^(-|z|/2), whose two factors stay normal where e does not, and multiplies x in two
@@ -105,6 +105,9 @@ __device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c) {
 // |z| from the rounding of the exponent: silu is off by 59 half steps at most in -60 .. -30 and
 // 111 at -92; gelu_tanh, whose z is rounded four times more, by 208 at x = -9 (z = -69).  That
 // is 2e-5 at worst, far below a bf16 half step of 4e-3.
+// gelu's left tail is erfc's, where 1 + erf would cancel (4% off at x = -5, zero from -5.5 on);
+// the rounding of erfc's argument makes its error grow like x^2: 18 half steps at most in -4 ..
+// -2, 48 in -6 .. -5, 211 at -13.  The derivative's e^(-x^2/2) is a square as well.
 // The cubic is evaluated at |x| <= 32, where s has long been 0 or 1: a larger x would overflow
 // it and make 0 * inf of the derivative.
 struct Sigmoid { float h, r, q; };    // s(z) = h h r, 1 - s(z) = q
@@ -119,8 +122,9 @@ __device__ __forceinline__ float cubic_arg(float x, float* slope) {
   *slope = c * (1.0f + 3.0f * q * t2);
   return c * t * (1.0f + q * t2);
 }
+__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
 __device__ __forceinline__ float act_of(int act, float x) {
-  if (act == FP4G_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+  if (act == FP4G_ACT_GELU) return x * normal_cdf(x);
   float z = x, slope;
   if (act == FP4G_ACT_GELU_TANH) z = cubic_arg(x, &slope);
   const Sigmoid s = sigmoid(z);
@@ -129,10 +133,11 @@ __device__ __forceinline__ float act_of(int act, float x) {
 // act(x) and its derivative.
 __device__ __forceinline__ void act_grad(int act, float x, float* a, float* da) {
   if (act == FP4G_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
+    const float cdf = normal_cdf(x);
     const float t = __builtin_amdgcn_fmed3f(x, -32.0f, 32.0f);
+    const float f = __builtin_amdgcn_exp2f(t * t * -0.36067376022224085f);   // e^(-t^2/4): log2(e) / 4
     *a = x * cdf;
-    *da = cdf + t * __expf(-0.5f * t * t) * 0.3989422804014327f;
+    *da = cdf + t * 0.3989422804014327f * f * f;
     return;
   }
   float z = x, slope = 1.0f;

@@ -81,3 +81,20 @@ def test_ends_of_the_type(act):
     # (act(most) is infinite in bf16 and would meet a zero weight in the sum)
     slope, _ = gradients(x[[0, 1, 3, 4, 5, 6, 7, 9]], act)
     assert slope[:7].tolist() == [0.5, 0.5, 0.0, 1.0, 0.0, 1.0, 0.0] and torch.isnan(slope[7])
+
+
+# gelu is a normal fp32 number down to x = -13.1
+@pytest.mark.parametrize("low,high", [(-13.1, -9.0), (-9.0, -5.0), (-5.0, -1.0), (-1.0, 30.0)])
+def test_erf_activation(low, high):
+    """erfc amplifies the rounding of its argument and of the constant 1/sqrt 2 (1.5 h(fp32) together) by at most
+    x^2 + 2, is itself off by 16 units at most (32 h(fp32)), and is subnormal below x = -12.9."""
+    print(f"case gelu {low} .. {high}", flush=True)
+    x = values(low, high)
+    a, da, _, _ = activation(x.double(), "gelu")
+    relative = H32 * (2 * x.double() ** 2 + 40)
+    for tokens in (1, 65):
+        within(served(x, "gelu", tokens), a, relative * a.abs() + 4 * TINY, f"gelu of {tokens} tokens")
+    got, kept = gradients(x, "gelu")
+    terms = da.abs() + 2 * (x.double() * torch.exp(-0.5 * x.double() ** 2)).abs() / math.sqrt(2 * math.pi)
+    within(got, da, (2 * HBF * da.abs() + (relative + 24 * H32) * terms) * 1.01 + 1e-38, "gelu'")
+    within(kept, a, (2 * HBF + relative) * 1.01 * a.abs() + 1e-38, "gelu in dU")
