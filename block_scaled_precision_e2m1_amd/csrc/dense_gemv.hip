@@ -269,7 +269,8 @@ hipError_t launch_form(const DenseArgs& a, hipStream_t s) {
 // Up to 32 tokens, and up to 64 of weights that do not stream: with 64 tokens and 14336 x 4096
 // int8 gated weights the tiles take 32.4 us and this 37.1, with 1000 x 1024 8.5 and 8.5, and
 // ungated 64 x 1000 x 1024 8.3 and 5.4.
-// (A launch holds fewer than 2^32 threads: N below 2^27 leaves room for any split.)
+// N below 2^27 is at most 2^23 groups of 256 threads, half of the 2^32 threads that a launch
+// holds fewer than; gemv_splits keeps their slices below it too.
 bool gemv_takes(int64_t M, int64_t N, int64_t KB, int64_t gates) {
   return N < (int64_t)1 << 27 && M <= (streams(N, KB, gates) ? 32 : 64);
 }
@@ -280,6 +281,7 @@ int gemv_splits(int64_t M, int64_t N, int64_t KB, int64_t gates, int64_t cap) {
   const double rows = wide(N, KB, gates) ? 32.0 : 16.0, cus = (double)device_cus();
   const double groups = (double)ceil_div(N, (int64_t)rows), own = (gates * rows + (double)M) * (double)KB;
   const int64_t rounds = ceil_div(KB, M <= 16 ? 1024 : 512);
+  cap = std::min(cap, (((int64_t)1 << 32) - 1) / ((int64_t)groups * 256));
   int best = 1;
   double best_t = 1e30;
   for (int64_t S = 1; S <= std::min<int64_t>({cap, rounds / 2, kMaxSplits}) || S == 1; S *= 2) {

@@ -1,7 +1,10 @@
 """Host-side behaviour of the feed-forward operators beyond the refusals of test_ffn_abi.py (no GPU needed: every
 call is refused before a launch)."""
+import ctypes
+
 import pytest
 
+from tests import ffn_plans as plans
 from tests.test_ffn_abi import EALIGN, EINVAL, P, backward, gated, gated8, gemm, lib  # noqa: F401
 
 
@@ -13,3 +16,17 @@ def test_workspace_sizes_past_63_bits(lib, call, size):  # noqa: F811
     assert call(lib, w=P[10] + 4, wb=size) == EALIGN
     assert call(lib, w=P[0], wb=size) == EINVAL          # reaches over the inputs
     assert call(lib, w=P[0] - 16, wb=size) == EINVAL
+
+
+def test_launches_of_few_token_products_hold_their_threads():
+    """Fewer than 2^32 threads a launch at the largest N, whatever K and M (256 threads a workgroup at most)."""
+    takes = plans.internal("_ZN4fp4g10gemv_takesEllll", ctypes.c_bool, 4)
+    splits = plans.internal("_ZN4fp4g11gemv_splitsElllll", ctypes.c_int, 5)
+    for n in ((1 << 27) - 1, 1 << 26, 1 << 21, 1 << 20, 5000):
+        for kb in (16, 1024, 65536, 1 << 22):
+            for m in (1, 16, 32, 64):
+                for gates in (1, 2):
+                    if takes(m, n, kb, gates):
+                        groups = -(-n // (32 if gates * n * kb >= 1 << 25 and n >= 32 * 171 else 16))
+                        assert groups * splits(m, n, kb, gates, 16) * 256 < 1 << 32, (m, n, kb, gates)
+    assert not takes(1, 1 << 27, 16, 1)
