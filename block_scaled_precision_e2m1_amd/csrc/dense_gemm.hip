@@ -154,7 +154,7 @@ __device__ __forceinline__ void dense_gemm(const DenseArgs& a, int block, int gr
     n0 = it.tn * C::OUTN;
     ks0 = 0;
     KS = KT;
-    if (SPLIT) {   // S slices, S <= 16 and KT < 2^20
+    if (SPLIT) {   // S slices; S <= 16 and KT <= 2^25 (the rows of a weight gradient), so 32 bits hold S * KT
       ks0 = (uint32_t)(it.s * KT) / (uint32_t)a.S;
       KS = (uint32_t)((it.s + 1) * KT) / (uint32_t)a.S - ks0;
     }
