@@ -12,7 +12,8 @@ Layouts (contiguous, all on one GPU):
   w8a8_gated_gemm      : A, sa as above; Bg, Bu [N, K] int8, sg, su [N] float32 -> D [M, N]
   gated_gemm           : X [M, K], Wg, Wu [N, K] bfloat16 -> H [M, N] bfloat16
   gated_gemm_backward  : the gradients of gated_gemm, bfloat16
-K is a multiple of 16 for int8 operands and of 8 for bf16; M and N are free.
+K is a multiple of 16 for int8 operands and of 8 for bf16; M and N are free, but for
+gated_gemm_backward's N of at most 2^21.
 """
 from __future__ import annotations
 

@@ -82,7 +82,9 @@ fp4g_status gated_gemm(int64_t M, int64_t N, int64_t K,
  *   dX[M][K] = dG Wg + dU Wu,  dWg[N][K] = dG^T X,  dWu[N][K] = dU^T X   with fp32 sums
  * The workspace is required: gated_gemm_backward_workspace_size gives `bytes`, which lets
  * the products split, and `least`, what dG and dU take (fewer is FP4G_EINVAL).  Where M
- * (for dWg, dWu) or N (for dX) is 0 those gradients are zeroed. */
+ * (for dWg, dWu) or N (for dX) is 0 those gradients are zeroed.  N is at most 2^21: rows of dG
+ * and dU are operands too (FP4G_EUNSUPPORTED otherwise, from the query as well; gated_gemm
+ * itself takes any N). */
 fp4g_status gated_gemm_backward_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes, size_t *least);
 fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K,
                                 const void *dH, const void *X, const void *Wg, const void *Wu,

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from tests import ffn_plans as plans
-from tests.test_ffn_abi import EALIGN, EINVAL, P, backward, gated, gated8, gemm, lib  # noqa: F401
+from tests.test_ffn_abi import EALIGN, EINVAL, EUNSUP, OK, P, backward, gated, gated8, gemm, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("call", [gemm, gated8, gated, backward])
@@ -30,3 +30,12 @@ def test_launches_of_few_token_products_hold_their_threads():
                         groups = -(-n // (32 if gates * n * kb >= 1 << 25 and n >= 32 * 171 else 16))
                         assert groups * splits(m, n, kb, gates, 16) * 256 < 1 << 32, (m, n, kb, gates)
     assert not takes(1, 1 << 27, 16, 1)
+
+
+def test_backward_takes_two_million_channels_and_no_more(lib):  # noqa: F811
+    n, least = ctypes.c_size_t(), ctypes.c_size_t()
+    query = lib.gated_gemm_backward_workspace_size
+    assert query(4, 1 << 21, 64, ctypes.byref(n), ctypes.byref(least)) == OK and least.value == 4 * 4 << 21
+    assert query(4, (1 << 21) + 1, 64, ctypes.byref(n), ctypes.byref(least)) == EUNSUP
+    assert backward(lib, N=(1 << 21) + 1, K=64) == EUNSUP
+    assert lib.gated_gemm_workspace_size(4, (1 << 21) + 1, 64, ctypes.byref(n)) == OK
