@@ -57,11 +57,11 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 // A contiguous matrix on a GPU, of one of two types.
 const at::Tensor& matrix(PyObject* o, const char* name, at::ScalarType a, at::ScalarType b) {
   const at::Tensor& t = tensor(o, name);
-  if (!t.is_cuda()) value_error("tensors must be on a GPU, got " + t.device().str());
   const at::ScalarType got = t.scalar_type();
   if (got != a && got != b)
     type_error(std::string(name) + " must have dtype " + dtype_name(a) + (a == b ? "" : " or " + dtype_name(b)) +
                ", got " + dtype_name(got));
+  if (!t.is_cuda()) value_error("tensors must be on a GPU, got " + t.device().str());
   if (t.dim() != 2) value_error(std::string(name) + " must be 2-D");
   if (!t.is_contiguous()) value_error(std::string(name) + " must be contiguous");
   return t;

@@ -3,7 +3,9 @@ call is refused before a launch)."""
 import ctypes
 
 import pytest
+import torch
 
+import block_scaled_precision_e2m1_amd as fp4
 from tests import ffn_plans as plans
 from tests.test_ffn_abi import EALIGN, EINVAL, EUNSUP, OK, P, backward, gated, gated8, gemm, lib  # noqa: F401
 
@@ -39,3 +41,15 @@ def test_backward_takes_two_million_channels_and_no_more(lib):  # noqa: F811
     assert query(4, (1 << 21) + 1, 64, ctypes.byref(n), ctypes.byref(least)) == EUNSUP
     assert backward(lib, N=(1 << 21) + 1, K=64) == EUNSUP
     assert lib.gated_gemm_workspace_size(4, (1 << 21) + 1, 64, ctypes.byref(n)) == OK
+
+
+def test_a_wrong_type_is_a_type_error_wherever_the_tensor_is():
+    """As for every other argument (the type, then the shape, then the device), and with or without a GPU."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: fp4.gated_gemm(x.half(), x, x), lambda: fp4.int8_quantize(x.half()),
+                 lambda: fp4.w8a8_gemm(x, x, x, x), lambda: fp4.w8a8_gated_gemm(x, x, x, x, x, x),
+                 lambda: fp4.gated_gemm_backward(x, x.float(), x, x, x, x)):
+        with pytest.raises(TypeError, match="dtype"):
+            call()
+    with pytest.raises(ValueError, match="on a GPU"):
+        fp4.gated_gemm(x, x, x)
