@@ -15,6 +15,7 @@
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 
 #include <cstring>
 #include <string>
@@ -300,7 +301,8 @@ PyObject* py_w8a8_gated_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
-// X, Wg, Wu, act, save, out, workspace
+// X, Wg, Wu, act, save, out, workspace.  None where autograd has to record the call: ffn.py makes
+// it again from its autograd function.
 PyObject* py_gated_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return entry(n, 7, [&] {
     const at::Tensor& X = matrix(v[0], "X", at::kBFloat16, at::kBFloat16);
@@ -314,6 +316,7 @@ PyObject* py_gated_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int act = activation(v[3]);
     const int save = PyObject_IsTrue(v[4]);
     if (save < 0) throw Raised{};
+    if (c10::GradMode::is_enabled() && (X.requires_grad() || Wg.requires_grad() || Wu.requires_grad())) Py_RETURN_NONE;
     const at::Tensor H = result(v[5], "out", at::kBFloat16, {M, N}, device);
     at::Tensor G, U;
     if (save) {

@@ -13,7 +13,8 @@ Layouts (contiguous, all on one GPU):
   gated_gemm           : X [M, K], Wg, Wu [N, K] bfloat16 -> H [M, N] bfloat16
   gated_gemm_backward  : the gradients of gated_gemm, bfloat16
 K is a multiple of 16 for int8 operands and of 8 for bf16; M and N are free, but for
-gated_gemm_backward's N of at most 2^21.
+gated_gemm_backward's N of at most 2^21.  gated_gemm takes part in autograd; the results of the
+other functions carry no graph.
 """
 from __future__ import annotations
 
@@ -118,16 +119,58 @@ def w8a8_gated_gemm(A, sa, Bg, sg, Bu, su, act="silu", out=None, out_dtype=torch
     return (_native or _binding()).w8a8_gated_gemm(A, sa, Bg, sg, Bu, su, act, out, out_dtype, workspace)
 
 
+class _Gradients(torch.autograd.Function):
+    """gated_gemm_backward within a backward pass.  Where that is recorded itself (create_graph), a second
+    derivative raises: without this it would vanish."""
+
+    @staticmethod
+    def forward(ctx, dH, X, Wg, Wu, G, U, act):
+        return _binding().gated_gemm_backward(dH, X, Wg, Wu, G, U, act, None)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("gated_gemm has no second derivatives")
+
+
+class _GatedGemm(torch.autograd.Function):
+    """gated_gemm with its gradient, from the G and U that it keeps."""
+
+    @staticmethod
+    def forward(ctx, X, Wg, Wu, act, out, workspace):
+        H, G, U = _binding().gated_gemm(X, Wg, Wu, act, True, out, workspace)
+        ctx.save_for_backward(X, Wg, Wu, G, U)
+        ctx.act = act
+        ctx.mark_non_differentiable(G, U)
+        ctx.set_materialize_grads(False)
+        if out is not None:
+            ctx.mark_dirty(out)
+        return H, G, U
+
+    @staticmethod
+    def backward(ctx, dH, dG, dU):
+        if dH is None:
+            return (None,) * 6
+        grads = _Gradients.apply(dH.contiguous(), *ctx.saved_tensors, ctx.act)
+        return *(d if wanted else None for d, wanted in zip(grads, ctx.needs_input_grad)), None, None, None
+
+
 def gated_gemm(X, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     """The gated half of a feed-forward block in bf16: H = act(X Wg^T) * (X Wu^T), fp32 sums,
     one rounding.  With save=True returns (H, G, U): G and U [M, N] float32 are the two
-    products, which gated_gemm_backward takes."""
-    return (_native or _binding()).gated_gemm(X, Wg, Wu, act, save, out, workspace)
+    products, which gated_gemm_backward takes.
+
+    Differentiable in X, Wg and Wu: where one of them requires a gradient, G and U are kept for
+    the backward pass, and H carries the graph (G and U do not)."""
+    r = (_native or _binding()).gated_gemm(X, Wg, Wu, act, save, out, workspace)
+    if r is None:
+        r = _GatedGemm.apply(X, Wg, Wu, act, out, workspace)
+        return r if save else r[0]
+    return r
 
 
 def gated_gemm_backward(dH, X, Wg, Wu, G, U, act="silu", workspace=None):
     """The gradients (dX [M, K], dWg [N, K], dWu [N, K], bfloat16) of gated_gemm for the
     incoming dH [M, N] bfloat16, with G and U as gated_gemm(..., save=True) returned them.
     `workspace` (uint8) needs the second of gated_gemm_backward_workspace_size's values; None
-    allocates the first."""
+    allocates the first.  Nothing is recorded: the results carry no graph."""
     return (_native or _binding()).gated_gemm_backward(dH, X, Wg, Wu, G, U, act, workspace)
