@@ -3,7 +3,7 @@
     python examples/feed_forward.py [--tokens M] [--width K] [--hidden N] [--act silu]
 
 ``Int8FeedForward`` quantizes its weights once and runs quantize -> gated product -> quantize ->
-product for every call.  ``gated_product`` is the gated half with its gradient for autograd.
+product for every call.  ``gated_product`` is the gated half, differentiable, over any leading dimensions.
 """
 from __future__ import annotations
 
@@ -35,27 +35,9 @@ class Int8FeedForward:
         return y.reshape(*x.shape[:-1], y.shape[-1])
 
 
-class _GatedProduct(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, wg, wu, act):
-        h, g, u = fp4.gated_gemm(x, wg, wu, act=act, save=True)
-        ctx.save_for_backward(x, wg, wu, g, u)
-        ctx.act = act
-        return h
-
-    @staticmethod
-    def backward(ctx, dh):
-        x, wg, wu, g, u = ctx.saved_tensors
-        return (*fp4.gated_gemm_backward(dh.contiguous(), x, wg, wu, g, u, act=ctx.act), None)
-
-
 def gated_product(x, wg, wu, act="silu"):
-    """act(x Wg^T) * (x Wu^T) for bf16 x [.., K], Wg and Wu [N, K], with gradients of all three."""
-    rows = x.reshape(-1, x.shape[-1])
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (x, wg, wu)):
-        h = _GatedProduct.apply(rows, wg, wu, act)
-    else:
-        h = fp4.gated_gemm(rows, wg, wu, act=act)     # keeps nothing for a backward pass
+    """act(x Wg^T) * (x Wu^T) for bf16 x [.., K], Wg and Wu [N, K], with gradients of those that require them."""
+    h = fp4.gated_gemm(x.reshape(-1, x.shape[-1]), wg, wu, act=act)
     return h.reshape(*x.shape[:-1], wg.shape[0])
 
 

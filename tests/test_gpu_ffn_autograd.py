@@ -1,4 +1,7 @@
 """gated_gemm under autograd: what a graph records is what gated_gemm_backward gives, and nothing is lost in silence."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -85,3 +88,19 @@ def test_refusals_are_those_of_the_plain_call():
         fp4.gated_gemm(t[0], t[1].float(), t[2])
     with pytest.raises(TypeError, match="must be a torch.Tensor"):
         fp4.gated_gemm(t[0], None, t[2])
+
+
+def test_the_example_hands_on_what_autograd_asks_for():
+    """Leading dimensions, a frozen weight, and second derivatives that raise rather than vanish."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_example_again", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    t, dh = leaves(6, 16, 24, (True, True, False))
+    h = example.gated_product(t[0].reshape(2, 3, 24), *t[1:])
+    h.backward(dh.reshape(2, 3, 16), retain_graph=True)
+    torch.cuda.synchronize(DEV)
+    assert t[0].grad.any() and t[1].grad.any() and t[2].grad is None
+    (dx,) = torch.autograd.grad(h.float().sum(), t[:1], create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        (dx.float().square().sum() + t[0].float().sum()).backward()
