@@ -260,8 +260,8 @@ fp4g_status gated_gemm_backward(int64_t M, int64_t N, int64_t K, const void* dH,
   if (pitch * 2 > kMaxPitch) return FP4G_EUNSUPPORTED;
   if (K == 0 || (M == 0 && N == 0)) return FP4G_OK;
   const bool some = M > 0 && N > 0;
-  st = check_buffers({buf(dH, M * N * 2), buf(X, some ? M * K * 2 : 0), buf(Wg, some ? N * K * 2 : 0),
-                      buf(Wu, some ? N * K * 2 : 0), buf(G, M * N * 4), buf(U, M * N * 4)},
+  st = check_buffers({buf(dH, M * N * 2, 2), buf(X, some ? M * K * 2 : 0), buf(Wg, some ? N * K * 2 : 0),
+                      buf(Wu, some ? N * K * 2 : 0), buf(G, M * N * 4, 4), buf(U, M * N * 4, 4)},
                      {buf(dX, M * K * 2), buf(dWg, N * K * 2), buf(dWu, N * K * 2),
                       buf(workspace, some ? workspace_bytes : 0)});
   if (st != FP4G_OK) return st;

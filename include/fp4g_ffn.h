@@ -11,8 +11,9 @@
  * Sizes (all entry points): each dimension >= 0 and below 2^31 and each buffer of at most
  * 2^50 elements (FP4G_EINVAL otherwise).  Operand rows are read 16 bytes at a time: int8
  * rows hold a multiple of 16 elements, bf16 rows a multiple of 8 (FP4G_EUNSUPPORTED
- * otherwise), at most 2^22 bytes.  Operands, activations and outputs are 16-byte aligned,
- * scales 4-byte (FP4G_EALIGN otherwise).  Outputs overlap neither an input nor each other.
+ * otherwise), at most 2^22 bytes.  Operands, the quantizer's input and outputs are 16-byte
+ * aligned; scales, and the backward pass's dH, G and U, are aligned to their elements
+ * (FP4G_EALIGN otherwise).  Outputs overlap neither an input nor each other.
  *
  * Workspaces: the products split K when their tiles cannot fill the GPU and `workspace`
  * (16-byte aligned, workspace_bytes long) has room for the partial sums.  The

@@ -53,3 +53,13 @@ def test_a_wrong_type_is_a_type_error_wherever_the_tensor_is():
             call()
     with pytest.raises(ValueError, match="on a GPU"):
         fp4.gated_gemm(x, x, x)
+
+
+def test_gradients_are_taken_at_any_element(lib):  # noqa: F811
+    """dH, G and U are read at their elements' alignment; a workspace that is too small is found after it."""
+    assert backward(lib, wb=16) == EINVAL
+    for name, at, element in (("dH", P[0], 2), ("G", P[4], 4), ("U", P[5], 4)):
+        assert backward(lib, **{name: at + element}, wb=16) == EINVAL
+        assert backward(lib, **{name: at + element // 2}, wb=16) == EALIGN
+    for name, at in (("X", P[1]), ("Wg", P[2]), ("Wu", P[3]), ("dX", P[6]), ("dWg", P[7]), ("dWu", P[8]), ("w", P[9])):
+        assert backward(lib, **{name: at + 4}, wb=16) == EALIGN

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_scaled_precision_e2m1_amd as fp4
-from tests.test_gpu_ffn import ACTS, DEV, bf16_inputs
+from tests.test_gpu_ffn import ACTS, DEV, bf16_inputs, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,24 @@ def test_the_example_hands_on_what_autograd_asks_for():
     (dx,) = torch.autograd.grad(h.float().sum(), t[:1], create_graph=True)
     with pytest.raises(RuntimeError, match="second derivatives"):
         (dx.float().square().sum() + t[0].float().sum()).backward()
+
+
+@pytest.mark.parametrize("m,n", [(5, 33), (130, 257), (40, 64)])
+def test_gradients_that_start_at_any_element(m, n):
+    """Row slices of tensors with odd rows start inside a 16-byte line."""
+    print(f"case gated_gemm_backward of slices {m}x{n}", flush=True)
+    t, _ = leaves(m, n, 72, (False,) * 3)
+    dh = torch.randn(m * n + 8, generator=gen(62), device=DEV).bfloat16()
+    kept = torch.randn(2, m * n + 8, generator=gen(63), device=DEV)
+    for first in (1, 3, 7):
+        d, g, u = dh[first:first + m * n].view(m, n), *(v[first:first + m * n].view(m, n) for v in kept)
+        got = fp4.gated_gemm_backward(d, *t, g, u)
+        want = fp4.gated_gemm_backward(d.clone(), *t, g.clone(), u.clone())
+        torch.cuda.synchronize(DEV)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    rows, _ = leaves(m - 1, n, 72)
+    h = fp4.gated_gemm(*rows)
+    h.backward(dh[:m * n].view(m, n)[1:])                # as a backward pass hands it over
+    torch.cuda.synchronize(DEV)
+    assert rows[0].grad.any()
