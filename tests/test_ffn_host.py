@@ -1,6 +1,7 @@
 """Host-side behaviour of the feed-forward operators beyond the refusals of test_ffn_abi.py (no GPU needed: every
 call is refused before a launch)."""
 import ctypes
+import shutil
 
 import pytest
 import torch
@@ -63,3 +64,19 @@ def test_gradients_are_taken_at_any_element(lib):  # noqa: F811
         assert backward(lib, **{name: at + element // 2}, wb=16) == EALIGN
     for name, at in (("X", P[1]), ("Wg", P[2]), ("Wu", P[3]), ("dX", P[6]), ("dWg", P[7]), ("dWu", P[8]), ("w", P[9])):
         assert backward(lib, **{name: at + 4}, wb=16) == EALIGN
+
+
+def test_the_library_is_built_where_the_binding_cannot_be(monkeypatch):
+    """No C++ compiler, or none of torch's headers: the library and the oracle are there, and the build says what is not."""
+    import __graft_entry__ as entry
+    import oracle
+    from block_scaled_precision_e2m1_amd import _build
+    done = []
+    monkeypatch.setattr(_build, "build", lambda *a, **k: done.append("library"))
+    monkeypatch.setattr(oracle, "build", lambda *a, **k: done.append("oracle"))
+    monkeypatch.setattr(fp4, "load_library", lambda: done.append("loaded"))
+    which = shutil.which
+    monkeypatch.setattr(_build.shutil, "which", lambda name: None if name in ("g++", "c++") else which(name))
+    with pytest.raises(RuntimeError, match="binding"):
+        entry.build()
+    assert done == ["library", "oracle", "loaded"]
