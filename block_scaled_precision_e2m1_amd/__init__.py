@@ -755,3 +755,9 @@ from .ffn import *  # noqa: E402,F401,F403
 from .ffn import __all__ as _ffn_all  # noqa: E402
 
 __all__ += _ffn_all
+
+# The operators around the products, of include/fp4g_lm.h, too.
+from .lm import *  # noqa: E402,F401,F403
+from .lm import __all__ as _lm_all  # noqa: E402
+
+__all__ += _lm_all

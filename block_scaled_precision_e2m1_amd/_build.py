@@ -70,13 +70,14 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
-BINDING_SRC = os.path.join(HERE, "binding", "ffn_binding.cpp")
-BINDING = os.path.join(HERE, "_ffn_binding.so")
+BINDINGS = {name: (os.path.join(HERE, "binding", f"{name}_binding.cpp"), os.path.join(HERE, f"_{name}_binding.so"))
+            for name in ("ffn", "lm")}
 
 
-def build_binding() -> str:
-    """The feed-forward operators' Python binding: host code against torch's headers, which
-    finds libfp4gemm.so next to itself.  Needs the library, so it is linked after it."""
+def build_binding() -> list[str]:
+    """The compiled Python bindings (of the feed-forward operators and of those around a
+    language model's products): host code against torch's headers, which finds libfp4gemm.so
+    next to itself.  Needs the library, so it is linked after it."""
     import sysconfig
 
     import torch
@@ -84,21 +85,25 @@ def build_binding() -> str:
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:
         raise RuntimeError("no C++ compiler: the Python binding cannot be built")
-    tmp = BINDING + ".tmp"
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-isystem", sysconfig.get_paths()["include"]]
-    for path in cpp_extension.include_paths():
-        cmd += ["-isystem", path]
-    cmd += [BINDING_SRC, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
-    for path in cpp_extension.library_paths():
-        cmd += ["-L" + path]
-    cmd += ["-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stdout}{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    def build_one(src, binding):
+        tmp = binding + ".tmp"
+        cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-isystem", sysconfig.get_paths()["include"]]
+        for path in cpp_extension.include_paths():
+            cmd += ["-isystem", path]
+        cmd += [src, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+        for path in cpp_extension.library_paths():
+            cmd += ["-L" + path]
+        cmd += ["-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cxx} failed for {src}:\n{r.stdout}{r.stderr}")
+        os.replace(tmp, binding)
+        return binding
+
+    with ThreadPoolExecutor(max_workers=len(BINDINGS)) as ex:
+        return list(ex.map(lambda b: build_one(*b), BINDINGS.values()))
 
 
 PROBE_SRC = os.path.join(HERE, "probe", "peak_probe.hip")
@@ -119,4 +124,4 @@ def build_probe(cc=None) -> str:
 
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
-    print(build_binding())
+    print(*build_binding(), sep="\n")

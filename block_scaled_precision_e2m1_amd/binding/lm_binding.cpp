@@ -1,0 +1,154 @@
+// The Python binding of the operators around a language model's products
+// (include/fp4g_lm.h) over torch tensors, in the manner of ffn_binding.cpp: every function takes
+// its arguments by position from the Python function of the same name in lm.py, checks them,
+// allocates what the caller did not give and calls the C ABI on the current stream of their
+// GPU.  Functions that autograd may have to record return None where it has to.
+#include "common.hpp"
+
+#include "../../include/fp4g_lm.h"
+
+namespace {
+
+int type_of(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 ? FP4G_IN_BF16 : FP4G_IN_F32; }
+
+bool recorded(std::initializer_list<const at::Tensor*> ts) {
+  if (!c10::GradMode::is_enabled()) return false;
+  for (const at::Tensor* t : ts)
+    if (t && t->defined() && t->requires_grad()) return true;
+  return false;
+}
+
+// A tensor of the caller's that is written: autograd learns of it where it is kept for a
+// backward pass, and it may not itself be waiting for a gradient.
+at::Tensor written(PyObject* given, const char* name, at::ScalarType dtype, at::IntArrayRef shape, at::Device device) {
+  const at::Tensor t = result(given, name, dtype, shape, device);
+  if (given != Py_None) {
+    if (recorded({&t})) value_error(std::string(name) + " requires a gradient");
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  }
+  return t;
+}
+
+double number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error(std::string(name) + " must be a number");
+  }
+  return v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
+// What every norm takes: X, weight, eps, and the residual with its sum.
+struct Norm {
+  at::Tensor X, W, R, H;
+  int64_t rows, K;
+  double eps;
+  int w_type;
+  const void* w() const { return W.defined() ? ptr(W) : nullptr; }
+  const void* r() const { return R.defined() ? ptr(R) : nullptr; }
+  void* h() const { return H.defined() ? ptr(H) : nullptr; }
+};
+Norm norm_of(PyObject* x, PyObject* weight, PyObject* eps, PyObject* residual) {
+  Norm n;
+  n.X = matrix(x, "X", at::kFloat, at::kBFloat16);
+  n.rows = n.X.size(0), n.K = n.X.size(1);
+  if (weight != Py_None) {
+    const at::ScalarType t = tensor(weight, "weight").scalar_type();
+    if (t != at::kFloat && t != at::kBFloat16)
+      type_error("weight must have dtype torch.float32 or torch.bfloat16, got " + dtype_name(t));
+    n.W = need(weight, "weight", t, {n.K}, n.X.device());
+  }
+  n.w_type = n.W.defined() ? type_of(n.W) : FP4G_IN_F32;
+  n.eps = number(eps, "eps");
+  if (residual != Py_None) n.R = need(residual, "residual", n.X.scalar_type(), {n.rows, n.K}, n.X.device());
+  return n;
+}
+
+// X, weight, eps, residual, out, sum_out
+PyObject* py_rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 6, [&] {
+    Norm a = norm_of(v[0], v[1], v[2], v[3]);
+    const at::Device device = a.X.device();
+    const c10::DeviceGuard guard(device);
+    if (v[3] == Py_None && v[5] != Py_None) value_error("sum_out without a residual");
+    if (recorded({&a.X, &a.W, &a.R})) {
+      if (v[4] != Py_None || v[5] != Py_None) value_error("out and sum_out are not taken where a gradient is recorded");
+      Py_RETURN_NONE;
+    }
+    const at::Tensor Y = written(v[4], "out", a.X.scalar_type(), {a.rows, a.K}, device);
+    if (a.R.defined()) a.H = written(v[5], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
+    launch("rms_norm", device, [&](void* stream) {
+      return rms_norm(a.rows, a.K, ptr(a.X), type_of(a.X), a.r(), a.w(), a.w_type, a.eps, a.h(), ptr(Y), stream);
+    });
+    return a.R.defined() ? tuple({Y, a.H}) : THPVariable_Wrap(Y);
+  });
+}
+
+// X, weight, eps, residual, codes, keep, sum_out
+PyObject* py_rms_norm_quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 7, [&] {
+    Norm a = norm_of(v[0], v[1], v[2], v[3]);
+    const at::Device device = a.X.device();
+    const c10::DeviceGuard guard(device);
+    const char* name = PyUnicode_Check(v[4]) ? PyUnicode_AsUTF8(v[4]) : nullptr;
+    PyErr_Clear();
+    const bool int8 = name && !std::strcmp(name, "int8");
+    if (!int8 && !(name && !std::strcmp(name, "e4m3")))
+      value_error(std::string("codes must be \"int8\" or \"e4m3\"") + (name ? std::string(", got ") + name : ""));
+    const bool keep = truth(v[5]);
+    if (v[3] == Py_None && v[6] != Py_None) value_error("sum_out without a residual");
+    if (recorded({&a.X, &a.W, &a.R})) value_error("rms_norm_quantize has no gradient: call it under torch.no_grad()");
+    const at::Tensor codes = empty({a.rows, a.K}, int8 ? at::kChar : at::kByte, device);
+    const at::Tensor scales = empty({a.rows}, at::kFloat, device);
+    at::Tensor Y;
+    if (a.R.defined()) a.H = written(v[6], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
+    if (keep) Y = empty({a.rows, a.K}, a.X.scalar_type(), device);
+    launch("rms_norm_quantize", device, [&](void* stream) {
+      return rms_norm_quantize(a.rows, a.K, ptr(a.X), type_of(a.X), a.r(), a.w(), a.w_type, a.eps, a.h(),
+                               keep ? ptr(Y) : nullptr, ptr(codes), int8 ? FP4G_CODE_INT8 : FP4G_CODE_E4M3,
+                               floats(scales), stream);
+    });
+    if (a.R.defined()) return keep ? tuple({codes, scales, a.H, Y}) : tuple({codes, scales, a.H});
+    return keep ? tuple({codes, scales, Y}) : tuple({codes, scales});
+  });
+}
+
+// dY, X, weight, eps, dH, want_dw, workspace
+PyObject* py_rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 7, [&] {
+    const Norm a = norm_of(v[1], v[2], v[3], Py_None);
+    const at::Device device = a.X.device();
+    const c10::DeviceGuard guard(device);
+    const at::ScalarType t = a.X.scalar_type();
+    const at::Tensor& dY = need(v[0], "dY", t, {a.rows, a.K}, device);
+    at::Tensor dH, dW;
+    if (v[4] != Py_None) dH = need(v[4], "dH", t, {a.rows, a.K}, device);
+    if (a.W.defined() && truth(v[5])) dW = empty({a.K}, a.W.scalar_type(), device);
+    const at::Tensor dX = empty({a.rows, a.K}, t, device);
+    const Space w = space(v[6], device, [&] {
+      size_t bytes = 0;
+      check_status("rms_norm_backward_workspace_size", rms_norm_backward_workspace_size(a.rows, a.K, type_of(a.X), &bytes));
+      return bytes;
+    });
+    launch("rms_norm_backward", device, [&](void* stream) {
+      return rms_norm_backward(a.rows, a.K, ptr(dY), ptr(a.X), type_of(a.X), a.w(), a.w_type, a.eps,
+                               dH.defined() ? ptr(dH) : nullptr, ptr(dX), dW.defined() ? ptr(dW) : nullptr, w.p,
+                               w.bytes, stream);
+    });
+    return tuple({dX, dW});   // None for an undefined tensor
+  });
+}
+
+PyMethodDef methods[] = {FASTCALL(rms_norm), FASTCALL(rms_norm_quantize), FASTCALL(rms_norm_backward),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__lm_binding() { return PyModule_Create(&module); }

@@ -4,10 +4,13 @@
 #include "ffn_internal.h"
 
 #include <algorithm>
-#include <initializer_list>
+
+#include "api_checks.hpp"
 
 namespace {
 
+using fp4g::buf;
+using fp4g::check_buffers;
 using fp4g::DenseArgs;
 using fp4g::DensePlan;
 
@@ -17,34 +20,6 @@ constexpr int64_t kMaxElems = (int64_t)1 << 50;
 constexpr int64_t kMaxPitch = (int64_t)1 << 22;
 // int8 sums: K * 128 * 128 must stay below 2^31.
 constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 16;
-
-struct Buffer {
-  const void* p;
-  uint64_t bytes;   // unsigned: a workspace may be said to hold any size_t
-  uintptr_t align;
-};
-
-// Every buffer present and aligned, every output clear of the inputs and the other outputs.
-fp4g_status check_buffers(std::initializer_list<Buffer> ins, std::initializer_list<Buffer> outs) {
-  for (const auto* list : {&ins, &outs})
-    for (const Buffer& b : *list)
-      if (b.bytes > 0 && !b.p) return FP4G_EINVAL;
-  for (const auto* list : {&ins, &outs})
-    for (const Buffer& b : *list)
-      if (b.bytes > 0 && reinterpret_cast<uintptr_t>(b.p) % b.align != 0) return FP4G_EALIGN;
-  auto clash = [](const Buffer& a, const Buffer& b) {
-    // By the distance of the starts: an end may pass 2^64.
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < a.bytes : x - y < b.bytes);
-  };
-  for (const Buffer* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Buffer& i : ins)
-      if (clash(*o, i)) return FP4G_EINVAL;
-    for (const Buffer* q = outs.begin(); q != o; ++q)
-      if (clash(*o, *q)) return FP4G_EINVAL;
-  }
-  return FP4G_OK;
-}
 
 // Sizes of a product whose operand rows hold K elements of `elem` bytes.
 fp4g_status check_sizes(int64_t M, int64_t N, int64_t K, int elem) {
@@ -125,9 +100,6 @@ fp4g_status product_workspace(int64_t M, int64_t N, int64_t K, int elem, int64_t
 
 // Rows of dG and dU: whole 128-byte K stages of dX.
 int64_t grad_pitch(int64_t N) { return (N + 63) / 64 * 64; }
-
-// Buffers of zero elements are not there.
-Buffer buf(const void* p, uint64_t bytes, uintptr_t align = 16) { return Buffer{p, bytes, align}; }
 
 hipError_t zero(void* p, int64_t count, bool bf16, hipStream_t s) {
   return count > 0 ? fp4g::launch_zero_fill(p, count, bf16, s) : hipSuccess;

@@ -1,0 +1,136 @@
+"""Operators around a language model's products: the norm before them, in their types or in 8 bits, with its gradient.
+
+A binding over the C ABI of ``include/fp4g_lm.h`` in the manner of the package's other
+functions: each has the name of its C entry point, checks its torch arguments, runs on the
+current stream of their GPU and raises ``Fp4GemmError`` on a non-zero status.  The checks and
+the calls are compiled (``binding/lm_binding.cpp``).
+
+Layouts (contiguous, all on one GPU):
+  rms_norm           : X [rows, K] float32 or bfloat16, weight [K] float32 or bfloat16 -> Y like X
+  rms_norm_quantize  : the same -> codes [rows, K] int8 or uint8 (E4M3), scales [rows] float32
+  rms_norm_backward  : the gradients of rms_norm
+rms_norm takes part in autograd; the results of the other functions carry no graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import importlib
+
+import torch
+
+import block_scaled_precision_e2m1_amd as _base
+
+__all__ = ["rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward", "LM_SYMBOLS"]
+
+LM_SYMBOLS = ("rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward")
+
+
+@functools.lru_cache(maxsize=None)
+def _library():
+    lib = _base.load_library()
+    i64, p, c_int, size, f64 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
+    psize = ctypes.POINTER(size)
+    args = {
+        "rms_norm": [i64, i64, p, c_int, p, p, c_int, f64, p, p, p],
+        "rms_norm_quantize": [i64, i64, p, c_int, p, p, c_int, f64, p, p, p, c_int, p, p],
+        "rms_norm_backward_workspace_size": [i64, i64, c_int, psize],
+        "rms_norm_backward": [i64, i64, p, p, c_int, p, c_int, f64, p, p, p, p, size, p],
+    }
+    for name, a in args.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = a, c_int
+    return lib
+
+
+_native = None
+
+
+def _binding():
+    """The compiled binding (binding/lm_binding.cpp); raises if the package is not built."""
+    global _native
+    if _native is None:
+        _library()
+        try:
+            _native = importlib.import_module("block_scaled_precision_e2m1_amd._lm_binding")
+        except ImportError as e:
+            raise ImportError("_lm_binding.so is not built or does not fit this torch; run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    return _native
+
+
+def _query(name, *sizes, results=1):
+    n = [ctypes.c_size_t(0) for _ in range(results)]
+    _base._raise_on(name, getattr(_library(), name)(*sizes, *map(ctypes.byref, n)))
+    return tuple(int(v.value) for v in n) if results > 1 else int(n[0].value)
+
+
+def _no_second(what):
+    raise RuntimeError(f"{what} has no second derivatives")
+
+
+class _NormGradients(torch.autograd.Function):
+    """rms_norm_backward within a backward pass.  Where that is recorded itself (create_graph), a second derivative
+    raises: without this it would vanish."""
+
+    @staticmethod
+    def forward(ctx, dY, X, weight, eps, dH, want_dw):
+        return _binding().rms_norm_backward(dY, X, weight, eps, dH, want_dw, None)
+
+    @staticmethod
+    def backward(ctx, *_):
+        _no_second("rms_norm")
+
+
+class _RmsNorm(torch.autograd.Function):
+    """rms_norm with its gradient, from the rows that were normed."""
+
+    @staticmethod
+    def forward(ctx, X, weight, eps, residual):
+        r = _binding().rms_norm(X, weight, eps, residual, None, None)
+        ctx.save_for_backward(X if residual is None else r[1], weight)
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        return r
+
+    @staticmethod
+    def backward(ctx, dY, dH=None):
+        if dY is None:                       # the sum alone was used
+            return dH, None, None, dH if ctx.needs_input_grad[3] else None
+        rows, weight = ctx.saved_tensors
+        dX, dW = _NormGradients.apply(dY.contiguous(), rows, weight, ctx.eps,
+                                      None if dH is None else dH.contiguous(), ctx.needs_input_grad[1])
+        return (dX if ctx.needs_input_grad[0] else None, dW, None, dX if ctx.needs_input_grad[3] else None)
+
+
+def rms_norm(X, weight=None, eps=1e-6, residual=None, out=None, sum_out=None):
+    """The root-mean-square norm of each row: Y = X / sqrt(mean(X^2) + eps) * weight.  With a residual (like X), of
+    H = X + residual, rounded to its type, and (Y, H) is returned.  `out` may be X or the residual, `sum_out` (for H)
+    too.
+
+    Differentiable in X, weight and residual (then without `out` and `sum_out`)."""
+    r = (_native or _binding()).rms_norm(X, weight, eps, residual, out, sum_out)
+    return _RmsNorm.apply(X, weight, eps, residual) if r is None else r
+
+
+def rms_norm_quantize(X, weight=None, eps=1e-6, residual=None, codes="int8", keep=False, sum_out=None):
+    """The same norm as codes with one scale for each row, as w8a8_gemm (codes="int8", int8) and w4a8_gemm
+    (codes="e4m3", uint8) take them: (codes [rows, K], scales [rows] float32), then H where there is a residual, then
+    with keep=True the rows themselves, Y.  Not differentiable."""
+    return (_native or _binding()).rms_norm_quantize(X, weight, eps, residual, codes, keep, sum_out)
+
+
+def rms_norm_backward_workspace_size(rows, K, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace rms_norm_backward takes for rows of this type on the current device."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+    return _query("rms_norm_backward_workspace_size", rows, K,
+                  _base.IN_BF16 if dtype == torch.bfloat16 else _base.IN_F32)
+
+
+def rms_norm_backward(dY, X, weight=None, eps=1e-6, dH=None, workspace=None):
+    """The gradients (dX like X, dW like weight or None) of rms_norm for the incoming dY and, where H was used further
+    on, dH, both like X.  X: the rows that were normed (H where there was a residual, whose gradient is dX too).
+    `workspace` (uint8) needs rms_norm_backward_workspace_size bytes; None allocates them.  Nothing is recorded: the
+    results carry no graph."""
+    return (_native or _binding()).rms_norm_backward(dY, X, weight, eps, dH, True, workspace)

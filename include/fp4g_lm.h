@@ -1,0 +1,75 @@
+/*
+ * fp4g_lm.h -- C ABI of the operators that stand around a language model's products in
+ * libfp4gemm.so for AMD Instinct MI355X (gfx950): the root-mean-square norm with its 8-bit
+ * outputs and its backward pass.
+ *
+ * Conventions are those of fp4gemm.h: plain device pointers owned by the caller, row-major
+ * buffers without padding, calls asynchronous on `stream` (a hipStream_t; NULL is the
+ * default stream), no allocation, arguments validated on the host before anything is
+ * launched, statuses of fp4g_status.  Only kernels are enqueued, so calls may be captured.
+ * Results repeat bit for bit: every sum has a fixed order.
+ *
+ * Sizes (all entry points): each dimension >= 0 and below 2^31 and each buffer of at most
+ * 2^50 elements (FP4G_EINVAL otherwise).  Workspaces are 16-byte aligned, need no clearing
+ * and hold nothing between calls; the *_workspace_size queries give their sizes on the
+ * current device.  Two calls that may run at once need a workspace each.  Outputs overlap
+ * neither an input nor each other, but for the cases named below.
+ */
+#ifndef FP4G_LM_H
+#define FP4G_LM_H
+
+#include "fp4gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The codes of rms_norm_quantize, taken as `int code_type` and validated (FP4G_EINVAL):
+ * what w8a8_gemm and w4a8_gemm take as activations. */
+typedef enum {
+    FP4G_CODE_INT8 = 0,
+    FP4G_CODE_E4M3 = 1
+} fp4g_code_type;
+
+/* The root-mean-square norm of each row:
+ *   h = x, or x + r rounded to their type where R is given,
+ *   Y = (h * s) * w,  s = 1 / sqrt(mean(h^2) + eps),
+ * with the mean in 64 bits, s rounded to fp32, both products in fp32 and one rounding to Y's
+ * type.  X, R, H and Y [rows][K] are all fp32 or all bf16 by x_type; W [K] is fp32 or bf16
+ * by w_type, or NULL (w = 1).  H is written where R is given (both or neither,
+ * FP4G_EINVAL).  eps is finite and not negative (FP4G_EINVAL); with eps == 0 a row of zeros
+ * gives NaN, as the formula does.  Any K; K == 0 is a no-op.  Buffers are aligned to their
+ * elements (FP4G_EALIGN).  H may be X or R itself, and Y may be X or R itself, but not both
+ * the same one. */
+fp4g_status rms_norm(int64_t rows, int64_t K, const void *X, int x_type, const void *R,
+                     const void *W, int w_type, double eps, void *H, void *Y, void *stream);
+
+/* The same norm quantized by rows: with y the fp32 products above, before any rounding to
+ * Y's type, and T = 127 (int8) or 448 (E4M3), every step in IEEE fp32:
+ *   scale = max|y| / T,  inv = min(1 / scale, FLT_MAX),
+ *   code  = y * inv rounded to the nearest code, ties to even, clamped to +-T.
+ * A row of zeros has scale 0 and zero codes; a row whose y hold an infinity or NaN has a NaN
+ * scale and zero codes.  codes [rows][K] are int8 or E4M3 bytes by code_type, scales [rows]
+ * fp32.  Y may be NULL: it is not written then.  K == 0 writes scales 0. */
+fp4g_status rms_norm_quantize(int64_t rows, int64_t K, const void *X, int x_type, const void *R,
+                              const void *W, int w_type, double eps, void *H, void *Y,
+                              void *codes, int code_type, float *scales, void *stream);
+
+/* The gradients of rms_norm in X (and in R, which has the same) and in W, from the incoming
+ * dY and, where it is not NULL, dH [rows][K], with X the rows that were normed (rms_norm's H
+ * where it added a residual), g = dY * w and n = x * s, in fp32 with one rounding each:
+ *   dX = s * (g - n * mean(g * n)) + dH,   dW = sum over rows of dY * n.
+ * dY, dH and dX have X's type, dW has W's.  dW may be NULL and has to be where W is
+ * (FP4G_EINVAL).  dX may be dY or dH itself.  The workspace is required (fewer bytes than
+ * the query's are FP4G_EINVAL): it holds dW's partial sums.  rows == 0 zeroes dW. */
+fp4g_status rms_norm_backward_workspace_size(int64_t rows, int64_t K, int x_type, size_t *bytes);
+fp4g_status rms_norm_backward(int64_t rows, int64_t K, const void *dY, const void *X, int x_type,
+                              const void *W, int w_type, double eps, const void *dH,
+                              void *dX, void *dW, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP4G_LM_H */
