@@ -145,7 +145,80 @@ PyObject* py_rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// What both passes of the loss take: X, W, target and ignore_index.
+struct Loss {
+  at::Tensor X, W, target;
+  int64_t M, V, K, ignore;
+};
+Loss loss_of(PyObject* x, PyObject* w, PyObject* target, PyObject* ignore) {
+  Loss a;
+  a.X = matrix(x, "X", at::kBFloat16, at::kBFloat16);
+  a.M = a.X.size(0), a.K = a.X.size(1);
+  a.V = matrix(w, "W", at::kBFloat16, at::kBFloat16).size(0);
+  multiple_of(a.K, 8);
+  a.W = need(w, "W", at::kBFloat16, {a.V, a.K}, a.X.device());
+  a.target = need(target, "target", at::kLong, {a.M}, a.X.device());
+  a.ignore = PyLong_AsLongLong(ignore);
+  if (a.ignore == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    type_error("ignore_index must be an integer of 64 bits");
+  }
+  return a;
+}
+
+// X, W, target, ignore_index, save, workspace
+PyObject* py_cross_entropy_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 6, [&] {
+    const Loss a = loss_of(v[0], v[1], v[2], v[3]);
+    const at::Device device = a.X.device();
+    const c10::DeviceGuard guard(device);
+    const bool save = truth(v[4]);
+    if (recorded({&a.X, &a.W})) Py_RETURN_NONE;
+    const at::Tensor loss = empty({a.M}, at::kFloat, device);
+    at::Tensor lse;
+    if (save) lse = empty({a.M}, at::kFloat, device);
+    const Space w = space(v[5], device, [&] {
+      size_t bytes = 0;
+      check_status("cross_entropy_gemm_workspace_size", cross_entropy_gemm_workspace_size(a.M, a.V, a.K, &bytes));
+      return bytes;
+    });
+    launch("cross_entropy_gemm", device, [&](void* stream) {
+      return cross_entropy_gemm(a.M, a.V, a.K, ptr(a.X), ptr(a.W), static_cast<const int64_t*>(ptr(a.target)), a.ignore,
+                                floats(loss), save ? floats(lse) : nullptr, w.p, w.bytes, stream);
+    });
+    return save ? tuple({loss, lse}) : THPVariable_Wrap(loss);
+  });
+}
+
+// dL, X, W, target, lse, ignore_index, want_dx, want_dw, workspace
+PyObject* py_cross_entropy_gemm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 9, [&] {
+    const Loss a = loss_of(v[1], v[2], v[3], v[5]);
+    const at::Device device = a.X.device();
+    const c10::DeviceGuard guard(device);
+    const at::Tensor& dL = need(v[0], "dL", at::kFloat, {a.M}, device);
+    const at::Tensor& lse = need(v[4], "lse", at::kFloat, {a.M}, device);
+    at::Tensor dX, dW;
+    if (truth(v[6])) dX = empty({a.M, a.K}, at::kBFloat16, device);
+    if (truth(v[7])) dW = empty({a.V, a.K}, at::kBFloat16, device);
+    const Space w = space(v[8], device, [&] {
+      size_t bytes = 0, least = 0;
+      check_status("cross_entropy_gemm_backward_workspace_size",
+                   cross_entropy_gemm_backward_workspace_size(a.M, a.V, a.K, &bytes, &least));
+      return bytes;
+    });
+    launch("cross_entropy_gemm_backward", device, [&](void* stream) {
+      return cross_entropy_gemm_backward(a.M, a.V, a.K, floats(dL), ptr(a.X), ptr(a.W),
+                                         static_cast<const int64_t*>(ptr(a.target)), a.ignore, floats(lse),
+                                         dX.defined() ? ptr(dX) : nullptr, dW.defined() ? ptr(dW) : nullptr, w.p,
+                                         w.bytes, stream);
+    });
+    return tuple({dX, dW});   // None for an undefined tensor
+  });
+}
+
 PyMethodDef methods[] = {FASTCALL(rms_norm), FASTCALL(rms_norm_quantize), FASTCALL(rms_norm_backward),
+                         FASTCALL(cross_entropy_gemm), FASTCALL(cross_entropy_gemm_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -3,6 +3,7 @@
 // so an invalid call returns its status without touching the device.
 #include "lm_internal.h"
 
+#include <algorithm>
 #include <cmath>
 
 #include "api_checks.hpp"
@@ -61,6 +62,21 @@ fp4g_status check_norm(int64_t rows, int64_t K, const void* X, int x_type, const
   return check_buffers({unless(x, {H, Y}), unless(r, {H, Y}), w}, {h, y, c, s});
 }
 
+// Sizes of a loss's products: rows of X and W are operands of the tiles.
+fp4g_status check_loss_sizes(int64_t M, int64_t V, int64_t K) {
+  if (!sizes_fit({M, V, K}) || !holds(M, K) || !holds(V, K) || !holds(M, V) || (M > 0 && V == 0)) return FP4G_EINVAL;
+  return K % 8 != 0 || K > (1 << 21) || M > (1 << 25) ? FP4G_EUNSUPPORTED : FP4G_OK;
+}
+
+// The columns of a piece for a workspace of `room` bytes: the choice without a limit, or as many
+// as fit; 0 if none do.
+int64_t piece_cols(int64_t M, int64_t V, int64_t K, size_t room) {
+  for (int64_t cols = fp4g::loss_grad_cols(M, V, K);; cols = std::max<int64_t>(64, cols / 2 / 64 * 64)) {
+    if ((size_t)fp4g::loss_grad_bytes(M, V, K, cols) <= room) return cols;
+    if (cols == 64) return 0;
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,6 +127,60 @@ fp4g_status rms_norm_backward(int64_t rows, int64_t K, const void* dY, const voi
   if (workspace_bytes < (size_t)fp4g::rms_norm_grad_bytes(rows, K, bf16)) return FP4G_EINVAL;
   const fp4g::NormGradArgs a{rows, K, dY, X, W, dH, dX, dW, bf16, w_type == FP4G_IN_BF16, eps, workspace};
   return finish(fp4g::launch_rms_norm_grad(a, s));
+}
+
+fp4g_status cross_entropy_gemm_workspace_size(int64_t M, int64_t V, int64_t K, size_t* bytes) {
+  const fp4g_status st = check_loss_sizes(M, V, K);
+  if (st != FP4G_OK) return st;
+  if (!bytes) return FP4G_EINVAL;
+  *bytes = M == 0 ? 0 : (size_t)fp4g::loss_bytes(M, V, K);
+  return FP4G_OK;
+}
+
+fp4g_status cross_entropy_gemm(int64_t M, int64_t V, int64_t K, const void* X, const void* W, const int64_t* target,
+                               int64_t ignore_index, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  fp4g_status st = check_loss_sizes(M, V, K);
+  if (st != FP4G_OK || M == 0) return st;
+  st = check_buffers({buf(X, M * K * 2), buf(W, V * K * 2), buf(target, M * 8, 8)},
+                     {buf(loss, M * 4, 4), buf(lse, lse ? M * 4 : 0, 4), buf(workspace, workspace_bytes)});
+  if (st != FP4G_OK) return st;
+  if (workspace_bytes < (size_t)fp4g::loss_bytes(M, V, K)) return FP4G_EINVAL;
+  fp4g::LossCall c{M, V, K, X, W, target, ignore_index};
+  c.loss = loss, c.lse = lse, c.space = static_cast<uint8_t*>(workspace);
+  return finish(fp4g::launch_loss(c, reinterpret_cast<hipStream_t>(stream)));
+}
+
+fp4g_status cross_entropy_gemm_backward_workspace_size(int64_t M, int64_t V, int64_t K, size_t* bytes, size_t* least) {
+  const fp4g_status st = check_loss_sizes(M, V, K);
+  if (st != FP4G_OK) return st;
+  if (!bytes || !least) return FP4G_EINVAL;
+  *bytes = *least = 0;
+  if (M == 0 || K == 0) return FP4G_OK;
+  *bytes = (size_t)fp4g::loss_grad_bytes(M, V, K, fp4g::loss_grad_cols(M, V, K));
+  *least = std::min(*bytes, (size_t)fp4g::loss_grad_bytes(M, V, K, 64));
+  return FP4G_OK;
+}
+
+fp4g_status cross_entropy_gemm_backward(int64_t M, int64_t V, int64_t K, const float* dL, const void* X, const void* W,
+                                        const int64_t* target, int64_t ignore_index, const float* lse, void* dX,
+                                        void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_loss_sizes(M, V, K);
+  if (st != FP4G_OK || K == 0) return st;
+  const bool some = M > 0;
+  st = check_buffers({buf(dL, M * 4, 4), buf(X, M * K * 2), buf(W, some ? V * K * 2 : 0), buf(target, M * 8, 8),
+                      buf(lse, M * 4, 4)},
+                     {buf(dX, dX ? M * K * 2 : 0), buf(dW, dW ? V * K * 2 : 0), buf(workspace, some ? workspace_bytes : 0)});
+  if (st != FP4G_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (!some) return finish(dW ? zero(dW, V * K, true, s) : hipSuccess);
+  const int64_t cols = piece_cols(M, V, K, workspace_bytes);
+  if (cols == 0) return FP4G_EINVAL;
+  if (!dX && !dW) return FP4G_OK;
+  fp4g::LossCall c{M, V, K, X, W, target, ignore_index};
+  c.lse = const_cast<float*>(lse), c.dL = dL, c.dX = dX, c.dW = dW;
+  c.space = static_cast<uint8_t*>(workspace), c.cols = cols;
+  return finish(fp4g::launch_loss_grad(c, s));
 }
 
 }  // extern "C"

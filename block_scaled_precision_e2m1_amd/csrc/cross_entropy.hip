@@ -1,0 +1,366 @@
+// The softmax cross entropy over a vocabulary for gfx950, without the logits in memory, and its
+// gradients:
+//   z = X W^T,  lse[m] = log sum_v e^z[m][v],  loss[m] = lse[m] - z[m][target[m]]
+//   P = (e^(z - lse) - [v == target]) dL,  dX = P W,  dW = P^T X
+//
+// Bound by the matrix instructions: 2 M V K operations forward, 8 M V K for the gradients, of
+// which 2 form the logits again.  The products are those of dense_tile.hpp:
+//
+//   * Forward, a tile's end leaves the maximum and the sum of the exponentials of each row over
+//     a wave's columns (8 bytes for 64 or 128 logits), and a last kernel joins them.
+//   * Backward, the vocabulary is taken in pieces.  A piece's logits are formed again and leave
+//     their tiles as P in bf16, the operand of both gradients' products; dW's rows of the piece
+//     are then whole, and dX is summed over the pieces in fp32.
+//   * Rows without a loss (a prompt's tokens, padding) take no part: the rows that have one are
+//     gathered first, their number stays on the GPU, and the tiles read it there.  Half of
+//     the rows ignored is half of the time, and what an ignored row holds reaches nothing.
+//     The gathering copy moves 4 M K bytes.
+#include <algorithm>
+
+#include "dense_tile.hpp"
+#include "launch.hpp"
+#include "lm_internal.h"
+
+namespace fp4g {
+namespace {
+
+// ---- the rows that take part ----
+
+struct Pick {
+  int64_t M, K;                   // K: a multiple of 8
+  int64_t V, ignore;
+  const int64_t* target;
+  const v4i* X;
+  const int* counts;              // rows that take part among each 1024, or null: count them here
+  v4i* rows;                      // [M][K] those rows, in order
+  int *map, *wanted, *count;      // which row each was, its target or -1, and their number
+  float *loss, *lse;              // forward: 0 for the rows that take no part
+  float* z;                       // forward: the wanted logit, NaN until it is found
+  const float *dL, *lse_in;       // backward: taken to the rows that take part
+  float *g, *lse2;
+  v4i* dX;                        // backward: 0 for the rows that take no part
+};
+constexpr int kChunk = 1024;
+
+__device__ __forceinline__ int block_sum(int v, int* part) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return part[0] + part[1] + part[2] + part[3];
+}
+
+__global__ void __launch_bounds__(256) loss_count_kernel(int64_t M, int64_t ignore, const int64_t* __restrict__ target,
+                                                         int* __restrict__ counts) {
+  __shared__ int part[4];
+  const int64_t first = (int64_t)blockIdx.x * kChunk;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk / 256; ++i) {
+    const int64_t m = first + i * 256 + threadIdx.x;
+    n += m < M && target[m] != ignore;
+  }
+  n = block_sum(n, part);
+  if (threadIdx.x == 0) counts[blockIdx.x] = n;
+}
+
+// A wave for each of 4 rows: how many before it take part is counted by the whole workgroup, in
+// the row's chunk alone where the chunks before it are counted already.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
+  __shared__ int part[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row0 = (int64_t)blockIdx.x * 4, m = row0 + wave;
+  int before = 0;
+  int64_t from = 0;
+  if (a.counts) {
+    from = row0 / kChunk * kChunk;
+    for (int64_t c = threadIdx.x; c < row0 / kChunk; c += 256) before += a.counts[c];
+  }
+  for (int64_t i = from + threadIdx.x; i < row0; i += 256) before += a.target[i] != a.ignore;
+  before = block_sum(before, part);
+  bool in[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) in[w] = row0 + w < a.M && a.target[row0 + w] != a.ignore;
+  int slot = before;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) slot += w < wave && in[w];
+  if (row0 + 4 >= a.M && threadIdx.x == 0) *a.count = before + in[0] + in[1] + in[2] + in[3];
+  if (m >= a.M) return;
+  const int64_t units = a.K / 8;
+  if (!in[wave]) {
+    if constexpr (GRAD) {
+      if (a.dX)
+        for (int64_t u = lane; u < units; u += 64) a.dX[m * units + u] = v4i{0, 0, 0, 0};
+    } else if (lane == 0) {
+      a.loss[m] = 0.0f;
+      if (a.lse) a.lse[m] = 0.0f;
+    }
+    return;
+  }
+  for (int64_t u = lane; u < units; u += 64) a.rows[slot * units + u] = a.X[m * units + u];
+  if (lane == 0) {
+    const int64_t t = a.target[m];
+    const bool known = t >= 0 && t < a.V;
+    a.map[slot] = (int)m;
+    a.wanted[slot] = known ? (int)t : -1;
+    if constexpr (GRAD) {
+      a.g[slot] = known ? a.dL[m] : __builtin_nanf("");
+      a.lse2[slot] = a.lse_in[m] * kLog2e;
+    } else {
+      a.z[slot] = __builtin_nanf("");
+    }
+  }
+}
+
+hipError_t launch_pick(Pick p, int* counts, bool grad, hipStream_t s) {
+  // Up to 4096 targets (32 KB) are counted by every workgroup for itself.
+  if (p.M > 4096) {
+    const hipError_t e = launch(loss_count_kernel, ceil_div(p.M, kChunk), 256, s, p.M, p.ignore, p.target, counts);
+    if (e != hipSuccess) return e;
+    p.counts = counts;
+  }
+  return launch(grad ? loss_pick_kernel<true> : loss_pick_kernel<false>, ceil_div(p.M, 4), 256, s, p);
+}
+
+// ---- forward ----
+
+// The parts of a row joined: 16 rows a workgroup, every 16th part a thread.
+__global__ void __launch_bounds__(256) loss_join_kernel(int64_t M, int parts, const int* __restrict__ count,
+                                                        const float2* __restrict__ part, const float* __restrict__ z,
+                                                        const int* __restrict__ map, float* __restrict__ loss,
+                                                        float* __restrict__ lse) {
+  __shared__ float2 held[16][17];
+  const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int64_t m = (int64_t)blockIdx.x * 16 + r;
+  const bool there = m < *count;
+  // e^(a - b) of the first part is e^-inf = 0; of two parts at -infinity 0, their sums are 0 too.
+  auto join = [](float2 x, float2 y) {
+    const float most = fmaxf(x.x, y.x), from = most == -__builtin_inff() ? 0.0f : most;
+    return make_float2(most, x.y * __builtin_amdgcn_exp2f((x.x - from) * kLog2e) +
+                                 y.y * __builtin_amdgcn_exp2f((y.x - from) * kLog2e));
+  };
+  float2 all = make_float2(-__builtin_inff(), 0.0f);
+  if (there) {
+#pragma unroll 4
+    for (int p = q; p < parts; p += 16) all = join(all, part[(int64_t)p * M + m]);
+  }
+  held[q][r] = all;
+  __syncthreads();
+  if (q == 0 && there) {
+#pragma unroll
+    for (int p = 1; p < 16; ++p) all = join(all, held[p][r]);
+    // (maximum - z) first: it is small where the loss is.
+    const float l = logf(all.y);
+    const int row = map[m];
+    loss[row] = (all.x - z[m]) + l;
+    if (lse) lse[row] = all.x + l;
+  }
+}
+
+template <class C, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) loss_gemm_kernel(const LossArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS];
+  dense_gemm<C, BF16, false, SPLIT>(a, blockIdx.x, gridDim.x, smem);
+}
+
+template <class C, bool BF16, bool SPLIT>
+hipError_t launch_tiles(const LossArgs& a, hipStream_t s) {
+  const int64_t items = ceil_div(a.M, C::BM) * ceil_div(a.N, C::OUTN) * a.S;
+  if (items > INT32_MAX / 2) return hipErrorInvalidConfiguration;
+  return launch(loss_gemm_kernel<C, BF16, SPLIT>, std::min<int64_t>(items, device_cus() * C::OCC), C::NW * 64, s, a);
+}
+
+// The tiles whose waves have whole sums (one group of waves): the loss's end joins a row's columns
+// in registers.
+constexpr uint32_t kOneGroup = 1u << kTile256 | 1u << kTile128 | 1u << kTile64x128 | 1u << kTile64x128Long;
+
+template <class S, bool BF16, bool SPLIT>
+hipError_t launch_one_group(const LossArgs& a, DenseTile tile, hipStream_t s) {
+  switch (tile) {
+    case kTile256: return launch_tiles<typename S::t256, BF16, SPLIT>(a, s);
+    case kTile128: return launch_tiles<typename S::t128, BF16, SPLIT>(a, s);
+    case kTile64x128: return launch_tiles<typename S::t64x128, BF16, SPLIT>(a, s);
+    case kTile64x128Long: return launch_tiles<typename S::t64x128_long, BF16, SPLIT>(a, s);
+    default: return hipErrorInvalidConfiguration;
+  }
+}
+template <class S, bool BF16, bool SPLIT>
+hipError_t launch_any(const LossArgs& a, DenseTile tile, hipStream_t s) {
+  switch (tile) {
+    case kTile128Deep: return launch_tiles<typename S::t128_deep, BF16, SPLIT>(a, s);
+    case kTile64Deep: return launch_tiles<typename S::t64_deep, BF16, SPLIT>(a, s);
+    case kTile64: return launch_tiles<typename S::t64, BF16, SPLIT>(a, s);
+    case kTile64Long: return launch_tiles<typename S::t64_long, BF16, SPLIT>(a, s);
+    default: return launch_one_group<S, BF16, SPLIT>(a, tile, s);
+  }
+}
+typedef Tiles<BF, kLoss, false, false, 1> Forward;       // X W^T: both operands' rows hold K
+typedef Tiles<BF, kProb, false, false, 1> Probabilities; // the same
+typedef Tiles<BF, kAccum, false, true, 1> GradInput;     // P W: W's rows are the contraction's
+typedef Tiles<BF, kCounted, true, true, 1> GradWeights;  // P^T X: both operands' rows are
+
+DensePlan forward_plan(int64_t M, int64_t V, int64_t K) {
+  return dense_plan_among(kOneGroup, M, V, 1, ceil_div(K, 64), 1);
+}
+int wave_cols(DenseTile t) { return t == kTile256 ? 128 : 64; }
+
+// Parts of a workspace, each on a line of its own.
+struct Space {
+  uint8_t* p;
+  int64_t used = 0;
+  template <class T>
+  T* take(int64_t count) {
+    T* r = reinterpret_cast<T*>(p + used);
+    used += (count * (int64_t)sizeof(T) + 255) / 256 * 256;
+    return r;
+  }
+};
+struct Picked {
+  uint8_t* rows;
+  int *map, *wanted, *count, *counts;
+  Picked(Space& s, int64_t M, int64_t K)
+      : rows(s.take<uint8_t>(M * K * 2)), map(s.take<int>(M)), wanted(s.take<int>(M)), count(s.take<int>(1)),
+        counts(s.take<int>(ceil_div(M, kChunk))) {}
+};
+struct ForwardSpace {
+  Space s;
+  Picked picked;
+  int64_t parts;
+  float* z;
+  float2* part;
+  ForwardSpace(uint8_t* p, int64_t M, int64_t V, int64_t K)
+      : s{p}, picked(s, M, K), parts(ceil_div(V, wave_cols(forward_plan(M, V, K).tile))), z(s.take<float>(M)),
+        part(s.take<float2>(parts * M)) {}
+};
+
+Pick pick_of(const LossCall& a, const Picked& p) {
+  Pick k{};
+  k.M = a.M, k.K = a.K, k.V = a.V, k.ignore = a.ignore, k.target = a.target;
+  k.X = static_cast<const v4i*>(a.X), k.rows = reinterpret_cast<v4i*>(p.rows);
+  k.map = p.map, k.wanted = p.wanted, k.count = p.count;
+  return k;
+}
+
+// ---- backward ----
+
+// The end of dX's split product: the slices in order, what the pieces before gave, and to the
+// rows' places at the last piece.
+template <bool BF16>
+__global__ void __launch_bounds__(256) loss_reduce_kernel(const LossArgs a) {
+  const uint32_t groups = (uint32_t)(a.N / 4), total = (uint32_t)*a.count * groups;
+  const int64_t plane = (int64_t)a.M * groups;
+  for (uint32_t x = blockIdx.x * 256 + threadIdx.x; x < total; x += gridDim.x * 256) {
+    const uint32_t m = x / groups, n = (x - m * groups) * 4;
+    const v4f* p = static_cast<const v4f*>(a.P) + x;
+    v4f t = p[0];
+#pragma unroll 4
+    for (int k = 1; k < a.S; ++k) t += p[k * plane];
+    if (a.add) t += *reinterpret_cast<const v4f*>(a.add + (int64_t)m * a.N + n);
+    const float y[4] = {t[0], t[1], t[2], t[3]};
+    store_cols<BF16>(a.D[0], (int64_t)(BF16 ? a.map[m] : (int)m) * a.N + n, 4, y);
+  }
+}
+
+// dX's product over one piece of the vocabulary.
+DensePlan input_plan(int64_t M, int64_t K, int64_t cols) { return dense_plan(M, K, 1, ceil_div(cols, 64), kMaxSplits); }
+
+struct GradSpace {
+  Space s;
+  Picked picked;
+  float *g, *lse2, *kept, *P;
+  int64_t ldp;
+  uint8_t* prob;
+  GradSpace(uint8_t* p, int64_t M, int64_t V, int64_t K, int64_t cols)
+      : s{p}, picked(s, M, K), g(s.take<float>(M)), lse2(s.take<float>(M)),
+        kept(s.take<float>(cols < V ? M * K : 0)), P(nullptr), ldp(ceil_div(cols, 64) * 64),
+        prob(s.take<uint8_t>(M * ldp * 2)) {
+    // Pieces differ by their last one, which may split further.
+    int64_t splits = 0;
+    for (int64_t c : {std::min(cols, V), V % cols ? V % cols : cols}) {
+      const int64_t S = input_plan(M, K, std::min(c, V)).S;
+      if (S > 1) splits = std::max(splits, S);
+    }
+    P = s.take<float>(splits * M * K);
+  }
+};
+
+}  // namespace
+
+int64_t loss_bytes(int64_t M, int64_t V, int64_t K) { return ForwardSpace(nullptr, M, V, K).s.used; }
+
+hipError_t launch_loss(const LossCall& c, hipStream_t s) {
+  const ForwardSpace w(c.space, c.M, c.V, c.K);
+  Pick k = pick_of(c, w.picked);
+  k.loss = c.loss, k.lse = c.lse, k.z = w.z;
+  hipError_t e = launch_pick(k, w.picked.counts, false, s);
+  if (e != hipSuccess) return e;
+  LossArgs a;
+  a.M = (int)c.M, a.N = (int)c.V, a.K = (int)c.K;
+  a.A[0] = w.picked.rows, a.B[0] = static_cast<const uint8_t*>(c.W), a.lda = a.ldb = c.K * 2;
+  a.count = w.picked.count, a.target = w.picked.wanted, a.parts = w.part, a.wanted = w.z;
+  e = launch_one_group<Forward, true, false>(a, forward_plan(c.M, c.V, c.K).tile, s);
+  if (e != hipSuccess) return e;
+  return launch(loss_join_kernel, ceil_div(c.M, 16), 256, s, c.M, (int)w.parts, static_cast<const int*>(a.count),
+                static_cast<const float2*>(w.part), static_cast<const float*>(w.z),
+                static_cast<const int*>(w.picked.map), c.loss, c.lse);
+}
+
+int64_t loss_grad_bytes(int64_t M, int64_t V, int64_t K, int64_t cols) {
+  return GradSpace(nullptr, M, V, K, cols).s.used;
+}
+
+// Pieces of about 256 MB of P, of equal length but for whole tiles: enough columns to fill the
+// chip with each product, few enough that P stays in the last-level cache on its way.
+int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K) {
+  const int64_t fill = ((int64_t)256 << 20) / (2 * M) / 256 * 256, most = std::min<int64_t>(std::max<int64_t>(fill, 1024), 1 << 20);
+  if (V <= most) return ceil_div(V, 64) * 64;
+  return ceil_div(ceil_div(V, ceil_div(V, most)), 256) * 256;
+}
+
+hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
+  const GradSpace w(c.space, c.M, c.V, c.K, c.cols);
+  Pick k = pick_of(c, w.picked);
+  k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse2 = w.lse2, k.dX = static_cast<v4i*>(c.dX);
+  hipError_t e = launch_pick(k, w.picked.counts, true, s);
+  if (e != hipSuccess) return e;
+  for (int64_t v = 0; v < c.V; v += c.cols) {
+    const int64_t n = std::min(c.cols, c.V - v);
+    const uint8_t* W = static_cast<const uint8_t*>(c.W) + v * c.K * 2;
+    LossArgs p;
+    p.M = (int)c.M, p.N = (int)n, p.K = (int)c.K;
+    p.A[0] = w.picked.rows, p.B[0] = W, p.lda = p.ldb = c.K * 2, p.D[0] = w.prob, p.ldp = w.ldp;
+    p.count = w.picked.count, p.target = w.picked.wanted, p.col0 = (int)v, p.lse2 = w.lse2, p.g = w.g;
+    e = launch_any<Probabilities, true, false>(p, dense_plan(c.M, n, 1, ceil_div(c.K, 64), 1).tile, s);
+    if (e != hipSuccess) return e;
+
+    if (c.dX) {
+      const DensePlan plan = input_plan(c.M, c.K, n);
+      const bool last = v + n == c.V;
+      LossArgs x;
+      x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
+      x.A[0] = w.prob, x.lda = w.ldp * 2, x.B[0] = W, x.ldb = c.K * 2, x.P = w.P;
+      x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
+      x.D[0] = last ? c.dX : w.kept;
+      if (plan.S > 1) {
+        e = launch_any<GradInput, false, true>(x, plan.tile, s);
+        if (e != hipSuccess) return e;
+        const int64_t grid = std::min<int64_t>(ceil_div(c.M * (c.K / 4), 256), device_cus() * 8);
+        e = launch(last ? loss_reduce_kernel<true> : loss_reduce_kernel<false>, grid, 256, s, x);
+      } else {
+        e = last ? launch_any<GradInput, true, false>(x, plan.tile, s) : launch_any<GradInput, false, false>(x, plan.tile, s);
+      }
+      if (e != hipSuccess) return e;
+    }
+    if (!c.dW) continue;
+    LossArgs d;
+    d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;
+    d.A[0] = w.prob, d.lda = w.ldp * 2, d.B[0] = w.picked.rows, d.ldb = c.K * 2;
+    d.D[0] = static_cast<uint8_t*>(c.dW) + v * c.K * 2, d.count = w.picked.count;
+    e = launch_any<GradWeights, true, false>(d, dense_plan(n, c.K, 1, ceil_div(c.M, 64), 1).tile, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp4g

@@ -43,6 +43,8 @@ struct GradPlan { DensePlan x, w; bool merged; };         // dX; dWg and dWu; in
 // Tile and K split for L products of rows x cols sums (gated: cols counts both weights'
 // columns) over KT stages of 128 bytes of K; at most `cap` slices.
 DensePlan dense_plan(int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap);
+// The same of the tiles whose bit (1 << DenseTile) is set.
+DensePlan dense_plan_among(uint32_t tiles, int64_t rows, int64_t cols, int64_t L, int64_t KT, int64_t cap);
 
 // Whether a product of M tokens with `gates` weights of N rows of KB bytes goes to the kernels
 // for few tokens (dense_gemv.hip), and its K split there, of at most `cap` slices.

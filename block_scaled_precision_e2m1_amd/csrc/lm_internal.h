@@ -39,4 +39,23 @@ struct NormGradArgs {
 int64_t rms_norm_grad_bytes(int64_t rows, int64_t K, bool bf16);
 hipError_t launch_rms_norm_grad(const NormGradArgs& a, hipStream_t s);
 
+struct LossCall {
+  int64_t M, V, K;
+  const void *X, *W;
+  const int64_t* target;
+  int64_t ignore;
+  float *loss, *lse;              // lse: may be null; backward: what the forward pass gave
+  const float* dL;                // backward
+  void *dX, *dW;
+  uint8_t* space;
+  int64_t cols;                   // backward: columns of a piece
+};
+// Workspace bytes of the two passes (M, V > 0); backward: with pieces of `cols` columns, and how
+// many columns a piece has by choice.
+int64_t loss_bytes(int64_t M, int64_t V, int64_t K);
+int64_t loss_grad_bytes(int64_t M, int64_t V, int64_t K, int64_t cols);
+int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K);
+hipError_t launch_loss(const LossCall& a, hipStream_t s);
+hipError_t launch_loss_grad(const LossCall& a, hipStream_t s);
+
 }  // namespace fp4g

@@ -1,4 +1,5 @@
-"""Operators around a language model's products: the norm before them, in their types or in 8 bits, with its gradient.
+"""Operators around a language model's products: the norm before them, in their types or in 8 bits, and the loss over
+the vocabulary behind them, with their gradients.
 
 A binding over the C ABI of ``include/fp4g_lm.h`` in the manner of the package's other
 functions: each has the name of its C entry point, checks its torch arguments, runs on the
@@ -9,7 +10,10 @@ Layouts (contiguous, all on one GPU):
   rms_norm           : X [rows, K] float32 or bfloat16, weight [K] float32 or bfloat16 -> Y like X
   rms_norm_quantize  : the same -> codes [rows, K] int8 or uint8 (E4M3), scales [rows] float32
   rms_norm_backward  : the gradients of rms_norm
-rms_norm takes part in autograd; the results of the other functions carry no graph.
+  cross_entropy_gemm           : X [M, K], W [V, K] bfloat16, target [M] int64 -> loss [M] float32
+  cross_entropy_gemm_backward  : the gradients of cross_entropy_gemm, bfloat16
+K of the loss is a multiple of 8.  rms_norm and cross_entropy_gemm take part in autograd; the results of the other
+functions carry no graph.
 """
 from __future__ import annotations
 
@@ -21,9 +25,11 @@ import torch
 
 import block_scaled_precision_e2m1_amd as _base
 
-__all__ = ["rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward", "LM_SYMBOLS"]
+LM_SYMBOLS = ("rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward",
+              "cross_entropy_gemm_workspace_size", "cross_entropy_gemm", "cross_entropy_gemm_backward_workspace_size",
+              "cross_entropy_gemm_backward")
 
-LM_SYMBOLS = ("rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward")
+__all__ = [*LM_SYMBOLS, "LM_SYMBOLS"]
 
 
 @functools.lru_cache(maxsize=None)
@@ -36,6 +42,10 @@ def _library():
         "rms_norm_quantize": [i64, i64, p, c_int, p, p, c_int, f64, p, p, p, c_int, p, p],
         "rms_norm_backward_workspace_size": [i64, i64, c_int, psize],
         "rms_norm_backward": [i64, i64, p, p, c_int, p, c_int, f64, p, p, p, p, size, p],
+        "cross_entropy_gemm_workspace_size": [i64, i64, i64, psize],
+        "cross_entropy_gemm": [i64, i64, i64, p, p, p, i64, p, p, p, size, p],
+        "cross_entropy_gemm_backward_workspace_size": [i64, i64, i64, psize, psize],
+        "cross_entropy_gemm_backward": [i64, i64, i64, p, p, p, p, i64, p, p, p, p, size, p],
     }
     for name, a in args.items():
         fn = getattr(lib, name)
@@ -134,3 +144,68 @@ def rms_norm_backward(dY, X, weight=None, eps=1e-6, dH=None, workspace=None):
     `workspace` (uint8) needs rms_norm_backward_workspace_size bytes; None allocates them.  Nothing is recorded: the
     results carry no graph."""
     return (_native or _binding()).rms_norm_backward(dY, X, weight, eps, dH, True, workspace)
+
+
+class _LossGradients(torch.autograd.Function):
+    """cross_entropy_gemm_backward within a backward pass; as _NormGradients."""
+
+    @staticmethod
+    def forward(ctx, dL, X, W, target, lse, ignore_index, want_dx, want_dw):
+        return _binding().cross_entropy_gemm_backward(dL, X, W, target, lse, ignore_index, want_dx, want_dw, None)
+
+    @staticmethod
+    def backward(ctx, *_):
+        _no_second("cross_entropy_gemm")
+
+
+class _CrossEntropyGemm(torch.autograd.Function):
+    """cross_entropy_gemm with its gradient, from the lse that it keeps."""
+
+    @staticmethod
+    def forward(ctx, X, W, target, ignore_index, workspace):
+        loss, lse = _binding().cross_entropy_gemm(X, W, target, ignore_index, True, workspace)
+        ctx.save_for_backward(X, W, target, lse)
+        ctx.ignore_index = ignore_index
+        ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, dL, _):
+        if dL is None:
+            return (None,) * 5
+        dX, dW = _LossGradients.apply(dL.contiguous(), *ctx.saved_tensors, ctx.ignore_index, *ctx.needs_input_grad[:2])
+        return dX, dW, None, None, None
+
+
+def cross_entropy_gemm_workspace_size(M, V, K) -> int:
+    """Bytes of workspace cross_entropy_gemm takes for these sizes on the current device."""
+    return _query("cross_entropy_gemm_workspace_size", M, V, K)
+
+
+def cross_entropy_gemm_backward_workspace_size(M, V, K):
+    """(bytes cross_entropy_gemm_backward can use, bytes it needs at least) on the current device."""
+    return _query("cross_entropy_gemm_backward_workspace_size", M, V, K, results=2)
+
+
+def cross_entropy_gemm(X, W, target, ignore_index=-100, save=False, workspace=None):
+    """The softmax cross entropy of each row of X [M, K] against its target token, over the vocabulary's W [V, K] and
+    without the logits X W^T in memory: loss [M] float32 = log sum exp(X W^T) - (X W^T)[target].  Rows whose target is
+    ignore_index have loss 0 and take no part.  With save=True returns (loss, lse): lse [M] float32, which
+    cross_entropy_gemm_backward takes.  `workspace` (uint8) needs cross_entropy_gemm_workspace_size bytes; None
+    allocates them.
+
+    Differentiable in X and W; lse carries no graph."""
+    r = (_native or _binding()).cross_entropy_gemm(X, W, target, ignore_index, save, workspace)
+    if r is None:
+        r = _CrossEntropyGemm.apply(X, W, target, ignore_index, workspace)
+        return r if save else r[0]
+    return r
+
+
+def cross_entropy_gemm_backward(dL, X, W, target, lse, ignore_index=-100, workspace=None):
+    """The gradients (dX [M, K], dW [V, K], bfloat16) of cross_entropy_gemm for the incoming dL [M] float32, with lse as
+    cross_entropy_gemm(..., save=True) returned it.  `workspace` (uint8) needs the second of
+    cross_entropy_gemm_backward_workspace_size's values; None allocates the first.  Nothing is recorded: the results
+    carry no graph."""
+    return (_native or _binding()).cross_entropy_gemm_backward(dL, X, W, target, lse, ignore_index, True, True, workspace)

@@ -1,7 +1,8 @@
 /*
  * fp4g_lm.h -- C ABI of the operators that stand around a language model's products in
  * libfp4gemm.so for AMD Instinct MI355X (gfx950): the root-mean-square norm with its 8-bit
- * outputs and its backward pass.
+ * outputs and its backward pass, and the cross entropy over a vocabulary with its backward
+ * pass.
  *
  * Conventions are those of fp4gemm.h: plain device pointers owned by the caller, row-major
  * buffers without padding, calls asynchronous on `stream` (a hipStream_t; NULL is the
@@ -67,6 +68,38 @@ fp4g_status rms_norm_backward(int64_t rows, int64_t K, const void *dY, const voi
                               const void *W, int w_type, double eps, const void *dH,
                               void *dX, void *dW, void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/* The softmax cross entropy of bf16 X[M][K] against the vocabulary's bf16 W[V][K], a target
+ * token for each row, without the logits z = X W^T in memory:
+ *   lse[m] = log sum_v e^z[m][v],   loss[m] = lse[m] - z[m][target[m]],
+ * logits with fp32 sums, exponentials and their sums in fp32.  loss and lse are fp32 [M]; lse
+ * may be NULL.  Rows whose target is ignore_index take no part: their loss and lse are 0,
+ * their X is not looked at.  Any other target outside 0 .. V-1 gives a NaN loss.  target is
+ * int64 [M].  V >= 1 where M > 0 (FP4G_EINVAL); K a multiple of 8 and at most 2^21, M at most
+ * 2^25 (FP4G_EUNSUPPORTED).  X and W are 16-byte aligned, the others aligned to their elements
+ * (FP4G_EALIGN).  The workspace is required (fewer bytes than the query's are FP4G_EINVAL). */
+fp4g_status cross_entropy_gemm_workspace_size(int64_t M, int64_t V, int64_t K, size_t *bytes);
+fp4g_status cross_entropy_gemm(int64_t M, int64_t V, int64_t K, const void *X, const void *W,
+                               const int64_t *target, int64_t ignore_index,
+                               float *loss, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradients of cross_entropy_gemm from the incoming fp32 dL[M] and the lse it gave, both
+ * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once,
+ *   dX[M][K] = P W,   dW[V][K] = P^T X   with fp32 sums.
+ * P is formed for a piece of the vocabulary at a time, in the workspace: the query gives
+ * `bytes`, with which pieces are large enough to fill the GPU, and `least`, the least a call
+ * takes (fewer is FP4G_EINVAL).  Rows whose target is ignore_index have dX = 0 and give dW
+ * nothing, whatever their X and dL hold; a row with another target outside 0 .. V-1 makes its
+ * dX, and dW, NaN.  dX or dW may be NULL where it is not wanted: its product is left out.
+ * M == 0 zeroes dW. */
+fp4g_status cross_entropy_gemm_backward_workspace_size(int64_t M, int64_t V, int64_t K,
+                                                       size_t *bytes, size_t *least);
+fp4g_status cross_entropy_gemm_backward(int64_t M, int64_t V, int64_t K, const float *dL,
+                                        const void *X, const void *W, const int64_t *target,
+                                        int64_t ignore_index, const float *lse,
+                                        void *dX, void *dW,
+                                        void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

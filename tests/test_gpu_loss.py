@@ -1,0 +1,317 @@
+"""The cross entropy over a vocabulary and its gradients against their formulas in 64 bits.
+
+Tolerances.  u = 2^-24 and b = 2^-8 are the half steps of fp32 and bf16.
+  z     a sum of K products in fp32: off by at most (K + 8) u S, S the largest sum of the products' magnitudes in a row.
+  loss  two such logits; exponents of at most |z - max| in 2 roundings; a sum of V terms in chains of at most
+        V / 1024 + 80 additions; the logarithm and three more operations on numbers of the size of lse and z:
+        2 dz + (V / 1024 + 100 + 4 max|z - max|) u + 8 u (|max| + |loss| + |z|).
+  P     p = e^(z - lse) is off by p eta, eta = dz + dlse + 8 u (|z| + |lse| + 1), and P = (p - [wanted]) dL is rounded to
+        bf16; dX and dW are sums over it in fp32 and are rounded once more:
+        dX: (b + (V + 20) u) |P| |W| + eta (p |dL|) |W| + b |dX|, and dW with M, X for V, W.
+"""
+import pytest
+import torch
+
+import block_scaled_precision_e2m1_amd as fp4
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U, B = 2.0 ** -24, 2.0 ** -8
+SIZES = [(1, 1, 8), (3, 65, 72), (7, 130, 64), (1, 5000, 256), (130, 257, 136), (64, 1000, 512), (301, 1003, 520), (5, 4099, 2056),
+         (16, 40000, 64), (257, 4099, 264), (700, 2050, 1024), (2100, 12000, 200)]
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def inputs(m, v, k, seed, ignored=0.2, scale=1.0):
+    g = gen(seed)
+    w = (torch.randn(v, k, generator=g, device=DEV) * scale / max(k, 1) ** 0.5).bfloat16()
+    t = torch.randint(0, v, (m,), generator=g, device=DEV)
+    x = torch.randn(m, k, generator=g, device=DEV) + 6 * torch.rand(m, 1, generator=g, device=DEV) * w[t].float()
+    t[torch.rand(m, generator=g, device=DEV) < ignored] = -100
+    dl = (torch.rand(m, generator=g, device=DEV) + 0.5) / max(m, 1)
+    return x.bfloat16(), w, t, dl
+
+
+def formula(x, w, t, dl, ignore=-100):
+    """loss, lse, dX, dW in 64 bits with their tolerances; rows without a loss as if they were not there."""
+    m, v, k = x.shape[0], w.shape[0], x.shape[1]
+    some = t != ignore
+    xd = torch.where(some[:, None], x.double(), torch.zeros((), dtype=torch.float64, device=DEV))
+    wd = w.double()
+    z = xd @ wd.t()
+    lse = torch.logsumexp(z, 1)
+    zt = z.gather(1, t.clamp(min=0)[:, None])[:, 0]
+    top = z.amax(1)
+    size = (xd.abs() @ wd.abs().t()).amax(1)
+    dz = (k + 8) * U * size
+    span = (top - z.amin(1))
+    tol = 2 * dz + (v / 1024 + 100 + 4 * span) * U + 8 * U * (top.abs() + (lse - zt).abs() + zt.abs())
+    zero = torch.zeros_like(lse)
+    loss = torch.where(some, lse - zt, zero)
+    d = torch.where(some, dl.double(), zero)[:, None]
+    p = torch.exp(z - lse[:, None])
+    one = torch.zeros_like(p).scatter_(1, t.clamp(min=0)[:, None], 1.0)
+    P = (p - one) * d
+    eta = (dz + tol + 8 * U * (z.abs().amax(1) + lse.abs() + 1))[:, None]
+    near = p * d.abs() * eta
+    dx, dw = P @ wd, P.t() @ xd
+    tx = ((B + (v + 20) * U) * P.abs() + near) @ wd.abs() + (B + U) * dx.abs()
+    tw = ((B + (m + 20) * U) * P.abs() + near).t() @ xd.abs() + (B + U) * dw.abs()
+    return loss, torch.where(some, lse, zero), torch.where(some, tol, zero), dx, tx, dw, tw
+
+
+def close(got, want, tol, what):
+    err = (got.double() - want).abs()
+    bad = ~(err <= tol + 2.0 ** -133)
+    assert not bad.any(), f"{what}: {int(bad.sum())} values past their tolerance, the worst by {(err - tol).max().item():.3g}"
+
+
+def check(x, w, t, dl, workspace=None):
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse, workspace=workspace)
+    torch.cuda.synchronize(DEV)
+    rl, rs, tol, rx, tx, rw, tw = formula(x, w, t, dl)
+    close(loss, rl, tol, "loss")
+    close(lse, rs, tol, "lse")
+    close(dx, rx, tx, "dX")
+    close(dw, rw, tw, "dW")
+    assert not dx[t == -100].any() and not loss[t == -100].any()
+    return loss, lse, dx, dw
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.4])
+@pytest.mark.parametrize("m,v,k", SIZES)
+def test_sizes(m, v, k, ignored):
+    print(f"case cross_entropy_gemm {m}x{v}x{k} ignored {ignored}", flush=True)
+    check(*inputs(m, v, k, 1, ignored))
+
+
+@pytest.mark.parametrize("m,v,k", [(3, 200, 72), (130, 1003, 136), (700, 2050, 520), (33, 130, 2048)])
+def test_pieces_of_any_length(m, v, k):
+    """A workspace of the least size, and some between it and the largest: the same gradients within their tolerance."""
+    x, w, t, dl = inputs(m, v, k, 2)
+    most, least = fp4.cross_entropy_gemm_backward_workspace_size(m, v, k)
+    for size in sorted({least, (least + most) // 2, least + (most - least) // 5, most}):
+        print(f"case cross_entropy_gemm_backward {m}x{v}x{k} workspace {size} of {least}..{most}", flush=True)
+        check(x, w, t, dl, torch.full((size,), 255, dtype=torch.uint8, device=DEV))
+    with pytest.raises(fp4.Fp4GemmError):
+        fp4.cross_entropy_gemm_backward(dl, x, w, t, dl, workspace=torch.empty(least - 16, dtype=torch.uint8, device=DEV))
+    size = fp4.cross_entropy_gemm_workspace_size(m, v, k)
+    with pytest.raises(fp4.Fp4GemmError):
+        fp4.cross_entropy_gemm(x, w, t, workspace=torch.empty(size - 16, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("m,v,k", [(9, 300, 64), (300, 2000, 256), (5000, 130, 64)])
+def test_what_ignored_rows_hold_reaches_nothing(m, v, k):
+    x, w, t, dl = inputs(m, v, k, 3, 0.5)
+    t[0], t[m - 1] = -100, -100
+    want = check(x, w, t, dl)
+    none = t == -100
+    x, dl = x.clone(), dl.clone()
+    x[none] = torch.tensor([float("nan"), float("inf")], device=DEV).repeat(k // 2).bfloat16()
+    dl[none] = float("nan")
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    lse = torch.where(none, torch.full_like(lse, float("inf")), lse)
+    got = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    torch.cuda.synchronize(DEV)
+    assert torch.equal(loss, want[0]) and torch.equal(got[0], want[2]) and torch.equal(got[1], want[3])
+
+
+def test_no_row_takes_part():
+    x, w, t, dl = inputs(70, 500, 64, 4)
+    t[:] = 7
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, ignore_index=7, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse, ignore_index=7)
+    torch.cuda.synchronize(DEV)
+    assert not loss.any() and not lse.any() and not dx.any() and not dw.any()
+
+
+def test_one_row_takes_part_among_many():
+    """More than 4096 targets are counted in chunks; the last row, alone, is the first of the tiles."""
+    x, w, t, dl = inputs(9001, 700, 64, 5, 0.0)
+    keep = t[9000].clone()
+    t[:] = -100
+    t[9000] = keep
+    check(x, w, t, dl)
+
+
+def test_targets_outside_the_vocabulary():
+    x, w, t, dl = inputs(40, 300, 64, 6, 0.2)
+    for at, bad in ((3, 300), (4, -1), (5, 1 << 40), (6, -(1 << 33))):
+        t[at] = bad
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    torch.cuda.synchronize(DEV)
+    assert torch.isnan(loss[3:7]).all() and torch.isfinite(lse).all()
+    assert torch.isnan(dx[3:7]).all() and torch.isnan(dw).all()
+    rest = torch.ones(40, dtype=torch.bool, device=DEV)
+    rest[3:7] = False
+    assert torch.isfinite(loss[rest]).all() and torch.isfinite(dx[rest].float()).all()
+
+
+def test_infinities_stay_in_their_rows():
+    x, w, t, dl = inputs(66, 300, 64, 7, 0.0)
+    x[5, 3] = float("inf")
+    x[6, 1] = float("nan")
+    loss = fp4.cross_entropy_gemm(x, w, t)
+    torch.cuda.synchronize(DEV)
+    rest = torch.ones(66, dtype=torch.bool, device=DEV)
+    rest[5:7] = False
+    assert torch.isnan(loss[5:7]).all() and torch.isfinite(loss[rest]).all()
+
+
+def test_logits_of_minus_infinity():
+    """A token that is ruled out (its logit -infinity for every row) has probability 0; where the wanted one is, the loss is infinite."""
+    m, v, k = 20, 300, 64
+    x, w, t, dl = inputs(m, v, k, 8, 0.0)
+    x[:, 0] = 1
+    w[:, 0] = 0
+    w[200, 0] = float("-inf")
+    w[64:128, 0] = float("-inf")            # a whole wave's columns
+    t[:] = torch.arange(m, device=DEV)
+    t[3] = 200
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    torch.cuda.synchronize(DEV)
+    ref = torch.logsumexp(x.double() @ w.double().t(), 1)
+    assert loss[3] == float("inf") and torch.isfinite(loss[torch.arange(m, device=DEV) != 3]).all()
+    assert ((lse.double() - ref).abs() < 1e-4).all()
+
+
+def test_large_logits():
+    """Logits of some thousands: one token has all of the probability."""
+    x, w, t, dl = inputs(50, 700, 128, 9, 0.1, 300.0)
+    check(x, w, t, dl)
+
+
+def test_the_same_token_many_times():
+    x, w, t, dl = inputs(400, 260, 64, 10, 0.0)
+    t[:] = 259
+    check(x, w, t, dl)
+
+
+def test_gradients_agree_with_differences():
+    """The slope of sum(loss dL) along random directions, by central differences of the formula in 64 bits at 1e-4 (off by
+    about 1e-8 of its terms), against gradients whose P and results are rounded to bf16: by the sums of the tolerances."""
+    m, v, k = 12, 90, 48
+    x, w, t, dl = inputs(m, v, k, 11)
+    _, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    vx, vw = torch.randn(m, k, generator=gen(12), device=DEV).double(), torch.randn(v, k, generator=gen(13), device=DEV).double()
+    some = (t != -100).double() * dl.double()
+
+    def value(at):
+        z = (x.double() + at * vx) @ (w.double() + at * vw).t()
+        return ((torch.logsumexp(z, 1) - z.gather(1, t.clamp(min=0)[:, None])[:, 0]) * some).sum()
+
+    slope = (value(1e-4) - value(-1e-4)) / 2e-4
+    got = (dx.double() * vx).sum() + (dw.double() * vw).sum()
+    _, _, _, _, tx, _, tw = formula(x, w, t, dl)
+    assert (got - slope).abs() <= (tx * vx.abs()).sum() + (tw * vw.abs()).sum() + 1e-6
+    assert (got - slope).abs() <= 0.02 * slope.abs() + 1e-4
+
+
+def test_autograd_has_the_same_gradients():
+    x, w, t, dl = inputs(90, 500, 72, 14)
+    a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+    loss, lse = fp4.cross_entropy_gemm(a, b, t, save=True)
+    assert loss.requires_grad and not lse.requires_grad
+    loss.backward(dl)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    assert torch.equal(a.grad, dx) and torch.equal(b.grad, dw)
+    # the mean, whose gradient is one number for all rows; only one side wanted
+    n = (t != -100).sum()
+    a = x.clone().requires_grad_()
+    (fp4.cross_entropy_gemm(a, w, t).sum() / n).backward()
+    even = torch.full_like(dl, 1.0) / n
+    assert torch.equal(a.grad, fp4.cross_entropy_gemm_backward(even, x, w, t, lse)[0])
+    b = w.clone().requires_grad_()
+    (fp4.cross_entropy_gemm(x, b, t).sum() / n).backward()
+    assert torch.equal(b.grad, fp4.cross_entropy_gemm_backward(even, x, w, t, lse)[1])
+    with torch.no_grad():
+        assert not fp4.cross_entropy_gemm(a, w, t).requires_grad
+    (d,) = torch.autograd.grad(fp4.cross_entropy_gemm(a, w, t).sum(), a, create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivatives"):
+        d.float().sum().backward()
+
+
+def test_captured_calls_and_other_streams():
+    """Two graphs with workspaces of their own, replayed among other work; the number of rows that take part changes between replays."""
+    x, w, t, dl = inputs(300, 1003, 520, 15)
+    t2 = t.clone()
+    t2[:200] = -100
+    most, _ = fp4.cross_entropy_gemm_backward_workspace_size(300, 1003, 520)
+    live = t.clone()
+
+    def calls(space):
+        loss, lse = fp4.cross_entropy_gemm(x, w, live, save=True)
+        return (loss, lse, *fp4.cross_entropy_gemm_backward(dl, x, w, live, lse, workspace=space))
+
+    eager = {}
+    for name, target in (("some", t2), ("most", t)):
+        live.copy_(target)
+        eager[name] = [v.clone() for v in calls(None)]
+    side = torch.cuda.Stream(device=DEV)
+    side.wait_stream(torch.cuda.current_stream(DEV))
+    with torch.cuda.stream(side):
+        for got, want in zip(calls(None), eager["most"]):
+            assert torch.equal(got, want)
+    torch.cuda.synchronize(DEV)
+    graphs, held = [], []
+    for _ in range(2):
+        space = torch.full((most,), 255, dtype=torch.uint8, device=DEV)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(calls(space))
+    for rep in range(4):
+        name = ("some", "most")[rep % 2]
+        live.copy_((t2, t)[rep % 2])
+        for v in (*held[0], *held[1]):
+            v.fill_(1)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize(DEV)
+        for r in held:
+            for got, want in zip(r, eager[name]):
+                assert torch.equal(got, want), rep
+        fp4.cross_entropy_gemm(x, w, t)
+        torch.cuda.synchronize(DEV)
+
+
+def test_nothing_beyond_the_results():
+    """Rows behind the last, before the first: left as they were."""
+    m, v, k = 70, 333, 72
+    x, w, t, dl = inputs(m, v, k, 16)
+    lib, stream = fp4.lm._library(), torch.cuda.current_stream(DEV).cuda_stream
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    want = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    most, _ = fp4.cross_entropy_gemm_backward_workspace_size(m, v, k)
+    fwd = fp4.cross_entropy_gemm_workspace_size(m, v, k)
+    pads = [torch.full((n + 64,), 7, dtype=d, device=DEV) for n, d in
+            ((m, torch.float32), (m, torch.float32), (m * k, torch.bfloat16), (v * k, torch.bfloat16), (most, torch.uint8),
+             (fwd, torch.uint8))]
+    at = [p[32:].data_ptr() for p in pads]
+    assert lib.cross_entropy_gemm(m, v, k, x.data_ptr(), w.data_ptr(), t.data_ptr(), -100, at[0], at[1], at[5], fwd, stream) == 0
+    assert lib.cross_entropy_gemm_backward(m, v, k, dl.data_ptr(), x.data_ptr(), w.data_ptr(), t.data_ptr(), -100, at[1], at[2],
+                                           at[3], at[4], most, stream) == 0
+    torch.cuda.synchronize(DEV)
+    for p, r in zip(pads, (loss, lse, *want)):
+        assert torch.equal(p[32:32 + r.numel()], r.reshape(-1))
+    for p in pads:
+        assert (p[:32] == 7).all() and (p[-32:] == 7).all()
+
+
+def test_empty_sizes():
+    x, w, t, dl = inputs(0, 40, 64, 17)
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    assert loss.shape == (0,) and dx.shape == (0, 64) and not dw.any()
+    # no columns: every logit is 0
+    x, w, t, dl = inputs(5, 40, 0, 18, 0.0)
+    loss, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    torch.cuda.synchronize(DEV)
+    assert (loss.cpu() - torch.log(torch.tensor(40.0))).abs().max() < 1e-6
+    assert fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)[1].shape == (40, 0)

@@ -96,6 +96,55 @@ def test_norm_backward_refusals(lib):
     assert q(4, 100, BF16, ctypes.byref(n)) == OK and n.value >= 400
 
 
+def loss(lib, M=4, V=50, K=64, X=P[0], W=P[1], t=P[2], out=P[3], lse=P[4], w=P[5], wb=1 << 24):
+    return lib.cross_entropy_gemm(M, V, K, X, W, t, -100, out, lse, w, wb, None)
+
+
+def loss_grad(lib, M=4, V=50, K=64, dL=P[6], X=P[0], W=P[1], t=P[2], lse=P[4], dX=P[7], dW=P[8], w=P[5], wb=1 << 24):
+    return lib.cross_entropy_gemm_backward(M, V, K, dL, X, W, t, -100, lse, dX, dW, w, wb, None)
+
+
+@pytest.mark.parametrize("call", [loss, loss_grad])
+def test_loss_refusals(lib, call):
+    for name in ("M", "V", "K"):
+        assert call(lib, **{name: -1}) == EINVAL and call(lib, **{name: 1 << 31}) == EINVAL
+    assert call(lib, V=0) == EINVAL                      # rows, and no vocabulary
+    assert call(lib, K=12) == EUNSUP and call(lib, K=(1 << 21) + 8) == EUNSUP and call(lib, M=(1 << 25) + 1, V=8) == EUNSUP
+    assert call(lib, V=1 << 30, K=1 << 21) == EINVAL
+    for name in ("X", "W", "t", "w"):
+        assert call(lib, **{name: None}) == EINVAL
+    for name, base, by in (("X", P[0], 8), ("W", P[1], 8), ("t", P[2], 4), ("lse", P[4], 2), ("w", P[5], 8)):
+        assert call(lib, **{name: base + by}) == EALIGN
+    assert call(lib, wb=64) == EINVAL
+    assert call(lib, w=P[0] - 16, wb=(1 << 64) - 16) == EINVAL
+    assert call(lib, w=P[1]) == EINVAL
+
+
+def test_loss_results_are_checked(lib):
+    assert loss(lib, out=None) == EINVAL and loss(lib, out=P[3] + 1) == EALIGN
+    assert loss(lib, out=P[2]) == EINVAL and loss(lib, lse=P[3]) == EINVAL
+    assert loss(lib, M=0, X=None, t=None, out=None) == OK
+    assert loss_grad(lib, dL=None) == EINVAL and loss_grad(lib, lse=None) == EINVAL
+    assert loss_grad(lib, dX=P[7] + 8) == EALIGN and loss_grad(lib, dW=P[8] + 8) == EALIGN
+    assert loss_grad(lib, dX=P[0]) == EINVAL and loss_grad(lib, dW=P[1]) == EINVAL and loss_grad(lib, dW=P[7]) == EINVAL
+    assert loss_grad(lib, dX=None, dW=None) == OK        # nothing is wanted
+    assert loss_grad(lib, K=0) == OK
+
+
+def test_loss_workspace_queries(lib):
+    n, least = ctypes.c_size_t(7), ctypes.c_size_t(7)
+    f, b = lib.cross_entropy_gemm_workspace_size, lib.cross_entropy_gemm_backward_workspace_size
+    assert f(-1, 4, 64, ctypes.byref(n)) == EINVAL and f(4, 4, 20, ctypes.byref(n)) == EUNSUP and f(4, 4, 64, None) == EINVAL
+    assert b(4, 0, 64, ctypes.byref(n), ctypes.byref(least)) == EINVAL and b(4, 4, 64, ctypes.byref(n), None) == EINVAL
+    assert f(0, 4, 64, ctypes.byref(n)) == OK and n.value == 0
+    assert b(0, 4, 64, ctypes.byref(n), ctypes.byref(least)) == OK and n.value == 0 and least.value == 0
+    for m, v, k in ((1, 1, 8), (301, 1003, 520), (8192, 131072, 4096), (3, 1 << 30, 64), (1 << 25, 1000, 64)):
+        assert f(m, v, k, ctypes.byref(n)) == OK and n.value >= 2 * m * k
+        assert b(m, v, k, ctypes.byref(n), ctypes.byref(least)) == OK and 0 < least.value <= n.value
+    # a step of 8192 tokens over 131072: far less than its logits (4 GB in fp32)
+    assert b(8192, 131072, 4096, ctypes.byref(n), ctypes.byref(least)) == OK and n.value < 1 << 29
+
+
 def test_python_checks_come_before_the_library():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     for call in (fp4.rms_norm, fp4.rms_norm_quantize):
@@ -107,13 +156,19 @@ def test_python_checks_come_before_the_library():
             call(x.half())
     with pytest.raises(TypeError, match="dtype"):
         fp4.rms_norm_backward(x, x.half())
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="on a GPU"):
+        fp4.cross_entropy_gemm(x, x, t)
+    with pytest.raises(TypeError, match="dtype"):
+        fp4.cross_entropy_gemm(x.float(), x, t)
     with pytest.raises(TypeError):
         fp4.rms_norm_backward_workspace_size(4, 4, torch.float16)
 
 
 def test_binding_takes_every_argument_by_position():
     native = fp4.lm._binding()
-    for name, count in (("rms_norm", 6), ("rms_norm_quantize", 7), ("rms_norm_backward", 7)):
+    for name, count in (("rms_norm", 6), ("rms_norm_quantize", 7), ("rms_norm_backward", 7), ("cross_entropy_gemm", 6),
+                        ("cross_entropy_gemm_backward", 9)):
         f = getattr(native, name)
         with pytest.raises(TypeError, match="expected"):
             f(*[None] * (count - 1))
