@@ -217,8 +217,43 @@ PyObject* py_cross_entropy_gemm_backward(PyObject*, PyObject* const* v, Py_ssize
   });
 }
 
+// base, X, A, B, index, scales, out, workspace
+PyObject* py_adapter_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return entry(n, 8, [&] {
+    const at::Tensor& base = matrix(v[0], "base", at::kBFloat16, at::kFloat);
+    const int64_t M = base.size(0), N = base.size(1);
+    const at::Device device = base.device();
+    const c10::DeviceGuard guard(device);
+    const int64_t K = matrix(v[1], "X", at::kBFloat16, at::kBFloat16).size(1);
+    const at::Tensor& X = need(v[1], "X", at::kBFloat16, {M, K}, device);
+    const at::Tensor& first = tensor(v[2], "A");
+    if (first.dim() != 3) value_error("A must be 3-D");
+    const int64_t L = first.size(0), R = first.size(1);
+    const at::Tensor& A = need(v[2], "A", at::kBFloat16, {L, R, K}, device);
+    const at::Tensor& B = need(v[3], "B", at::kBFloat16, {L, N, R}, device);
+    const at::Tensor& index = need(v[4], "index", at::kInt, {M}, device);
+    at::Tensor scales;
+    if (v[5] != Py_None) scales = need(v[5], "scales", at::kFloat, {L}, device);
+    multiple_of(K, 8);
+    if (R % 8) value_error("R=" + std::to_string(R) + " must be a multiple of 8");
+    if (recorded({&base, &X, &A, &B, &scales})) value_error("adapter_gemm has no gradient: call it under torch.no_grad()");
+    const at::Tensor D = written(v[6], "out", base.scalar_type(), {M, N}, device);
+    const Space w = space(v[7], device, [&] {
+      size_t bytes = 0;
+      check_status("adapter_gemm_workspace_size", adapter_gemm_workspace_size(M, N, K, R, L, &bytes));
+      return bytes;
+    });
+    launch("adapter_gemm", device, [&](void* stream) {
+      return adapter_gemm(M, N, K, R, L, ptr(base), ptr(X), ptr(A), ptr(B), scales.defined() ? floats(scales) : nullptr,
+                          static_cast<const int32_t*>(ptr(index)), ptr(D),
+                          base.scalar_type() == at::kBFloat16 ? FP4G_OUT_BF16 : FP4G_OUT_F32, w.p, w.bytes, stream);
+    });
+    return THPVariable_Wrap(D);
+  });
+}
+
 PyMethodDef methods[] = {FASTCALL(rms_norm), FASTCALL(rms_norm_quantize), FASTCALL(rms_norm_backward),
-                         FASTCALL(cross_entropy_gemm), FASTCALL(cross_entropy_gemm_backward),
+                         FASTCALL(cross_entropy_gemm), FASTCALL(cross_entropy_gemm_backward), FASTCALL(adapter_gemm),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

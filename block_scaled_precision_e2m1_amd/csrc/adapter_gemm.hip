@@ -1,0 +1,443 @@
+// Low-rank adapters of many requests beside a shared projection, for gfx950:
+//   D[m] = base[m] + s_i B_i (A_i X[m]),  i = index[m];  A_i [R][K], B_i [N][R]
+//
+// HBM-bound: X and base are read and D written once, and the adapters that are used read once
+// where the tokens of each lie in one tile.  Two kernels, both on tiles of up to TM tokens of
+// ONE adapter:
+//
+//   * down   V = X A_i^T.  A wave multiplies 16-row fragments straight from memory (nothing is
+//     used twice but by the tokens of its tile) and the four waves of a workgroup, and S
+//     workgroups, share K; V's S partial sums are kept in fp32, 4 R bytes a token each.
+//   * up     D = base + V B_i^T.  V's sums are added, scaled and split into two bf16 terms
+//     (V = hi + lo to 2^-17 of each value), which both meet the same fragment of B, so that
+//     the second product loses nothing that fp32 results could show.  A lane ends up with 16
+//     consecutive columns of a token: base is read and D written as whole 16-byte vectors.
+//
+// The tokens of an adapter are found on the GPU.  Up to 256 tokens every workgroup finds its tile
+// by itself, in LDS, from the indexes; more are put in the adapters' order by one
+// workgroup first.  The order of a tile's tokens is of no consequence for any of them.
+// Tokens without an adapter form tiles too, which `up` copies where D is not base.
+#include <algorithm>
+
+#include "dense.hpp"
+#include "launch.hpp"
+#include "lm_internal.h"
+
+namespace fp4g {
+namespace {
+
+constexpr int kDirect = 256;      // tokens whose tiles need no order made beforehand
+constexpr int kRC = 64;           // rows of A_i that a workgroup of `down` takes
+
+struct Tile { int adapter, first, count, pad; };   // adapter -1: none
+
+struct Args {
+  int M, N, K, R, L, S;
+  const uint8_t *X, *A, *B;
+  const float* scales;
+  const int* index;
+  const void* base;
+  void* D;
+  float* V;               // [S][M][R]
+  const Tile* tiles;      // ordered tokens: [tiles]
+  const int* order;       // [M] tokens by adapter
+  const int* count;       // how many tiles there are
+  int steps;              // up: steps of 256 columns a workgroup takes
+};
+
+__device__ __forceinline__ int adapter_of(int i, int L) { return i >= 0 && i < L ? i : -1; }
+
+// The tile `t` of at most kDirect tokens: its adapter and count (0: there is no such tile), the
+// tokens in tok.  The tiles of an adapter hold its tokens in order, TM each; they are
+// numbered by their first token.
+struct alignas(16) FindSpace { int ids[kDirect], waves[4], lead[2], n; };
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const Args& a, int t, FindSpace& f, int* tok) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool there = tid < a.M;
+  const int id = there ? adapter_of(a.index[tid], a.L) : -2;
+  f.ids[tid] = id;
+  if (tid == 0) f.lead[0] = -2, f.n = 0;
+  __syncthreads();
+  int rank = 0;
+  for (int j = 0; j < tid; j += 4) {
+    const v4i o = *reinterpret_cast<const v4i*>(f.ids + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) rank += j + e < tid && o[e] == id;
+  }
+  const bool leads = there && rank % TM == 0;
+  const uint64_t mask = __ballot(leads);
+  if (lane == 0) f.waves[wave] = __popcll(mask);
+  __syncthreads();
+  int number = __popcll(mask & ((1ull << lane) - 1));
+  for (int w = 0; w < wave; ++w) number += f.waves[w];
+  if (leads && number == t) f.lead[0] = id, f.lead[1] = rank / TM;
+  __syncthreads();
+  const int adapter = f.lead[0];
+  if (there && id == adapter && rank / TM == f.lead[1]) {
+    tok[rank % TM] = tid;
+    atomicAdd(&f.n, 1);
+  }
+  __syncthreads();
+  return Tile{adapter, 0, f.n, 0};
+}
+template <int TM, bool DIRECT>
+__device__ __forceinline__ Tile tile_of(const Args& a, int t, FindSpace& f, int* tok) {
+  if constexpr (DIRECT) {
+    return find_tile<TM>(a, t, f, tok);
+  } else {
+    if (t >= *a.count) return Tile{-2, 0, 0, 0};
+    const Tile r = a.tiles[t];
+    if ((int)threadIdx.x < r.count) tok[threadIdx.x] = a.order[r.first + threadIdx.x];
+    __syncthreads();
+    return r;
+  }
+}
+
+// ---- down ----
+
+template <int TM, bool DIRECT>
+__global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
+  constexpr int FT = TM / 16, FR = kRC / 16;
+  __shared__ int tok[TM];
+  __shared__ FindSpace find;
+  __shared__ __attribute__((aligned(16))) float sums[4][TM][kRC + 4];
+  const int chunks = (a.R + kRC - 1) / kRC;
+  const int slice = blockIdx.x % a.S, rest = blockIdx.x / a.S, r0 = rest % chunks * kRC;
+  const Tile t = tile_of<TM, DIRECT>(a, rest / chunks, find, tok);
+  if (t.adapter < 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, slot = lane >> 4;
+  const int rows = min(a.R - r0, kRC), blocks = (rows + 15) / 16;
+  // Rows past the tile's tokens, or past R, repeat the last one: what they give is not kept.
+  const uint8_t* x[FT];
+#pragma unroll
+  for (int i = 0; i < FT; ++i) x[i] = a.X + (int64_t)tok[min(i * 16 + row, t.count - 1)] * a.K * 2;
+  const uint8_t* w[FR];
+#pragma unroll
+  for (int j = 0; j < FR; ++j)
+    w[j] = a.A + ((int64_t)t.adapter * a.R + r0 + min(j * 16 + row, rows - 1)) * a.K * 2;
+  v4f acc[FT][FR] = {};
+  const int units = (a.K + 63) / 64;
+  const int begin = (int)((int64_t)units * slice / a.S), end = (int)((int64_t)units * (slice + 1) / a.S);
+  // A unit is a line of 128 bytes of every row: slot h of an instruction takes chunk h, then h + 4.
+  for (int u = begin + wave; u < end; u += 4) {
+    v4i fx[2][FT], fw[2][FR];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = u * 64 + (h * 4 + slot) * 8;
+      const bool in = k < a.K;
+#pragma unroll
+      for (int i = 0; i < FT; ++i) fx[h][i] = in ? *reinterpret_cast<const v4i*>(x[i] + k * 2) : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+        fw[h][j] = in && j < blocks ? *reinterpret_cast<const v4i*>(w[j] + k * 2) : v4i{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+        if (j < blocks)
+#pragma unroll
+          for (int i = 0; i < FT; ++i) acc[i][j] = mfma16(fw[h][j], fx[h][i], acc[i][j]);
+  }
+  // A lane holds rows 4 slot .. + 3 of each block of A_i for token `row` of each 16.
+#pragma unroll
+  for (int i = 0; i < FT; ++i)
+#pragma unroll
+    for (int j = 0; j < FR; ++j) *reinterpret_cast<v4f*>(&sums[wave][i * 16 + row][j * 16 + 4 * slot]) = acc[i][j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < TM * kRC / 4; e += 256) {
+    const int m = e / (kRC / 4), r = e % (kRC / 4) * 4;
+    if (m >= t.count || r >= rows) continue;
+    v4f v = *reinterpret_cast<const v4f*>(&sums[0][m][r]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const v4f*>(&sums[k][m][r]);
+    *reinterpret_cast<v4f*>(a.V + ((int64_t)slice * a.M + tok[m]) * a.R + r0 + r) = v;
+  }
+}
+
+// ---- up ----
+
+// 16 consecutive columns of a row, of which the first `left` exist.
+template <bool BF16>
+__device__ __forceinline__ void load_cols(const void* base, int64_t at, int left, float (&y)[16]) {
+  if constexpr (BF16) {
+    typedef v4i v4i_any __attribute__((aligned(2)));
+    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
+    if (left >= 16) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const v4i v = *reinterpret_cast<const v4i_any*>(p + 8 * q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = (uint32_t)v[e / 2];
+          y[8 * q + e] = __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = e < left ? __builtin_bit_cast(float, (uint32_t)p[e] << 16) : 0.0f;
+    }
+  } else {
+    typedef v4f v4f_any __attribute__((aligned(4)));
+    const float* p = static_cast<const float*>(base) + at;
+    if (left >= 16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const v4f v = *reinterpret_cast<const v4f_any*>(p + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[4 * q + e] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = e < left ? p[e] : 0.0f;
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_16(void* D, int64_t at, int left, const float (&y)[16]) {
+  constexpr int V = BF16 ? 8 : 4;
+#pragma unroll
+  for (int q = 0; q < 16; q += V) {
+    float t[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] = y[q + e];
+    if (left > q) store_cols<BF16>(D, at + q, left - q, t);
+  }
+}
+
+template <int TM, int RMAX, bool DIRECT, bool BF16>
+__global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int shares) {
+  constexpr int FT = TM / 16;
+  __shared__ int tok[TM];
+  __shared__ FindSpace find;
+  constexpr int pitch = RMAX * 2 + 16;
+  __shared__ __attribute__((aligned(16))) uint8_t terms[2 * TM * pitch];   // hi, lo
+  const int share = blockIdx.x % shares;
+  const Tile t = tile_of<TM, DIRECT>(a, blockIdx.x / shares, find, tok);
+  if (t.count == 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, slot = lane >> 4;
+  const int first = share * a.steps * 256;
+  if (t.adapter < 0) {
+    if (a.D == a.base) return;
+    for (int s = 0; s < a.steps; ++s) {
+      const int n = first + s * 256 + (threadIdx.x & 15) * 16;
+      if (n >= a.N) break;
+      for (int m = threadIdx.x >> 4; m < t.count; m += 16) {
+        float y[16];
+        const int64_t at = (int64_t)tok[m] * a.N + n;
+        load_cols<BF16>(a.base, at, a.N - n, y);
+        store_16<BF16>(a.D, at, a.N - n, y);
+      }
+    }
+    return;
+  }
+  // V's sums as two bf16 terms, zeros past R and past the tile's tokens.
+  const int RP = (a.R + 31) / 32 * 32;
+  const float scale = a.scales ? a.scales[t.adapter] : 1.0f;
+  for (int e = threadIdx.x; e < TM * (RP / 4); e += 256) {
+    const int m = e / (RP / 4), r = (e - m * (RP / 4)) * 4;
+    v4f v{0.0f, 0.0f, 0.0f, 0.0f};
+    if (m < t.count && r < a.R) {
+      const float* p = a.V + (int64_t)tok[m] * a.R + r;
+      v = *reinterpret_cast<const v4f*>(p);
+      for (int s = 1; s < a.S; ++s) v += *reinterpret_cast<const v4f*>(p + (int64_t)s * a.M * a.R);
+    }
+    float lo[4];
+    uint32_t hi2[2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] *= scale;
+    hi2[0] = pack_bf16x2(v[0], v[1]), hi2[1] = pack_bf16x2(v[2], v[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      lo[k] = v[k] - __builtin_bit_cast(float, k & 1 ? hi2[k / 2] & 0xffff0000u : hi2[k / 2] << 16);
+    // An infinity or NaN is in hi alone.
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(__builtin_fabsf(lo[k]) < __builtin_inff())) lo[k] = 0.0f;
+    *reinterpret_cast<v2i*>(terms + m * pitch + r * 2) = v2i{(int)hi2[0], (int)hi2[1]};
+    *reinterpret_cast<v2i*>(terms + (TM + m) * pitch + r * 2) = v2i{(int)pack_bf16x2(lo[0], lo[1]), (int)pack_bf16x2(lo[2], lo[3])};
+  }
+  __syncthreads();
+  const int tiles16 = (t.count + 15) / 16;
+  const uint8_t* B = a.B + (int64_t)t.adapter * a.N * a.R * 2;
+  for (int s = 0; s < a.steps; ++s) {
+    // Row 4 g + e of block b is column n0 + 16 g + 4 b + e: a lane (slot g) has 16 columns in a row.
+    const int n0 = first + s * 256 + wave * 64, mine = n0 + slot * 16;
+    if (n0 >= a.N) break;
+    v4f acc[FT][4] = {};
+    for (int kb = 0; kb < RP; kb += 32) {
+      const int k = kb + slot * 8;
+      v4i fb[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int n = n0 + (row >> 2) * 16 + 4 * b + (row & 3);
+        fb[b] = k < a.R && n < a.N ? *reinterpret_cast<const v4i*>(B + ((int64_t)n * a.R + k) * 2) : v4i{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+        if (i < tiles16) {
+          const uint8_t* p = terms + (i * 16 + row) * pitch + k * 2;
+          const v4i hi = *reinterpret_cast<const v4i*>(p), lo = *reinterpret_cast<const v4i*>(p + TM * pitch);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[i][b] = mfma16(fb[b], hi, acc[i][b]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) acc[i][b] = mfma16(fb[b], lo, acc[i][b]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < FT; ++i) {
+      if (i * 16 + row < t.count && mine < a.N) {
+        const int64_t at = (int64_t)tok[i * 16 + row] * a.N + mine;
+        float y[16];
+        load_cols<BF16>(a.base, at, a.N - mine, y);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] += acc[i][e / 4][e % 4];
+        store_16<BF16>(a.D, at, a.N - mine, y);
+      }
+    }
+  }
+}
+
+// ---- the tokens in the adapters' order ----
+
+constexpr int kOrderThreads = 1024;
+// The last of the L + 1 buckets is for tokens without an adapter.
+template <int TM>
+__global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(int M, int L, const int* __restrict__ index,
+                                                                      int* __restrict__ rank, int* __restrict__ order,
+                                                                      Tile* __restrict__ tiles, int* __restrict__ count) {
+  __shared__ int counts[kMaxAdapters + 1];
+  __shared__ int2 waves[kOrderThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, buckets = L + 1;
+  for (int b = tid; b < buckets; b += kOrderThreads) counts[b] = 0;
+  __syncthreads();
+  for (int64_t m0 = 0; m0 < M; m0 += kOrderThreads) {
+    const int64_t m = m0 + tid;
+    const int id = m < M ? adapter_of(index[m], L) : -2, bucket = id < 0 ? L : id;
+    bool left = id != -2;
+    int at = 0;
+    // Neighbours mostly share an adapter: two of a wave's adapters are counted at once, the
+    // others one by one.
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+      const uint64_t open = __ballot(left);
+      if (open == 0) break;
+      const int leader = __ffsll((unsigned long long)open) - 1, its = __shfl(bucket, leader);
+      const uint64_t same = __ballot(left && bucket == its);
+      int old = 0;
+      if (lane == leader) old = atomicAdd(&counts[its], __popcll(same));
+      old = __shfl(old, leader);
+      if (left && bucket == its) {
+        at = old + __popcll(same & ((1ull << lane) - 1));
+        left = false;
+      }
+    }
+    if (left) at = atomicAdd(&counts[bucket], 1);
+    if (m < M) rank[m] = at;
+  }
+  __syncthreads();
+  // Where each bucket's tokens and tiles start: a run of buckets a thread.
+  const int per = (buckets + kOrderThreads - 1) / kOrderThreads, b0 = min(tid * per, buckets), b1 = min(b0 + per, buckets);
+  int2 mine = make_int2(0, 0);
+  for (int b = b0; b < b1; ++b) mine.x += counts[b], mine.y += (counts[b] + TM - 1) / TM;
+  int2 upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(upto.x, d), y = __shfl_up(upto.y, d);
+    if (lane >= d) upto.x += x, upto.y += y;
+  }
+  if (lane == 63) waves[wave] = upto;
+  __syncthreads();
+  int2 start = make_int2(upto.x - mine.x, upto.y - mine.y);
+  for (int w = 0; w < wave; ++w) start.x += waves[w].x, start.y += waves[w].y;
+  for (int b = b0; b < b1; ++b) {
+    const int n = counts[b];
+    counts[b] = start.x;
+    for (int i = 0; i < n; i += TM) tiles[start.y++] = Tile{b < L ? b : -1, start.x + i, min(n - i, TM), 0};
+    start.x += n;
+  }
+  if (tid == kOrderThreads - 1) *count = start.y;
+  __syncthreads();
+  for (int64_t m = tid; m < M; m += kOrderThreads) {
+    const int id = adapter_of(index[m], L);
+    order[counts[id < 0 ? L : id] + rank[m]] = (int)m;
+  }
+}
+
+// How a call is cut up: tokens a tile, tiles at most, K slices, columns' shares.
+struct Plan {
+  bool direct;
+  int tm;
+  int64_t tiles, S;
+};
+Plan plan_of(int64_t M, int64_t K, int64_t R, int64_t L) {
+  Plan p;
+  p.direct = M <= kDirect;
+  p.tm = p.direct ? 16 : 64;
+  p.tiles = std::min(M, ceil_div(M, p.tm) + L);   // an adapter's last tile may be short; so may that of none
+  // Two units of 128 bytes of K a wave at least, and workgroups for the chip.
+  const int64_t units = ceil_div(K, 64), work = p.tiles * std::max<int64_t>(1, ceil_div(R, kRC));
+  p.S = std::max<int64_t>(1, std::min({units / 8, 4 * device_cus() / work, (int64_t)(p.direct ? 16 : 4)}));
+  return p;
+}
+
+struct Space {
+  uint8_t* p;
+  int64_t used = 0;
+  template <class T>
+  T* take(int64_t count) {
+    T* r = reinterpret_cast<T*>(p + used);
+    used += (count * (int64_t)sizeof(T) + 255) / 256 * 256;
+    return r;
+  }
+};
+struct AdapterSpace {
+  Space s;
+  float* V;
+  int *rank, *order, *count;
+  Tile* tiles;
+  AdapterSpace(uint8_t* p, int64_t M, int64_t R, const Plan& plan)
+      : s{p}, V(s.take<float>(plan.S * M * R)), rank(s.take<int>(plan.direct ? 0 : M)),
+        order(s.take<int>(plan.direct ? 0 : M)), count(s.take<int>(1)), tiles(s.take<Tile>(plan.direct ? 0 : plan.tiles)) {}
+};
+
+template <int TM, bool DIRECT, bool BF16>
+hipError_t launch_up(int64_t grid, hipStream_t s, const Args& a, int shares) {
+  if (a.R <= 64) return launch(adapter_up_kernel<TM, 64, DIRECT, BF16>, grid, 256, s, a, shares);
+  if (a.R <= 128) return launch(adapter_up_kernel<TM, 128, DIRECT, BF16>, grid, 256, s, a, shares);
+  return launch(adapter_up_kernel<TM, 256, DIRECT, BF16>, grid, 256, s, a, shares);
+}
+
+}  // namespace
+
+int64_t adapter_bytes(int64_t M, int64_t K, int64_t R, int64_t L) {
+  return AdapterSpace(nullptr, M, R, plan_of(M, K, R, L)).s.used;
+}
+
+hipError_t launch_adapter_gemm(const AdapterCall& c, hipStream_t s) {
+  // Without adapters, rows of them or columns every token is one without.
+  const int64_t L = c.K > 0 && c.R > 0 ? c.L : 0;
+  if (L == 0 && c.D == c.base) return hipSuccess;
+  const Plan p = plan_of(c.M, c.K, c.R, c.L);
+  const AdapterSpace w(c.space, c.M, c.R, p);
+  Args a{(int)c.M, (int)c.N, (int)c.K, (int)c.R, (int)L, (int)p.S, static_cast<const uint8_t*>(c.X),
+         static_cast<const uint8_t*>(c.A), static_cast<const uint8_t*>(c.B), c.scales, c.index, c.base, c.D, w.V,
+         w.tiles, w.order, w.count, 1};
+  hipError_t e = hipSuccess;
+  if (!p.direct)
+    e = launch(adapter_order_kernel<64>, 1, kOrderThreads, s, a.M, a.L, c.index, w.rank, w.order, w.tiles, w.count);
+  if (e == hipSuccess && L > 0)
+    e = launch(p.direct ? adapter_down_kernel<16, true> : adapter_down_kernel<64, false>,
+               p.tiles * ceil_div(c.R, kRC) * p.S, 256, s, a);
+  if (e != hipSuccess) return e;
+  const int64_t steps = ceil_div(c.N, 256), most = std::min(steps, ceil_div(4 * device_cus(), p.tiles));
+  a.steps = (int)ceil_div(steps, most);
+  const int shares = (int)ceil_div(steps, a.steps);
+  if (p.direct) return c.bf16 ? launch_up<16, true, true>(p.tiles * shares, s, a, shares)
+                              : launch_up<16, true, false>(p.tiles * shares, s, a, shares);
+  return c.bf16 ? launch_up<64, false, true>(p.tiles * shares, s, a, shares)
+                : launch_up<64, false, false>(p.tiles * shares, s, a, shares);
+}
+
+}  // namespace fp4g

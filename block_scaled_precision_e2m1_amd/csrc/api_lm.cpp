@@ -77,6 +77,13 @@ int64_t piece_cols(int64_t M, int64_t V, int64_t K, size_t room) {
   }
 }
 
+fp4g_status check_adapter_sizes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  if (!sizes_fit({M, N, K, R, L}) || !holds(M, N) || !holds(M, K) || !holds(L, R, K) || !holds(L, N, R)) return FP4G_EINVAL;
+  return K % 8 != 0 || R % 8 != 0 || R > 256 || K > (1 << 21) || L > fp4g::kMaxAdapters || M > (1 << 25) || N > (1 << 30)
+             ? FP4G_EUNSUPPORTED
+             : FP4G_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -181,6 +188,34 @@ fp4g_status cross_entropy_gemm_backward(int64_t M, int64_t V, int64_t K, const f
   c.lse = const_cast<float*>(lse), c.dL = dL, c.dX = dX, c.dW = dW;
   c.space = static_cast<uint8_t*>(workspace), c.cols = cols;
   return finish(fp4g::launch_loss_grad(c, s));
+}
+
+fp4g_status adapter_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, size_t* bytes) {
+  const fp4g_status st = check_adapter_sizes(M, N, K, R, L);
+  if (st != FP4G_OK) return st;
+  if (!bytes) return FP4G_EINVAL;
+  *bytes = M == 0 || N == 0 ? 0 : (size_t)fp4g::adapter_bytes(M, K, R, L);
+  return FP4G_OK;
+}
+
+fp4g_status adapter_gemm(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, const void* base, const void* X,
+                         const void* A, const void* B, const float* scales, const int32_t* index, void* D, int d_type,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  fp4g_status st = check_adapter_sizes(M, N, K, R, L);
+  if (st != FP4G_OK) return st;
+  if (d_type != FP4G_OUT_F32 && d_type != FP4G_OUT_BF16) return FP4G_EINVAL;
+  if (M == 0 || N == 0) return FP4G_OK;
+  const int64_t e = d_type == FP4G_OUT_BF16 ? 2 : 4;
+  const Buffer b = buf(base, M * N * e, e);
+  const Buffer x = buf(X, M * K * 2), wa = buf(A, L * R * K * 2), wb = buf(B, L * N * R * 2);
+  const Buffer s = buf(scales, scales ? L * 4 : 0, 4), i = buf(index, M * 4, 4);
+  st = check_buffers({b, x, wa, wb, s, i}, {});
+  if (st != FP4G_OK) return st;
+  st = check_buffers({unless(b, {D}), x, wa, wb, s, i}, {buf(D, M * N * e, e), buf(workspace, workspace_bytes)});
+  if (st != FP4G_OK) return st;
+  if (workspace_bytes < (size_t)fp4g::adapter_bytes(M, K, R, L)) return FP4G_EINVAL;
+  const fp4g::AdapterCall c{M, N, K, R, L, base, X, A, B, scales, index, D, e == 2, static_cast<uint8_t*>(workspace)};
+  return finish(fp4g::launch_adapter_gemm(c, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -58,4 +58,17 @@ int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K);
 hipError_t launch_loss(const LossCall& a, hipStream_t s);
 hipError_t launch_loss_grad(const LossCall& a, hipStream_t s);
 
+struct AdapterCall {
+  int64_t M, N, K, R, L;          // M, N > 0; K and R multiples of 8, R <= 256, L <= kMaxAdapters
+  const void *base, *X, *A, *B;
+  const float* scales;            // null: 1
+  const int* index;
+  void* D;
+  bool bf16;                      // the type of base and D
+  uint8_t* space;
+};
+constexpr int64_t kMaxAdapters = 8192;   // counted in a workgroup's LDS
+int64_t adapter_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
+hipError_t launch_adapter_gemm(const AdapterCall& c, hipStream_t s);
+
 }  // namespace fp4g

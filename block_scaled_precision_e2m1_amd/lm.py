@@ -1,5 +1,5 @@
 """Operators around a language model's products: the norm before them, in their types or in 8 bits, and the loss over
-the vocabulary behind them, with their gradients.
+the vocabulary behind them, with their gradients; and the adapters of many requests beside one.
 
 A binding over the C ABI of ``include/fp4g_lm.h`` in the manner of the package's other
 functions: each has the name of its C entry point, checks its torch arguments, runs on the
@@ -12,7 +12,9 @@ Layouts (contiguous, all on one GPU):
   rms_norm_backward  : the gradients of rms_norm
   cross_entropy_gemm           : X [M, K], W [V, K] bfloat16, target [M] int64 -> loss [M] float32
   cross_entropy_gemm_backward  : the gradients of cross_entropy_gemm, bfloat16
-K of the loss is a multiple of 8.  rms_norm and cross_entropy_gemm take part in autograd; the results of the other
+  adapter_gemm       : base [M, N] float32 or bfloat16, X [M, K], A [L, R, K], B [L, N, R] bfloat16, index [M] int32
+                       -> D like base
+K of the loss and K and R of the adapters are multiples of 8.  rms_norm and cross_entropy_gemm take part in autograd; the results of the other
 functions carry no graph.
 """
 from __future__ import annotations
@@ -27,7 +29,7 @@ import block_scaled_precision_e2m1_amd as _base
 
 LM_SYMBOLS = ("rms_norm", "rms_norm_quantize", "rms_norm_backward_workspace_size", "rms_norm_backward",
               "cross_entropy_gemm_workspace_size", "cross_entropy_gemm", "cross_entropy_gemm_backward_workspace_size",
-              "cross_entropy_gemm_backward")
+              "cross_entropy_gemm_backward", "adapter_gemm_workspace_size", "adapter_gemm")
 
 __all__ = [*LM_SYMBOLS, "LM_SYMBOLS"]
 
@@ -46,6 +48,8 @@ def _library():
         "cross_entropy_gemm": [i64, i64, i64, p, p, p, i64, p, p, p, size, p],
         "cross_entropy_gemm_backward_workspace_size": [i64, i64, i64, psize, psize],
         "cross_entropy_gemm_backward": [i64, i64, i64, p, p, p, p, i64, p, p, p, p, size, p],
+        "adapter_gemm_workspace_size": [i64, i64, i64, i64, i64, psize],
+        "adapter_gemm": [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, c_int, p, size, p],
     }
     for name, a in args.items():
         fn = getattr(lib, name)
@@ -209,3 +213,17 @@ def cross_entropy_gemm_backward(dL, X, W, target, lse, ignore_index=-100, worksp
     cross_entropy_gemm_backward_workspace_size's values; None allocates the first.  Nothing is recorded: the results
     carry no graph."""
     return (_native or _binding()).cross_entropy_gemm_backward(dL, X, W, target, lse, ignore_index, True, True, workspace)
+
+
+def adapter_gemm_workspace_size(M, N, K, R, L) -> int:
+    """Bytes of workspace adapter_gemm takes for these sizes on the current device."""
+    return _query("adapter_gemm_workspace_size", M, N, K, R, L)
+
+
+def adapter_gemm(base, X, A, B, index, scales=None, out=None, workspace=None):
+    """Low-rank adapters of many requests beside a projection that they share and that has given `base` [M, N] (of any of
+    the package's products): D[m] = base[m] + scales[i] * B[i] (A[i] X[m]) with i = index[m], for A [L, R, K], B [L, N, R]
+    and scales [L] float32 (None: 1).  A row whose index is outside 0 .. L-1 (-1, say) keeps its base.  Adapters of
+    a lower rank than R are filled up with zeros.  `out` may be base itself.  `workspace` (uint8) needs
+    adapter_gemm_workspace_size bytes; None allocates them.  Not differentiable."""
+    return (_native or _binding()).adapter_gemm(base, X, A, B, index, scales, out, workspace)

@@ -1,8 +1,8 @@
 /*
  * fp4g_lm.h -- C ABI of the operators that stand around a language model's products in
  * libfp4gemm.so for AMD Instinct MI355X (gfx950): the root-mean-square norm with its 8-bit
- * outputs and its backward pass, and the cross entropy over a vocabulary with its backward
- * pass.
+ * outputs and its backward pass, the cross entropy over a vocabulary with its backward pass,
+ * and low-rank adapters beside a shared projection.
  *
  * Conventions are those of fp4gemm.h: plain device pointers owned by the caller, row-major
  * buffers without padding, calls asynchronous on `stream` (a hipStream_t; NULL is the
@@ -100,6 +100,24 @@ fp4g_status cross_entropy_gemm_backward(int64_t M, int64_t V, int64_t K, const f
                                         int64_t ignore_index, const float *lse,
                                         void *dX, void *dW,
                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Low-rank adapters of many requests, beside a projection that they share and that has given
+ * base[M][N]: with i = index[m],
+ *   D[m] = base[m] + scales[i] * B[i] (A[i] X[m])
+ * for bf16 X[M][K], A[L][R][K], B[L][N][R] and fp32 scales[L] (NULL: 1).  Sums and the R
+ * values between the products are fp32 (these enter the second product as two bf16 terms,
+ * which keep 16 bits of each); base and D are fp32 or bf16 by d_type, rounded once.  A row
+ * whose index is outside 0 .. L-1 has no adapter: D[m] = base[m], and its X is not looked at.
+ * D may be base itself.  K and R are multiples of 8, R at most 256, K at most 2^21, L at most
+ * 8192, M at most 2^25, N at most 2^30 (FP4G_EUNSUPPORTED).  X, A and B are 16-byte aligned,
+ * the others aligned to their elements (FP4G_EALIGN).  The workspace is required (fewer
+ * bytes than the query's are FP4G_EINVAL). */
+fp4g_status adapter_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                                        size_t *bytes);
+fp4g_status adapter_gemm(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                         const void *base, const void *X, const void *A, const void *B,
+                         const float *scales, const int32_t *index, void *D, int d_type,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

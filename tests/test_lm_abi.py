@@ -145,6 +145,36 @@ def test_loss_workspace_queries(lib):
     assert b(8192, 131072, 4096, ctypes.byref(n), ctypes.byref(least)) == OK and n.value < 1 << 29
 
 
+def adapters(lib, M=4, N=40, K=64, R=16, L=3, base=P[0], X=P[1], A=P[2], B=P[3], s=P[4], i=P[5], D=P[6], t=BF16, w=P[7],
+             wb=1 << 20):
+    return lib.adapter_gemm(M, N, K, R, L, base, X, A, B, s, i, D, t, w, wb, None)
+
+
+def test_adapter_refusals(lib):
+    for name in ("M", "N", "K", "R", "L"):
+        assert adapters(lib, **{name: -1}) == EINVAL and adapters(lib, **{name: 1 << 31}) == EINVAL
+    assert adapters(lib, K=12) == EUNSUP and adapters(lib, R=12) == EUNSUP and adapters(lib, R=264) == EUNSUP
+    assert adapters(lib, L=8193) == EUNSUP and adapters(lib, K=(1 << 21) + 8) == EUNSUP
+    assert adapters(lib, M=(1 << 25) + 1) == EUNSUP and adapters(lib, N=(1 << 30) + 1) == EUNSUP
+    assert adapters(lib, N=1 << 30, R=256, L=8192) == EINVAL               # more than 2^50 elements
+    assert adapters(lib, t=2) == EINVAL
+    for name in ("base", "X", "A", "B", "i", "D", "w"):
+        assert adapters(lib, **{name: None}) == EINVAL
+    for name, at, by in (("base", P[0], 1), ("X", P[1], 8), ("A", P[2], 8), ("B", P[3], 8), ("s", P[4], 2), ("i", P[5], 2),
+                         ("D", P[6], 1), ("w", P[7], 8)):
+        assert adapters(lib, **{name: at + by}) == EALIGN
+    assert adapters(lib, D=P[0] + 64) == EINVAL and adapters(lib, D=P[1]) == EINVAL and adapters(lib, D=P[3]) == EINVAL
+    assert adapters(lib, w=P[0]) == EINVAL and adapters(lib, w=P[6]) == EINVAL
+    assert adapters(lib, wb=64) == EINVAL and adapters(lib, w=P[0] - 16, wb=(1 << 64) - 16) == EINVAL
+    assert adapters(lib, M=0, base=None, X=None, i=None, D=None) == OK and adapters(lib, N=0, base=None, B=None, D=None) == OK
+    n = ctypes.c_size_t(7)
+    q = lib.adapter_gemm_workspace_size
+    assert q(-1, 4, 64, 8, 1, ctypes.byref(n)) == EINVAL and q(4, 4, 20, 8, 1, ctypes.byref(n)) == EUNSUP
+    assert q(4, 4, 64, 8, 1, None) == EINVAL
+    assert q(0, 4, 64, 8, 1, ctypes.byref(n)) == OK and n.value == 0
+    assert q(4, 4, 64, 8, 1, ctypes.byref(n)) == OK and n.value >= 4 * 8 * 4
+
+
 def test_python_checks_come_before_the_library():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     for call in (fp4.rms_norm, fp4.rms_norm_quantize):
@@ -161,6 +191,8 @@ def test_python_checks_come_before_the_library():
         fp4.cross_entropy_gemm(x, x, t)
     with pytest.raises(TypeError, match="dtype"):
         fp4.cross_entropy_gemm(x.float(), x, t)
+    with pytest.raises(ValueError, match="on a GPU"):
+        fp4.adapter_gemm(x, x, x, x, t)
     with pytest.raises(TypeError):
         fp4.rms_norm_backward_workspace_size(4, 4, torch.float16)
 
@@ -168,7 +200,7 @@ def test_python_checks_come_before_the_library():
 def test_binding_takes_every_argument_by_position():
     native = fp4.lm._binding()
     for name, count in (("rms_norm", 6), ("rms_norm_quantize", 7), ("rms_norm_backward", 7), ("cross_entropy_gemm", 6),
-                        ("cross_entropy_gemm_backward", 9)):
+                        ("cross_entropy_gemm_backward", 9), ("adapter_gemm", 8)):
         f = getattr(native, name)
         with pytest.raises(TypeError, match="expected"):
             f(*[None] * (count - 1))
