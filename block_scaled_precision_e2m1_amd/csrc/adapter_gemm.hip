@@ -10,8 +10,9 @@
 //     workgroups, share K; V's S partial sums are kept in fp32, 4 R bytes a token each.
 //   * up     D = base + V B_i^T.  V's sums are added, scaled and split into two bf16 terms
 //     (V = hi + lo to 2^-17 of each value), which both meet the same fragment of B, so that
-//     the second product loses nothing that fp32 results could show.  A lane ends up with 16
-//     consecutive columns of a token: base is read and D written as whole 16-byte vectors.
+//     the second product loses nothing that fp32 results could show.  B's rows are dealt to
+//     the instruction's so that a lane ends up with whole 16-byte vectors of a token's columns,
+//     and the four lanes of a token with 64 bytes side by side.
 //
 // The tokens of an adapter are found on the GPU.  Up to 256 tokens every workgroup finds its tile
 // by itself, in LDS, from the indexes; more are put in the adapters' order by one
@@ -60,10 +61,13 @@ __device__ __forceinline__ Tile find_tile(const Args& a, int t, FindSpace& f, in
   if (tid == 0) f.lead[0] = -2, f.n = 0;
   __syncthreads();
   int rank = 0;
-  for (int j = 0; j < tid; j += 4) {
-    const v4i o = *reinterpret_cast<const v4i*>(f.ids + j);
+  if (there) {
+#pragma unroll 8
+    for (int j = 0; j < tid; j += 4) {
+      const v4i o = *reinterpret_cast<const v4i*>(f.ids + j);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) rank += j + e < tid && o[e] == id;
+      for (int e = 0; e < 4; ++e) rank += j + e < tid && o[e] == id;
+    }
   }
   const bool leads = there && rank % TM == 0;
   const uint64_t mask = __ballot(leads);
@@ -120,25 +124,36 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
   const int units = (a.K + 63) / 64;
   const int begin = (int)((int64_t)units * slice / a.S), end = (int)((int64_t)units * (slice + 1) / a.S);
   // A unit is a line of 128 bytes of every row: slot h of an instruction takes chunk h, then h + 4.
-  for (int u = begin + wave; u < end; u += 4) {
-    v4i fx[2][FT], fw[2][FR];
+  // The next unit's loads are on their way while this one is multiplied.
+  struct Unit { v4i x[2][FT], w[2][FR]; };
+  auto fetch = [&](int u, Unit& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = u * 64 + (h * 4 + slot) * 8;
-      const bool in = k < a.K;
+      const bool in = u < end && k < a.K;
 #pragma unroll
-      for (int i = 0; i < FT; ++i) fx[h][i] = in ? *reinterpret_cast<const v4i*>(x[i] + k * 2) : v4i{0, 0, 0, 0};
+      for (int i = 0; i < FT; ++i) f.x[h][i] = in ? *reinterpret_cast<const v4i*>(x[i] + k * 2) : v4i{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < FR; ++j)
-        fw[h][j] = in && j < blocks ? *reinterpret_cast<const v4i*>(w[j] + k * 2) : v4i{0, 0, 0, 0};
+        f.w[h][j] = in && j < blocks ? *reinterpret_cast<const v4i*>(w[j] + k * 2) : v4i{0, 0, 0, 0};
     }
+  };
+  auto multiply = [&](const Unit& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < FR; ++j)
         if (j < blocks)
 #pragma unroll
-          for (int i = 0; i < FT; ++i) acc[i][j] = mfma16(fw[h][j], fx[h][i], acc[i][j]);
+          for (int i = 0; i < FT; ++i) acc[i][j] = mfma16(f.w[h][j], f.x[h][i], acc[i][j]);
+  };
+  Unit f0, f1;
+  fetch(begin + wave, f0);
+  for (int u = begin + wave; u < end; u += 8) {
+    fetch(u + 4, f1);
+    multiply(f0);
+    fetch(u + 8, f0);
+    multiply(f1);
   }
   // A lane holds rows 4 slot .. + 3 of each block of A_i for token `row` of each 16.
 #pragma unroll
@@ -158,57 +173,59 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
 
 // ---- up ----
 
-// 16 consecutive columns of a row, of which the first `left` exist.
+// The 16 columns of a row that a lane has, as Q vectors of 16 bytes: vector q's columns follow
+// those of the row's other three lanes, so that each load and store of a wave covers whole
+// 64-byte pieces.  `left`: how many columns there are from the vector's first on.
+typedef v4i v4i_at2 __attribute__((aligned(2)));
+typedef v4i v4i_at4 __attribute__((aligned(4)));
 template <bool BF16>
-__device__ __forceinline__ void load_cols(const void* base, int64_t at, int left, float (&y)[16]) {
-  if constexpr (BF16) {
-    typedef v4i v4i_any __attribute__((aligned(2)));
-    const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    if (left >= 16) {
+struct Cols {
+  static constexpr int Q = BF16 ? 2 : 4, V = 16 / Q;
+  typedef typename std::conditional<BF16, v4i_at2, v4i_at4>::type any;
+  v4i v[Q];
+  __device__ __forceinline__ void load(const void* base, int64_t row, int n, int N) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const v4i v = *reinterpret_cast<const v4i_any*>(p + 8 * q);
+    for (int q = 0; q < Q; ++q) {
+      const int c = n + q * 4 * V, left = N - c;
+      const uint8_t* p = static_cast<const uint8_t*>(base) + (row + c) * (16 / V);
+      if (left >= V) {
+        v[q] = *reinterpret_cast<const any*>(p);
+      } else {
+        v[q] = v4i{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t w = (uint32_t)v[e / 2];
-          y[8 * q + e] = __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
-        }
+        for (int e = 0; e < V; ++e)
+          if (e < left) {
+            if constexpr (BF16) v[q][e / 2] |= (int)((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (e & 1 ? 16 : 0));
+            else v[q][e] = reinterpret_cast<const int*>(p)[e];
+          }
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = e < left ? __builtin_bit_cast(float, (uint32_t)p[e] << 16) : 0.0f;
-    }
-  } else {
-    typedef v4f v4f_any __attribute__((aligned(4)));
-    const float* p = static_cast<const float*>(base) + at;
-    if (left >= 16) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f v = *reinterpret_cast<const v4f_any*>(p + 4 * q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[4 * q + e] = v[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = e < left ? p[e] : 0.0f;
     }
   }
-}
-template <bool BF16>
-__device__ __forceinline__ void store_16(void* D, int64_t at, int left, const float (&y)[16]) {
-  constexpr int V = BF16 ? 8 : 4;
-#pragma unroll
-  for (int q = 0; q < 16; q += V) {
-    float t[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) t[e] = y[q + e];
-    if (left > q) store_cols<BF16>(D, at + q, left - q, t);
+  __device__ __forceinline__ float at(int q, int e) const {
+    if constexpr (BF16) {
+      const uint32_t w = (uint32_t)v[q][e / 2];
+      return __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
+    } else {
+      const int w = v[q][e];
+      return __builtin_bit_cast(float, w);
+    }
   }
-}
+  // base + acc, block b = q V / 4 + e / 4 holding element e of vector q.
+  __device__ __forceinline__ void add_store(void* D, int64_t row, int n, int N, const v4f (&acc)[4]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int c = n + q * 4 * V;
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = at(q, e) + acc[q * V / 4 + e / 4][e % 4];
+      if (c < N) store_cols<BF16>(D, row + c, N - c, y);
+    }
+  }
+};
 
 template <int TM, int RMAX, bool DIRECT, bool BF16>
 __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int shares) {
-  constexpr int FT = TM / 16;
+  constexpr int FT = TM / 16, V = Cols<BF16>::V;
   __shared__ int tok[TM];
   __shared__ FindSpace find;
   constexpr int pitch = RMAX * 2 + 16;
@@ -220,17 +237,41 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
   const int first = share * a.steps * 256;
   if (t.adapter < 0) {
     if (a.D == a.base) return;
+    const v4f none[4] = {};
     for (int s = 0; s < a.steps; ++s) {
-      const int n = first + s * 256 + (threadIdx.x & 15) * 16;
-      if (n >= a.N) break;
-      for (int m = threadIdx.x >> 4; m < t.count; m += 16) {
-        float y[16];
-        const int64_t at = (int64_t)tok[m] * a.N + n;
-        load_cols<BF16>(a.base, at, a.N - n, y);
-        store_16<BF16>(a.D, at, a.N - n, y);
+      const int n0 = first + s * 256 + wave * 64, n = n0 + slot * V;
+      if (n0 >= a.N) break;
+      for (int m = row; m < t.count; m += 16) {
+        const int64_t at = (int64_t)tok[m] * a.N;
+        Cols<BF16> c;
+        c.load(a.base, at, n, a.N);
+        c.add_store(a.D, at, n, a.N, none);
       }
     }
     return;
+  }
+  // What a step needs of base, and of B for the first 32 of R, is asked for before V is needed.
+  const uint8_t* B = a.B + (int64_t)t.adapter * a.N * a.R * 2;
+  const int tiles16 = (t.count + 15) / 16;
+  Cols<BF16> base[FT];
+  v4i fb[4];
+  auto fetch_base = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < FT; ++i)
+      if (i * 16 + row < t.count) base[i].load(a.base, (int64_t)tok[i * 16 + row] * a.N, n0 + slot * V, a.N);
+  };
+  // Row 4 g + e of block b is the column that element 4 b + e of slot g's 16 stands for.
+  auto fetch_b = [&](int n0, int k) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int n = n0 + b * 4 / V * 4 * V + (row >> 2) * V + b * 4 % V + (row & 3);
+      fb[b] = k < a.R && n < a.N ? *reinterpret_cast<const v4i*>(B + ((int64_t)n * a.R + k) * 2) : v4i{0, 0, 0, 0};
+    }
+  };
+  int n0 = first + wave * 64;
+  if (n0 < a.N) {
+    fetch_base(n0);
+    fetch_b(n0, slot * 8);
   }
   // V's sums as two bf16 terms, zeros past R and past the tile's tokens.
   const int RP = (a.R + 31) / 32 * 32;
@@ -241,6 +282,7 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
     if (m < t.count && r < a.R) {
       const float* p = a.V + (int64_t)tok[m] * a.R + r;
       v = *reinterpret_cast<const v4f*>(p);
+#pragma unroll 4
       for (int s = 1; s < a.S; ++s) v += *reinterpret_cast<const v4f*>(p + (int64_t)s * a.M * a.R);
     }
     float lo[4];
@@ -259,21 +301,15 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
     *reinterpret_cast<v2i*>(terms + (TM + m) * pitch + r * 2) = v2i{(int)pack_bf16x2(lo[0], lo[1]), (int)pack_bf16x2(lo[2], lo[3])};
   }
   __syncthreads();
-  const int tiles16 = (t.count + 15) / 16;
-  const uint8_t* B = a.B + (int64_t)t.adapter * a.N * a.R * 2;
-  for (int s = 0; s < a.steps; ++s) {
-    // Row 4 g + e of block b is column n0 + 16 g + 4 b + e: a lane (slot g) has 16 columns in a row.
-    const int n0 = first + s * 256 + wave * 64, mine = n0 + slot * 16;
-    if (n0 >= a.N) break;
+  for (int s = 0; s < a.steps && n0 < a.N; ++s, n0 += 256) {
+    if (s > 0) {
+      fetch_base(n0);
+      fetch_b(n0, slot * 8);
+    }
     v4f acc[FT][4] = {};
     for (int kb = 0; kb < RP; kb += 32) {
       const int k = kb + slot * 8;
-      v4i fb[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int n = n0 + (row >> 2) * 16 + 4 * b + (row & 3);
-        fb[b] = k < a.R && n < a.N ? *reinterpret_cast<const v4i*>(B + ((int64_t)n * a.R + k) * 2) : v4i{0, 0, 0, 0};
-      }
+      if (kb > 0) fetch_b(n0, k);
 #pragma unroll
       for (int i = 0; i < FT; ++i)
         if (i < tiles16) {
@@ -286,16 +322,9 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
         }
     }
 #pragma unroll
-    for (int i = 0; i < FT; ++i) {
-      if (i * 16 + row < t.count && mine < a.N) {
-        const int64_t at = (int64_t)tok[i * 16 + row] * a.N + mine;
-        float y[16];
-        load_cols<BF16>(a.base, at, a.N - mine, y);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] += acc[i][e / 4][e % 4];
-        store_16<BF16>(a.D, at, a.N - mine, y);
-      }
-    }
+    for (int i = 0; i < FT; ++i)
+      if (i * 16 + row < t.count)
+        base[i].add_store(a.D, (int64_t)tok[i * 16 + row] * a.N, n0 + slot * V, a.N, acc[i]);
   }
 }
 
@@ -312,9 +341,12 @@ __global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(int M, int
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, buckets = L + 1;
   for (int b = tid; b < buckets; b += kOrderThreads) counts[b] = 0;
   __syncthreads();
+  int ahead = tid < M ? index[tid] : 0;
   for (int64_t m0 = 0; m0 < M; m0 += kOrderThreads) {
     const int64_t m = m0 + tid;
-    const int id = m < M ? adapter_of(index[m], L) : -2, bucket = id < 0 ? L : id;
+    const int now = ahead;
+    if (m + kOrderThreads < M) ahead = index[m + kOrderThreads];
+    const int id = m < M ? adapter_of(now, L) : -2, bucket = id < 0 ? L : id;
     bool left = id != -2;
     int at = 0;
     // Neighbours mostly share an adapter: two of a wave's adapters are counted at once, the

@@ -64,41 +64,59 @@ __global__ void __launch_bounds__(256) loss_count_kernel(int64_t M, int64_t igno
   if (threadIdx.x == 0) counts[blockIdx.x] = n;
 }
 
-// A wave for each of 4 rows: how many before it take part is counted by the whole workgroup, in
-// the row's chunk alone where the chunks before it are counted already.
-template <bool GRAD>
+// A wave for each of 4 rows, or (ROWS == 1) the workgroup for one: how many before take part is
+// counted by the whole workgroup, in the rows' chunk alone where the chunks before it are
+// counted already.  A row's copy is under way before the count is known.
+template <bool GRAD, int ROWS>
 __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
+  constexpr int LANES = 256 / ROWS, AHEAD = 4;
   __shared__ int part[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row0 = (int64_t)blockIdx.x * 4, m = row0 + wave;
+  const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
+  const int64_t row0 = (int64_t)blockIdx.x * ROWS, m = row0 + mine, units = a.K / 8;
+  bool in[ROWS], here = false;
+#pragma unroll
+  for (int w = 0; w < ROWS; ++w) {
+    in[w] = row0 + w < a.M && a.target[row0 + w] != a.ignore;
+    here |= w == mine && in[w];
+  }
+  const v4i* x = a.X + m * units;
+  v4i held[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (here && lane + i * LANES < units) held[i] = x[lane + i * LANES];
   int before = 0;
   int64_t from = 0;
   if (a.counts) {
     from = row0 / kChunk * kChunk;
     for (int64_t c = threadIdx.x; c < row0 / kChunk; c += 256) before += a.counts[c];
   }
+#pragma unroll 4
   for (int64_t i = from + threadIdx.x; i < row0; i += 256) before += a.target[i] != a.ignore;
   before = block_sum(before, part);
-  bool in[4];
+  int slot = before, last = before;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) in[w] = row0 + w < a.M && a.target[row0 + w] != a.ignore;
-  int slot = before;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) slot += w < wave && in[w];
-  if (row0 + 4 >= a.M && threadIdx.x == 0) *a.count = before + in[0] + in[1] + in[2] + in[3];
+  for (int w = 0; w < ROWS; ++w) {
+    slot += w < mine && in[w];
+    last += in[w];
+  }
+  if (row0 + ROWS >= a.M && threadIdx.x == 0) *a.count = last;
   if (m >= a.M) return;
-  const int64_t units = a.K / 8;
-  if (!in[wave]) {
+  if (!here) {
     if constexpr (GRAD) {
       if (a.dX)
-        for (int64_t u = lane; u < units; u += 64) a.dX[m * units + u] = v4i{0, 0, 0, 0};
+        for (int64_t u = lane; u < units; u += LANES) a.dX[m * units + u] = v4i{0, 0, 0, 0};
     } else if (lane == 0) {
       a.loss[m] = 0.0f;
       if (a.lse) a.lse[m] = 0.0f;
     }
     return;
   }
-  for (int64_t u = lane; u < units; u += 64) a.rows[slot * units + u] = a.X[m * units + u];
+  v4i* to = a.rows + slot * units;
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (lane + i * LANES < units) to[lane + i * LANES] = held[i];
+#pragma unroll 4
+  for (int64_t u = lane + AHEAD * LANES; u < units; u += LANES) to[u] = x[u];
   if (lane == 0) {
     const int64_t t = a.target[m];
     const bool known = t >= 0 && t < a.V;
@@ -120,36 +138,55 @@ hipError_t launch_pick(Pick p, int* counts, bool grad, hipStream_t s) {
     if (e != hipSuccess) return e;
     p.counts = counts;
   }
-  return launch(grad ? loss_pick_kernel<true> : loss_pick_kernel<false>, ceil_div(p.M, 4), 256, s, p);
+  // Few rows are spread over the chip: 16 x 4096 take 3 us a row to a workgroup, 7 four to one.
+  if (p.M <= 1024) return launch(grad ? loss_pick_kernel<true, 1> : loss_pick_kernel<false, 1>, p.M, 256, s, p);
+  return launch(grad ? loss_pick_kernel<true, 4> : loss_pick_kernel<false, 4>, ceil_div(p.M, 4), 256, s, p);
 }
 
 // ---- forward ----
 
-// The parts of a row joined: 16 rows a workgroup, every 16th part a thread.
+// e^(a - b) of a part and its share of a row: of two parts at -infinity 0, their sums are 0 too.
+__device__ __forceinline__ float2 join(float2 x, float2 y) {
+  const float most = fmaxf(x.x, y.x), from = most == -__builtin_inff() ? 0.0f : most;
+  return make_float2(most, x.y * __builtin_amdgcn_exp2f((x.x - from) * kLog2e) +
+                               y.y * __builtin_amdgcn_exp2f((y.x - from) * kLog2e));
+}
+
+// The parts of a row joined, ROWS rows a workgroup: every 256 / ROWS th part a thread, then the
+// threads of a row in pairs.
+template <int ROWS>
 __global__ void __launch_bounds__(256) loss_join_kernel(int64_t M, int parts, const int* __restrict__ count,
                                                         const float2* __restrict__ part, const float* __restrict__ z,
                                                         const int* __restrict__ map, float* __restrict__ loss,
                                                         float* __restrict__ lse) {
-  __shared__ float2 held[16][17];
-  const int r = threadIdx.x & 15, q = threadIdx.x >> 4;
-  const int64_t m = (int64_t)blockIdx.x * 16 + r;
+  constexpr int Q = 256 / ROWS;
+  __shared__ float2 held[Q][ROWS + 1];
+  const int r = threadIdx.x % ROWS, q = threadIdx.x / ROWS;
+  const int64_t m = (int64_t)blockIdx.x * ROWS + r;
+  if ((int64_t)blockIdx.x * ROWS >= *count) return;
   const bool there = m < *count;
-  // e^(a - b) of the first part is e^-inf = 0; of two parts at -infinity 0, their sums are 0 too.
-  auto join = [](float2 x, float2 y) {
-    const float most = fmaxf(x.x, y.x), from = most == -__builtin_inff() ? 0.0f : most;
-    return make_float2(most, x.y * __builtin_amdgcn_exp2f((x.x - from) * kLog2e) +
-                                 y.y * __builtin_amdgcn_exp2f((y.x - from) * kLog2e));
-  };
   float2 all = make_float2(-__builtin_inff(), 0.0f);
   if (there) {
-#pragma unroll 4
-    for (int p = q; p < parts; p += 16) all = join(all, part[(int64_t)p * M + m]);
+    for (int p = q; p < parts; p += 8 * Q) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = p + i * Q < parts ? part[(int64_t)(p + i * Q) * M + m] : make_float2(-__builtin_inff(), 0.0f);
+#pragma unroll
+      for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i) v[i] = join(v[i], v[i + d]);
+      all = join(all, v[0]);
+    }
   }
   held[q][r] = all;
-  __syncthreads();
-  if (q == 0 && there) {
 #pragma unroll
-    for (int p = 1; p < 16; ++p) all = join(all, held[p][r]);
+  for (int d = Q / 2; d > 0; d /= 2) {
+    __syncthreads();
+    if (q < d) held[q][r] = join(held[q][r], held[q + d][r]);
+  }
+  if (q == 0 && there) {
+    all = held[0][r];
     // (maximum - z) first: it is small where the loss is.
     const float l = logf(all.y);
     const int row = map[m];
@@ -301,8 +338,10 @@ hipError_t launch_loss(const LossCall& c, hipStream_t s) {
   a.count = w.picked.count, a.target = w.picked.wanted, a.parts = w.part, a.wanted = w.z;
   e = launch_one_group<Forward, true, false>(a, forward_plan(c.M, c.V, c.K).tile, s);
   if (e != hipSuccess) return e;
-  return launch(loss_join_kernel, ceil_div(c.M, 16), 256, s, c.M, (int)w.parts, static_cast<const int*>(a.count),
-                static_cast<const float2*>(w.part), static_cast<const float*>(w.z),
+  // 16 rows side by side are whole lines of parts; few rows need the threads.
+  const int rows = c.M >= 2048 ? 16 : 1;
+  return launch(rows == 16 ? loss_join_kernel<16> : loss_join_kernel<1>, ceil_div(c.M, rows), 256, s, c.M, (int)w.parts,
+                static_cast<const int*>(a.count), static_cast<const float2*>(w.part), static_cast<const float*>(w.z),
                 static_cast<const int*>(w.picked.map), c.loss, c.lse);
 }
 

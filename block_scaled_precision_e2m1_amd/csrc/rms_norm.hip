@@ -39,15 +39,11 @@ __device__ __forceinline__ double squares(const v4u& h, double sum) {
   return sum;
 }
 
-// y = (h * s) * w of the unit at `first`; zero past the row's end, whatever s is.
-template <bool BF16, bool WBF16>
-__device__ __forceinline__ void normed(const v4u& h, float s, const void* W, int64_t first, int64_t K,
-                                       float (&y)[Unit<BF16>::EPU]) {
-  constexpr int EPU = Unit<BF16>::EPU;
-  float w[EPU];
-  load_weight<WBF16>(W, first, K, w);
+// y = (h * s) * w of a unit.
+template <bool BF16, class WEIGHTS>
+__device__ __forceinline__ void normed(const v4u& h, float s, const WEIGHTS& w, float (&y)[Unit<BF16>::EPU]) {
 #pragma unroll
-  for (int e = 0; e < EPU; ++e) y[e] = Unit<BF16>::at(h, e) * s * w[e];
+  for (int e = 0; e < Unit<BF16>::EPU; ++e) y[e] = Unit<BF16>::at(h, e) * s * w.at(e);
 }
 
 // max|y| as bits: magnitudes order like integers, infinities and NaN past every finite one.
@@ -122,37 +118,54 @@ struct Rows {
 };
 
 // H may be X or R, Y may be X or R: a row's units are stored by the lanes that read them, and
-// after every load of theirs.
-template <bool BF16, bool WBF16, bool QUANT, int L, int C>
-__global__ void __launch_bounds__(L < 256 ? 256 : L) rms_norm_kernel(const Rows a) {
+// after every load of theirs.  The weights are asked for before the row's sum is known, so that
+// one latency covers both.
+template <bool BF16, bool WBF16, bool QUANT, bool TAIL, int L, int C>
+__global__ void __launch_bounds__(L ? 256 : 1024) rms_norm_kernel(const Rows a) {
   typedef Unit<BF16> U;
-  constexpr int NT = L < 256 ? 256 : L, RPW = NT / L;
-  __shared__ double sums[NT / 64];
-  __shared__ uint32_t mosts[NT / 64];
-  const int64_t mine = (int64_t)blockIdx.x * RPW + threadIdx.x / L;
+  constexpr int RPW = L ? 256 / L : 1;
+  __shared__ double sums[16];
+  __shared__ uint32_t mosts[16];
+  const int lanes = lanes_of<L>(), lane = threadIdx.x % lanes;
+  const int64_t mine = (int64_t)blockIdx.x * RPW + threadIdx.x / lanes;
   const bool there = mine < a.rows;
   const int64_t row = there ? mine : a.rows - 1;
-  const int lane = threadIdx.x % L, units = ((uint32_t)a.K + U::EPU - 1) / U::EPU;
+  const int units = ((uint32_t)a.K + U::EPU - 1) / U::EPU;
   const int64_t at = row * a.K * U::ELEM;
+  const bool more = (a.rows - 1 - row) * a.K >= U::EPU;
   v4u h[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int u = lane + c * L;
-    h[c] = u < units ? U::template load<true>(a.X + at, (int64_t)u * U::EPU, a.K) : v4u{0, 0, 0, 0};
+    const int u = lane + c * lanes;
+    h[c] = u < units ? U::template load<TAIL, true>(a.X + at, (int64_t)u * U::EPU, a.K, more) : v4u{0, 0, 0, 0};
   }
+  Weights<WBF16, U::EPU> w[C];
+  auto weights = [&]() {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int u = lane + c * lanes;
+      if (u < units) w[c].template load<TAIL>(a.W, (int64_t)u * U::EPU, a.K);
+    }
+  };
   if (a.R) {
     v4u r[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int u = lane + c * L;
-      r[c] = u < units ? U::template load<true>(a.R + at, (int64_t)u * U::EPU, a.K) : v4u{0, 0, 0, 0};
+      const int u = lane + c * lanes;
+      r[c] = u < units ? U::template load<TAIL, true>(a.R + at, (int64_t)u * U::EPU, a.K, more) : v4u{0, 0, 0, 0};
     }
+    weights();
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int u = lane + c * L;
+      const int u = lane + c * lanes;
       h[c] = add_units<BF16>(h[c], r[c]);
-      if (there && u < units) U::store(a.H + at, (int64_t)u * U::EPU, a.K, h[c]);
+      U::template clear<TAIL>(h[c], (int64_t)u * U::EPU, a.K);
+      if (there && u < units) U::template store<TAIL>(a.H + at, (int64_t)u * U::EPU, a.K, h[c]);
     }
+  } else {
+    weights();
+#pragma unroll
+    for (int c = 0; c < C; ++c) U::template clear<TAIL>(h[c], (int64_t)(lane + c * lanes) * U::EPU, a.K);
   }
   double sum = 0.0;
 #pragma unroll
@@ -163,13 +176,13 @@ __global__ void __launch_bounds__(L < 256 ? 256 : L) rms_norm_kernel(const Rows 
   uint32_t most = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int u = lane + c * L;
+    const int u = lane + c * lanes;
     const int64_t first = (int64_t)u * U::EPU;
     float(&v)[U::EPU] = y[QUANT ? c : 0];
     if (u < units) {
-      normed<BF16, WBF16>(h[c], s, a.W, first, a.K, v);
-      if constexpr (QUANT) most = max_bits(v, a.K - first, most);
-      if (there && (!QUANT || a.Y)) U::store(a.Y + at, first, a.K, U::pack(v));
+      normed<BF16>(h[c], s, w[c], v);
+      if constexpr (QUANT) most = max_bits(v, TAIL ? a.K - first : U::EPU, most);
+      if (there && (!QUANT || a.Y)) U::template store<TAIL>(a.Y + at, first, a.K, U::pack(v));
     }
   }
   if constexpr (QUANT) {
@@ -180,10 +193,10 @@ __global__ void __launch_bounds__(L < 256 ? 256 : L) rms_norm_kernel(const Rows 
     if (lane == 0) a.scales[row] = scale;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int u = lane + c * L;
+      const int u = lane + c * lanes;
       const int64_t first = (int64_t)u * U::EPU;
       if (u < units)
-        store_codes(a.codes + row * a.K + first, a.K - first, y[c], inv, a.e4m3, has_codes(most));
+        store_codes(a.codes + row * a.K + first, TAIL ? a.K - first : U::EPU, y[c], inv, a.e4m3, has_codes(most));
     }
   }
 }
@@ -199,33 +212,37 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const Rows a) {
   double sum = 0.0;
   for (int u = threadIdx.x; u < units; u += 1024) {
     const int64_t first = (int64_t)u * U::EPU;
-    v4u h = U::load(a.X + at, first, a.K);
+    v4u h = U::load(a.X + at, first, a.K, false);
     if (a.R) {
-      h = add_units<BF16>(h, U::load(a.R + at, first, a.K));
+      h = add_units<BF16>(h, U::load(a.R + at, first, a.K, false));
       U::store(a.H + at, first, a.K, h);
     }
     sum = squares<BF16>(h, sum);
   }
-  sum = over_row<1024>(sum, Add{}, sums);
+  sum = over_row<0>(sum, Add{}, sums);
   const float s = inv_sqrt(sum / (double)a.K + a.eps);
   const uint8_t* src = (a.R ? a.H : a.X) + at;   // a thread reads what it wrote itself
   uint32_t most = 0;
   for (int u = threadIdx.x; u < units; u += 1024) {
     const int64_t first = (int64_t)u * U::EPU;
     float y[U::EPU];
-    normed<BF16, WBF16>(U::load(src, first, a.K), s, a.W, first, a.K, y);
+    Weights<WBF16, U::EPU> w;
+    w.load(a.W, first, a.K);
+    normed<BF16>(U::load(src, first, a.K, false), s, w, y);
     if constexpr (QUANT) most = max_bits(y, a.K - first, most);
     else U::store(a.Y + at, first, a.K, U::pack(y));
   }
   if constexpr (QUANT) {
-    most = over_row<1024>(most, Max{}, mosts);
+    most = over_row<0>(most, Max{}, mosts);
     float scale;
     const float inv = inverse_of(most, a.e4m3 ? 448.0f : 127.0f, &scale);
     if (threadIdx.x == 0) a.scales[row] = scale;
     for (int u = threadIdx.x; u < units; u += 1024) {
       const int64_t first = (int64_t)u * U::EPU;
       float y[U::EPU];
-      normed<BF16, WBF16>(U::load(src, first, a.K), s, a.W, first, a.K, y);
+      Weights<WBF16, U::EPU> w;
+      w.load(a.W, first, a.K);
+      normed<BF16>(U::load(src, first, a.K, false), s, w, y);
       if (a.Y) U::store(a.Y + at, first, a.K, U::pack(y));   // over X, if at all, once it is no longer read
       store_codes(a.codes + row * a.K + first, a.K - first, y, inv, a.e4m3, has_codes(most));
     }
@@ -236,12 +253,17 @@ template <bool BF16, bool WBF16, bool QUANT>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   const int64_t units = ceil_div(a.K, Unit<BF16>::EPU), elem = Unit<BF16>::ELEM;
   void (*kernel)(Rows) = rms_norm_long_kernel<BF16, WBF16, QUANT>;
-  int lanes = 1024;
-#define PICK(U, L, C) else if (units <= U) kernel = rms_norm_kernel<BF16, WBF16, QUANT, L, C>, lanes = L;
-  if (false) {}
-  FP4G_NORM_SHAPES(PICK)
-#undef PICK
-  const int block = std::max(lanes, 256), per = block / lanes;
+  int block = 1024, per = 1;
+#define SHAPE(L, C)                                                                                       \
+  kernel = a.K % Unit<BF16>::EPU ? rms_norm_kernel<BF16, WBF16, QUANT, true, L, C>                        \
+                                 : rms_norm_kernel<BF16, WBF16, QUANT, false, L, C>,                      \
+  block = L ? 256 : (int)(ceil_div(units, 64 * C) * 64), per = L ? 256 / (L + !L) : 1
+  if (units <= 16) SHAPE(16, 1);
+  else if (units <= 32) SHAPE(32, 1);
+  else if (units <= 64) SHAPE(64, 1);
+  else if (units <= 2048) SHAPE(0, 2);
+  else if (units <= 4096) SHAPE(0, 4);
+#undef SHAPE
   const int64_t most = ((int64_t)1 << 31) / block * per;
   for (int64_t first = 0; first < a.rows; first += most) {
     const int64_t n = std::min(a.rows - first, most), at = first * a.K;
