@@ -28,7 +28,6 @@ namespace fp4g {
 namespace {
 
 constexpr int kDirect = 256;      // tokens whose tiles need no order made beforehand
-constexpr int kRC = 64;           // rows of A_i that a workgroup of `down` takes
 
 struct Tile { int adapter, first, count, pad; };   // adapter -1: none
 
@@ -100,42 +99,41 @@ __device__ __forceinline__ Tile tile_of(const Args& a, int t, FindSpace& f, int*
 
 // ---- down ----
 
-template <int TM, bool DIRECT>
+// FR blocks of 16 rows of A_i at once.
+template <int TM, int FR, bool DIRECT>
 __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
-  constexpr int FT = TM / 16, FR = kRC / 16;
+  constexpr int FT = TM / 16, RC = FR * 16;
   __shared__ int tok[TM];
   __shared__ FindSpace find;
-  __shared__ __attribute__((aligned(16))) float sums[4][TM][kRC + 4];
-  const int chunks = (a.R + kRC - 1) / kRC;
-  const int slice = blockIdx.x % a.S, rest = blockIdx.x / a.S, r0 = rest % chunks * kRC;
+  __shared__ __attribute__((aligned(16))) float sums[4][TM][RC + 4];
+  const int chunks = (a.R + RC - 1) / RC;
+  const int slice = blockIdx.x % a.S, rest = blockIdx.x / a.S, r0 = rest % chunks * RC;
   const Tile t = tile_of<TM, DIRECT>(a, rest / chunks, find, tok);
   if (t.adapter < 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, slot = lane >> 4;
-  const int rows = min(a.R - r0, kRC), blocks = (rows + 15) / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 15, slot = lane >> 4, rows = min(a.R - r0, RC);
   // Rows past the tile's tokens, or past R, repeat the last one: what they give is not kept.
   const uint8_t* x[FT];
 #pragma unroll
-  for (int i = 0; i < FT; ++i) x[i] = a.X + (int64_t)tok[min(i * 16 + row, t.count - 1)] * a.K * 2;
+  for (int i = 0; i < FT; ++i) x[i] = a.X + (int64_t)tok[min(i * 16 + row, t.count - 1)] * a.K * 2 + slot * 16;
   const uint8_t* w[FR];
 #pragma unroll
   for (int j = 0; j < FR; ++j)
-    w[j] = a.A + ((int64_t)t.adapter * a.R + r0 + min(j * 16 + row, rows - 1)) * a.K * 2;
+    w[j] = a.A + ((int64_t)t.adapter * a.R + r0 + min(j * 16 + row, rows - 1)) * a.K * 2 + slot * 16;
   v4f acc[FT][FR] = {};
-  const int units = (a.K + 63) / 64;
+  const int units = a.K / 64;
   const int begin = (int)((int64_t)units * slice / a.S), end = (int)((int64_t)units * (slice + 1) / a.S);
   // A unit is a line of 128 bytes of every row: slot h of an instruction takes chunk h, then h + 4.
-  // The next unit's loads are on their way while this one is multiplied.
+  // Nothing in it branches (at the end of a branch the compiler waits for the loads within), and
+  // the order is pinned: left to itself the compiler puts each load before its use.
   struct Unit { v4i x[2][FT], w[2][FR]; };
   auto fetch = [&](int u, Unit& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = u * 64 + (h * 4 + slot) * 8;
-      const bool in = u < end && k < a.K;
 #pragma unroll
-      for (int i = 0; i < FT; ++i) f.x[h][i] = in ? *reinterpret_cast<const v4i*>(x[i] + k * 2) : v4i{0, 0, 0, 0};
+      for (int i = 0; i < FT; ++i) f.x[h][i] = *reinterpret_cast<const v4i*>(x[i] + (int64_t)u * 128 + h * 64);
 #pragma unroll
-      for (int j = 0; j < FR; ++j)
-        f.w[h][j] = in && j < blocks ? *reinterpret_cast<const v4i*>(w[j] + k * 2) : v4i{0, 0, 0, 0};
+      for (int j = 0; j < FR; ++j) f.w[h][j] = *reinterpret_cast<const v4i*>(w[j] + (int64_t)u * 128 + h * 64);
     }
   };
   auto multiply = [&](const Unit& f) {
@@ -143,17 +141,41 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < FR; ++j)
-        if (j < blocks)
 #pragma unroll
-          for (int i = 0; i < FT; ++i) acc[i][j] = mfma16(f.w[h][j], f.x[h][i], acc[i][j]);
+        for (int i = 0; i < FT; ++i) acc[i][j] = mfma16(f.w[h][j], f.x[h][i], acc[i][j]);
   };
-  Unit f0, f1;
-  fetch(begin + wave, f0);
-  for (int u = begin + wave; u < end; u += 8) {
-    fetch(u + 4, f1);
-    multiply(f0);
-    fetch(u + 8, f0);
-    multiply(f1);
+  // The next unit's loads are on their way while this one is multiplied; past the last the last
+  // is read again.
+  int u = begin + wave;
+  if (u < end) {
+    Unit f0, f1;
+    fetch(u, f0);
+    while (true) {
+      fetch(min(u + 4, end - 1), f1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(f0);
+      __builtin_amdgcn_sched_barrier(0);
+      if ((u += 4) >= end) break;
+      fetch(min(u + 4, end - 1), f0);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(f1);
+      __builtin_amdgcn_sched_barrier(0);
+      if ((u += 4) >= end) break;
+    }
+  }
+  if (a.K % 64 != 0 && slice == a.S - 1 && wave == 3) {   // the last line is short
+    Unit f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = units * 64 + (h * 4 + slot) * 8 < a.K;
+#pragma unroll
+      for (int i = 0; i < FT; ++i)
+        f.x[h][i] = in ? *reinterpret_cast<const v4i*>(x[i] + (int64_t)units * 128 + h * 64) : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < FR; ++j)
+        f.w[h][j] = in ? *reinterpret_cast<const v4i*>(w[j] + (int64_t)units * 128 + h * 64) : v4i{0, 0, 0, 0};
+    }
+    multiply(f);
   }
   // A lane holds rows 4 slot .. + 3 of each block of A_i for token `row` of each 16.
 #pragma unroll
@@ -161,8 +183,8 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < FR; ++j) *reinterpret_cast<v4f*>(&sums[wave][i * 16 + row][j * 16 + 4 * slot]) = acc[i][j];
   __syncthreads();
-  for (int e = threadIdx.x; e < TM * kRC / 4; e += 256) {
-    const int m = e / (kRC / 4), r = e % (kRC / 4) * 4;
+  for (int e = threadIdx.x; e < TM * RC / 4; e += 256) {
+    const int m = e / (RC / 4), r = e % (RC / 4) * 4;
     if (m >= t.count || r >= rows) continue;
     v4f v = *reinterpret_cast<const v4f*>(&sums[0][m][r]);
 #pragma unroll
@@ -175,7 +197,8 @@ __global__ void __launch_bounds__(256) adapter_down_kernel(const Args a) {
 
 // The 16 columns of a row that a lane has, as Q vectors of 16 bytes: vector q's columns follow
 // those of the row's other three lanes, so that each load and store of a wave covers whole
-// 64-byte pieces.  `left`: how many columns there are from the vector's first on.
+// 64-byte pieces.  FULL: all of them are there; the code for those that are not stays out of
+// the way of the rest.
 typedef v4i v4i_at2 __attribute__((aligned(2)));
 typedef v4i v4i_at4 __attribute__((aligned(4)));
 template <bool BF16>
@@ -183,12 +206,13 @@ struct Cols {
   static constexpr int Q = BF16 ? 2 : 4, V = 16 / Q;
   typedef typename std::conditional<BF16, v4i_at2, v4i_at4>::type any;
   v4i v[Q];
+  template <bool FULL>
   __device__ __forceinline__ void load(const void* base, int64_t row, int n, int N) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int c = n + q * 4 * V, left = N - c;
       const uint8_t* p = static_cast<const uint8_t*>(base) + (row + c) * (16 / V);
-      if (left >= V) {
+      if (FULL || left >= V) {
         v[q] = *reinterpret_cast<const any*>(p);
       } else {
         v[q] = v4i{0, 0, 0, 0};
@@ -211,6 +235,7 @@ struct Cols {
     }
   }
   // base + acc, block b = q V / 4 + e / 4 holding element e of vector q.
+  template <bool FULL>
   __device__ __forceinline__ void add_store(void* D, int64_t row, int n, int N, const v4f (&acc)[4]) const {
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -218,13 +243,13 @@ struct Cols {
       float y[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) y[e] = at(q, e) + acc[q * V / 4 + e / 4][e % 4];
-      if (c < N) store_cols<BF16>(D, row + c, N - c, y);
+      if (FULL || c < N) store_cols<BF16>(D, row + c, FULL ? V : N - c, y);
     }
   }
 };
 
 template <int TM, int RMAX, bool DIRECT, bool BF16>
-__global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int shares) {
+__global__ void __launch_bounds__(256, 2) adapter_up_kernel(const Args a, int shares) {
   constexpr int FT = TM / 16, V = Cols<BF16>::V;
   __shared__ int tok[TM];
   __shared__ FindSpace find;
@@ -233,7 +258,7 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
   const int share = blockIdx.x % shares;
   const Tile t = tile_of<TM, DIRECT>(a, blockIdx.x / shares, find, tok);
   if (t.count == 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, slot = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = lane & 15, slot = lane >> 4;
   const int first = share * a.steps * 256;
   if (t.adapter < 0) {
     if (a.D == a.base) return;
@@ -241,37 +266,61 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
     for (int s = 0; s < a.steps; ++s) {
       const int n0 = first + s * 256 + wave * 64, n = n0 + slot * V;
       if (n0 >= a.N) break;
-      for (int m = row; m < t.count; m += 16) {
-        const int64_t at = (int64_t)tok[m] * a.N;
-        Cols<BF16> c;
-        c.load(a.base, at, n, a.N);
-        c.add_store(a.D, at, n, a.N, none);
+      if (n0 + 64 <= a.N) {
+        Cols<BF16> c[FT];
+#pragma unroll
+        for (int i = 0; i < FT; ++i) c[i].template load<true>(a.base, (int64_t)tok[min(i * 16 + row, t.count - 1)] * a.N, n, a.N);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < FT; ++i)
+          if (i * 16 + row < t.count) c[i].template add_store<true>(a.D, (int64_t)tok[i * 16 + row] * a.N, n, a.N, none);
+      } else {
+        for (int m = row; m < t.count; m += 16) {
+          Cols<BF16> c;
+          c.template load<false>(a.base, (int64_t)tok[m] * a.N, n, a.N);
+          c.template add_store<false>(a.D, (int64_t)tok[m] * a.N, n, a.N, none);
+        }
       }
     }
     return;
   }
   // What a step needs of base, and of B for the first 32 of R, is asked for before V is needed.
-  const uint8_t* B = a.B + (int64_t)t.adapter * a.N * a.R * 2;
-  const int tiles16 = (t.count + 15) / 16;
-  Cols<BF16> base[FT];
-  v4i fb[4];
-  auto fetch_base = [&](int n0) {
-#pragma unroll
-    for (int i = 0; i < FT; ++i)
-      if (i * 16 + row < t.count) base[i].load(a.base, (int64_t)tok[i * 16 + row] * a.N, n0 + slot * V, a.N);
-  };
-  // Row 4 g + e of block b is the column that element 4 b + e of slot g's 16 stands for.
-  auto fetch_b = [&](int n0, int k) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int n = n0 + b * 4 / V * 4 * V + (row >> 2) * V + b * 4 % V + (row & 3);
-      fb[b] = k < a.R && n < a.N ? *reinterpret_cast<const v4i*>(B + ((int64_t)n * a.R + k) * 2) : v4i{0, 0, 0, 0};
-    }
-  };
+  // Addresses only advance from step to step: formed anew, in 64 bits, they took as many
+  // instructions as the product.
+  const int end = min((int64_t)first + a.steps * 256, (int64_t)a.N);
   int n0 = first + wave * 64;
-  if (n0 < a.N) {
-    fetch_base(n0);
-    fetch_b(n0, slot * 8);
+  const uint8_t* B = a.B + (int64_t)t.adapter * a.N * a.R * 2;
+  uint32_t of_b[4];
+  int64_t at[FT];
+#pragma unroll
+  for (int i = 0; i < FT; ++i) at[i] = (int64_t)tok[min(i * 16 + row, t.count - 1)] * a.N;
+  // Row 4 g + e of block b is the column that element 4 b + e of slot g's 16 stands for.
+  auto col_of = [&](int b) { return b * 4 / V * 4 * V + (row >> 2) * V + b * 4 % V + (row & 3); };
+#pragma unroll
+  for (int b = 0; b < 4; ++b) of_b[b] = (uint32_t)(col_of(b) * a.R + slot * 8) * 2;
+  // Rows of B past the last column lie past the buffer's end and read as zeros, as do chunks past R.
+  struct Base { Cols<BF16> c[FT]; };
+  auto fetch_base = [&](int n, Base& f) {   // tokens past the tile's repeat the last one and are not stored
+#pragma unroll
+    for (int i = 0; i < FT; ++i) f.c[i].template load<true>(a.base, at[i], n + slot * V, a.N);
+  };
+  struct Rows { v4i v[4]; };
+  auto fetch_b = [&](int n, int kb, Rows& f) {
+    const rsrc_t buffer = make_rsrc(B + (int64_t)n * a.R * 2, min(a.N - n, 64) * a.R * 2);
+    const bool in = kb + slot * 8 < a.R;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) f.v[b] = load_buffer16(buffer, in ? of_b[b] + kb * 2 : kNoLoad);
+  };
+  // Whole steps: 64 columns that all exist.  The last one, short, goes by itself below.
+  const int whole = min(end, a.N / 64 * 64);
+  // Two sets of four times 16 fp32 columns would not leave two waves a SIMD.
+  constexpr bool AHEAD = BF16 || TM == 16;
+  Base f0, f1;
+  Rows b0, b1;
+  if (n0 < whole) {
+    if constexpr (AHEAD) fetch_base(n0, f0);
+    fetch_b(n0, 0, b0);
+    __builtin_amdgcn_sched_barrier(0);
   }
   // V's sums as two bf16 terms, zeros past R and past the tile's tokens.
   const int RP = (a.R + 31) / 32 * 32;
@@ -301,30 +350,59 @@ __global__ void __launch_bounds__(256) adapter_up_kernel(const Args a, int share
     *reinterpret_cast<v2i*>(terms + (TM + m) * pitch + r * 2) = v2i{(int)pack_bf16x2(lo[0], lo[1]), (int)pack_bf16x2(lo[2], lo[3])};
   }
   __syncthreads();
-  for (int s = 0; s < a.steps && n0 < a.N; ++s, n0 += 256) {
-    if (s > 0) {
-      fetch_base(n0);
-      fetch_b(n0, slot * 8);
-    }
+  // acc += B's rows f with V's terms kb .. kb + 31, for 16 tokens from `first16`.
+  auto multiply = [&](const Rows& f, int kb, int first16, v4f(&acc)[4]) {
+    const uint8_t* p = terms + (first16 + row) * pitch + (kb + slot * 8) * 2;
+    const v4i hi = *reinterpret_cast<const v4i*>(p), lo = *reinterpret_cast<const v4i*>(p + TM * pitch);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], hi, acc[b]);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], lo, acc[b]);
+  };
+  // A step's product while the next step's base, and the next rows of B, are on their way.
+  auto step = [&](int n, Base& now, Base& ahead) {
     v4f acc[FT][4] = {};
+    const int next = n + 256 < whole ? n + 256 : n;
+    if constexpr (AHEAD) fetch_base(next, ahead);
+    else fetch_base(n, now);
+    __builtin_amdgcn_sched_barrier(0);
     for (int kb = 0; kb < RP; kb += 32) {
-      const int k = kb + slot * 8;
-      if (kb > 0) fetch_b(n0, k);
+      if (kb + 32 < RP) fetch_b(n, kb + 32, b1);
+      else fetch_b(next, 0, b1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < FT; ++i)
-        if (i < tiles16) {
-          const uint8_t* p = terms + (i * 16 + row) * pitch + k * 2;
-          const v4i hi = *reinterpret_cast<const v4i*>(p), lo = *reinterpret_cast<const v4i*>(p + TM * pitch);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[i][b] = mfma16(fb[b], hi, acc[i][b]);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[i][b] = mfma16(fb[b], lo, acc[i][b]);
-        }
+      for (int i = 0; i < FT; ++i) multiply(b0, kb, i * 16, acc[i]);
+      __builtin_amdgcn_sched_barrier(0);
+      b0 = b1;
     }
 #pragma unroll
     for (int i = 0; i < FT; ++i)
-      if (i * 16 + row < t.count)
-        base[i].add_store(a.D, (int64_t)tok[i * 16 + row] * a.N, n0 + slot * V, a.N, acc[i]);
+      if (i * 16 + row < t.count) now.c[i].template add_store<true>(a.D, at[i], n + slot * V, a.N, acc[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  while (n0 < whole) {
+    step(n0, f0, f1);
+    if ((n0 += 256) >= whole) break;
+    if constexpr (AHEAD) {
+      step(n0, f1, f0);
+      n0 += 256;
+    }
+  }
+  if (n0 < end) {
+#pragma unroll 1
+    for (int i = 0; i < t.count; i += 16) {
+      v4f acc[4] = {};
+      for (int kb = 0; kb < RP; kb += 32) {
+        fetch_b(n0, kb, b0);
+        multiply(b0, kb, i, acc);
+      }
+      if (i + row < t.count) {
+        const int64_t mine = (int64_t)tok[i + row] * a.N;
+        Cols<BF16> c;
+        c.template load<false>(a.base, mine, n0 + slot * V, a.N);
+        c.template add_store<false>(a.D, mine, n0 + slot * V, a.N, acc);
+      }
+    }
   }
 }
 
@@ -409,7 +487,7 @@ Plan plan_of(int64_t M, int64_t K, int64_t R, int64_t L) {
   p.tm = p.direct ? 16 : 64;
   p.tiles = std::min(M, ceil_div(M, p.tm) + L);   // an adapter's last tile may be short; so may that of none
   // Two units of 128 bytes of K a wave at least, and workgroups for the chip.
-  const int64_t units = ceil_div(K, 64), work = p.tiles * std::max<int64_t>(1, ceil_div(R, kRC));
+  const int64_t units = ceil_div(K, 64), work = p.tiles * std::max<int64_t>(1, ceil_div(R, 64));
   p.S = std::max<int64_t>(1, std::min({units / 8, 4 * device_cus() / work, (int64_t)(p.direct ? 16 : 4)}));
   return p;
 }
@@ -459,9 +537,12 @@ hipError_t launch_adapter_gemm(const AdapterCall& c, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (!p.direct)
     e = launch(adapter_order_kernel<64>, 1, kOrderThreads, s, a.M, a.L, c.index, w.rank, w.order, w.tiles, w.count);
-  if (e == hipSuccess && L > 0)
-    e = launch(p.direct ? adapter_down_kernel<16, true> : adapter_down_kernel<64, false>,
-               p.tiles * ceil_div(c.R, kRC) * p.S, 256, s, a);
+  if (e == hipSuccess && L > 0) {
+    const int64_t grid = p.tiles * ceil_div(c.R, 64) * p.S;
+    if (c.R <= 16) e = launch(p.direct ? adapter_down_kernel<16, 1, true> : adapter_down_kernel<64, 1, false>, grid, 256, s, a);
+    else if (c.R <= 32) e = launch(p.direct ? adapter_down_kernel<16, 2, true> : adapter_down_kernel<64, 2, false>, grid, 256, s, a);
+    else e = launch(p.direct ? adapter_down_kernel<16, 4, true> : adapter_down_kernel<64, 4, false>, grid, 256, s, a);
+  }
   if (e != hipSuccess) return e;
   const int64_t steps = ceil_div(c.N, 256), most = std::min(steps, ceil_div(4 * device_cus(), p.tiles));
   a.steps = (int)ceil_div(steps, most);
