@@ -8,9 +8,9 @@
 //   * down   V = X A_i^T.  A wave multiplies 16-row fragments straight from memory (nothing is
 //     used twice but by the tokens of its tile) and the four waves of a workgroup, and S
 //     workgroups, share K; V's S partial sums are kept in fp32, 4 R bytes a token each.
-//   * up     D = base + V B_i^T.  V's sums are added, scaled and split into two bf16 terms
-//     (V = hi + lo to 2^-17 of each value), which both meet the same fragment of B, so that
-//     the second product loses nothing that fp32 results could show.  B's rows are dealt to
+//   * up     D = base + V B_i^T.  V's sums are added, scaled and split into bf16 terms that all
+//     meet the same fragment of B: two for bf16 results (V to 2^-17 of each value, where one
+//     alone, 2^-9, would show in them), three for fp32 (all of V's bits).  B's rows are dealt to
 //     the instruction's so that a lane ends up with whole 16-byte vectors of a token's columns,
 //     and the four lanes of a token with 64 bytes side by side.
 //
@@ -249,12 +249,12 @@ struct Cols {
 };
 
 template <int TM, int RMAX, bool DIRECT, bool BF16>
-__global__ void __launch_bounds__(256, 2) adapter_up_kernel(const Args a, int shares) {
+__global__ void __launch_bounds__(256, TM * RMAX < 64 * 256 || BF16 ? 2 : 1) adapter_up_kernel(const Args a, int shares) {
   constexpr int FT = TM / 16, V = Cols<BF16>::V;
   __shared__ int tok[TM];
   __shared__ FindSpace find;
-  constexpr int pitch = RMAX * 2 + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t terms[2 * TM * pitch];   // hi, lo
+  constexpr int pitch = RMAX * 2 + 16, TERMS = BF16 ? 2 : 3;
+  __shared__ __attribute__((aligned(16))) uint8_t terms[TERMS * TM * pitch];
   const int share = blockIdx.x % shares;
   const Tile t = tile_of<TM, DIRECT>(a, blockIdx.x / shares, find, tok);
   if (t.count == 0) return;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(256, 2) adapter_up_kernel(const Args a, int sh
     fetch_b(n0, 0, b0);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // V's sums as two bf16 terms, zeros past R and past the tile's tokens.
+  // V's sums as bf16 terms, zeros past R and past the tile's tokens.
   const int RP = (a.R + 31) / 32 * 32;
   const float scale = a.scales ? a.scales[t.adapter] : 1.0f;
   for (int e = threadIdx.x; e < TM * (RP / 4); e += 256) {
@@ -334,30 +334,31 @@ __global__ void __launch_bounds__(256, 2) adapter_up_kernel(const Args a, int sh
 #pragma unroll 4
       for (int s = 1; s < a.S; ++s) v += *reinterpret_cast<const v4f*>(p + (int64_t)s * a.M * a.R);
     }
-    float lo[4];
-    uint32_t hi2[2];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] *= scale;
-    hi2[0] = pack_bf16x2(v[0], v[1]), hi2[1] = pack_bf16x2(v[2], v[3]);
+    // Each term is what the ones before it leave, rounded to bf16; an infinity or NaN is in the
+    // first alone.
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      lo[k] = v[k] - __builtin_bit_cast(float, k & 1 ? hi2[k / 2] & 0xffff0000u : hi2[k / 2] << 16);
-    // An infinity or NaN is in hi alone.
+    for (int n = 0; n < TERMS; ++n) {
+      const uint32_t w[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      *reinterpret_cast<v2i*>(terms + (n * TM + m) * pitch + r * 2) = v2i{(int)w[0], (int)w[1]};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (!(__builtin_fabsf(lo[k]) < __builtin_inff())) lo[k] = 0.0f;
-    *reinterpret_cast<v2i*>(terms + m * pitch + r * 2) = v2i{(int)hi2[0], (int)hi2[1]};
-    *reinterpret_cast<v2i*>(terms + (TM + m) * pitch + r * 2) = v2i{(int)pack_bf16x2(lo[0], lo[1]), (int)pack_bf16x2(lo[2], lo[3])};
+      for (int k = 0; k < 4; ++k) {
+        v[k] -= __builtin_bit_cast(float, k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        if (!(__builtin_fabsf(v[k]) < __builtin_inff())) v[k] = 0.0f;
+      }
+    }
   }
   __syncthreads();
   // acc += B's rows f with V's terms kb .. kb + 31, for 16 tokens from `first16`.
   auto multiply = [&](const Rows& f, int kb, int first16, v4f(&acc)[4]) {
     const uint8_t* p = terms + (first16 + row) * pitch + (kb + slot * 8) * 2;
-    const v4i hi = *reinterpret_cast<const v4i*>(p), lo = *reinterpret_cast<const v4i*>(p + TM * pitch);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], hi, acc[b]);
+    for (int n = 0; n < TERMS; ++n) {
+      const v4i t = *reinterpret_cast<const v4i*>(p + n * TM * pitch);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], lo, acc[b]);
+      for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], t, acc[b]);
+    }
   };
   // A step's product while the next step's base, and the next rows of B, are on their way.
   auto step = [&](int n, Base& now, Base& ahead) {

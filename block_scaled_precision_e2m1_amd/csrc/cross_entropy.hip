@@ -201,6 +201,18 @@ __global__ void __launch_bounds__(C::NW * 64, C::NW * C::OCC / 4) loss_gemm_kern
   dense_gemm<C, BF16, false, SPLIT>(a, blockIdx.x, gridDim.x, smem);
 }
 
+// Both gradients' products over all of a small vocabulary in one launch: workgroups 0 .. split-1
+// take dX's items, the others dW's.  They need the same operands, and neither fills the GPU.
+template <class CX, class CW, bool SPLIT>
+__global__ void __launch_bounds__(CX::NW * 64, CX::NW * CX::OCC / 4)
+loss_grads_kernel(const LossArgs x, const LossArgs w, int split) {
+  static_assert(CX::NW == CW::NW && CX::LDS == CW::LDS && CX::OCC == CW::OCC, "one launch shape");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[CX::LDS];
+  const int b = blockIdx.x;
+  if (b < split) dense_gemm<CX, !SPLIT, false, SPLIT>(x, b, split, smem);
+  else dense_gemm<CW, true, false, false>(w, b - split, gridDim.x - split, smem);
+}
+
 template <class C, bool BF16, bool SPLIT>
 hipError_t launch_tiles(const LossArgs& a, hipStream_t s) {
   const int64_t items = ceil_div(a.M, C::BM) * ceil_div(a.N, C::OUTN) * a.S;
@@ -285,18 +297,37 @@ Pick pick_of(const LossCall& a, const Picked& p) {
 // rows' places at the last piece.
 template <bool BF16>
 __global__ void __launch_bounds__(256) loss_reduce_kernel(const LossArgs a) {
-  const uint32_t groups = (uint32_t)(a.N / 4), total = (uint32_t)*a.count * groups;
-  const int64_t plane = (int64_t)a.M * groups;
+  const int rows = *a.count, S = splits_of(a, rows);
+  const uint32_t groups = (uint32_t)(a.N / 4), total = (uint32_t)rows * groups;
+  const int64_t plane = total;
   for (uint32_t x = blockIdx.x * 256 + threadIdx.x; x < total; x += gridDim.x * 256) {
     const uint32_t m = x / groups, n = (x - m * groups) * 4;
     const v4f* p = static_cast<const v4f*>(a.P) + x;
     v4f t = p[0];
 #pragma unroll 4
-    for (int k = 1; k < a.S; ++k) t += p[k * plane];
+    for (int k = 1; k < S; ++k) t += p[k * plane];
     if (a.add) t += *reinterpret_cast<const v4f*>(a.add + (int64_t)m * a.N + n);
     const float y[4] = {t[0], t[1], t[2], t[3]};
     store_cols<BF16>(a.D[0], (int64_t)(BF16 ? a.map[m] : (int)m) * a.N + n, 4, y);
   }
+}
+
+int64_t tile_rows(DenseTile t) { return t == kTile256 ? 256 : t == kTile128 || t == kTile128Deep ? 128 : 64; }
+
+// Whether one launch on 64 x 64 tiles holds both gradients' items at once: each is then as long as
+// its longest item, and the two run side by side.
+typedef GradInput::t64_deep SmallX;
+typedef GradWeights::t64_deep SmallW;
+bool merges(const DensePlan& x, const DensePlan& w, int64_t M, int64_t cols, int64_t K) {
+  const int64_t items = (ceil_div(M, 64) * x.S + ceil_div(cols, 64)) * ceil_div(K, 64);
+  return tile_rows(x.tile) == 64 && tile_rows(w.tile) == 64 && items + 8 <= device_cus() * SmallX::OCC;
+}
+hipError_t launch_both(const LossArgs& x, const LossArgs& w, hipStream_t s) {
+  // A multiple of 8 workgroups for x, so that the others' ids keep their XCDs.
+  const int split = (int)(ceil_div(ceil_div(x.M, 64) * ceil_div(x.N, 64) * x.S, 8) * 8);
+  const int64_t grid = split + ceil_div(w.M, 64) * ceil_div(w.N, 64);
+  return launch(x.S > 1 ? loss_grads_kernel<SmallX, SmallW, true> : loss_grads_kernel<SmallX, SmallW, false>, grid,
+                SmallX::NW * 64, s, x, w, split);
 }
 
 // dX's product over one piece of the vocabulary.
@@ -318,7 +349,7 @@ struct GradSpace {
       const int64_t S = input_plan(M, K, std::min(c, V)).S;
       if (S > 1) splits = std::max(splits, S);
     }
-    P = s.take<float>(splits * M * K);
+    P = s.take<float>(splits * ceil_div(M, 256) * 256 * K);   // whole tiles: splits_of
   }
 };
 
@@ -373,31 +404,33 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     e = launch_any<Probabilities, true, false>(p, dense_plan(c.M, n, 1, ceil_div(c.K, 64), 1).tile, s);
     if (e != hipSuccess) return e;
 
-    if (c.dX) {
-      const DensePlan plan = input_plan(c.M, c.K, n);
-      const bool last = v + n == c.V;
-      LossArgs x;
-      x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
-      x.A[0] = w.prob, x.lda = w.ldp * 2, x.B[0] = W, x.ldb = c.K * 2, x.P = w.P;
-      x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
-      x.D[0] = last ? c.dX : w.kept;
-      if (plan.S > 1) {
-        e = launch_any<GradInput, false, true>(x, plan.tile, s);
-        if (e != hipSuccess) return e;
-        const int64_t grid = std::min<int64_t>(ceil_div(c.M * (c.K / 4), 256), device_cus() * 8);
-        e = launch(last ? loss_reduce_kernel<true> : loss_reduce_kernel<false>, grid, 256, s, x);
-      } else {
-        e = last ? launch_any<GradInput, true, false>(x, plan.tile, s) : launch_any<GradInput, false, false>(x, plan.tile, s);
-      }
-      if (e != hipSuccess) return e;
-    }
-    if (!c.dW) continue;
-    LossArgs d;
+    const DensePlan plan = input_plan(c.M, c.K, n);
+    const bool last = v + n == c.V;
+    LossArgs x, d;
+    x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
+    x.A[0] = w.prob, x.lda = w.ldp * 2, x.B[0] = W, x.ldb = c.K * 2, x.P = w.P;
+    x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
+    x.D[0] = last ? c.dX : w.kept;
+    x.bm = (int)tile_rows(plan.tile), x.most = (int)std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, n / 512));
     d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;
     d.A[0] = w.prob, d.lda = w.ldp * 2, d.B[0] = w.picked.rows, d.ldb = c.K * 2;
     d.D[0] = static_cast<uint8_t*>(c.dW) + v * c.K * 2, d.count = w.picked.count;
-    e = launch_any<GradWeights, true, false>(d, dense_plan(n, c.K, 1, ceil_div(c.M, 64), 1).tile, s);
+    const DensePlan weights = dense_plan(n, c.K, 1, ceil_div(c.M, 64), 1);
+    if (c.dX && c.dW && n == c.V && merges(plan, weights, c.M, n, c.K)) {
+      e = launch_both(x, d, s);
+    } else {
+      if (c.dX) {
+        if (plan.S > 1) e = launch_any<GradInput, false, true>(x, plan.tile, s);
+        else e = last ? launch_any<GradInput, true, false>(x, plan.tile, s) : launch_any<GradInput, false, false>(x, plan.tile, s);
+      }
+      if (e == hipSuccess && c.dW) e = launch_any<GradWeights, true, false>(d, weights.tile, s);
+    }
     if (e != hipSuccess) return e;
+    if (c.dX && plan.S > 1) {
+      const int64_t grid = std::min<int64_t>(ceil_div(c.M * (c.K / 4), 256), device_cus() * 8);
+      e = launch(last ? loss_reduce_kernel<true> : loss_reduce_kernel<false>, grid, 256, s, x);
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }

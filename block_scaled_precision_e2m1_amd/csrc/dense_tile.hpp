@@ -82,7 +82,14 @@ struct LossArgs : DenseArgs {
   const float* g = nullptr;         // prob: what each row is multiplied by
   int64_t ldp = 0;                  // prob: elements between rows of D, a multiple of 8
   const float* add = nullptr;       // accum: [M][N] what is added to the product, if anything
+  int bm = 1, most = 1;             // accum, split: rows of a tile, K slices at most
 };
+// The K slices of a split product whose rows the GPU has counted: as many as give the items that S
+// slices of all M rows would have been.  Their sums then take no more room than those.
+__device__ __forceinline__ int splits_of(const LossArgs& a, int rows) {
+  const uint32_t planned = ((uint32_t)a.M + a.bm - 1) / a.bm, there = max(1u, ((uint32_t)rows + a.bm - 1) / a.bm);
+  return min((uint32_t)a.most, a.S * planned / there);
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // KG groups of waves share a tile: group g multiplies quarters QN g .. of every stage, which
@@ -220,9 +227,11 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
   int M = a.M, K = a.K;
   if constexpr (C::FORM == kLoss || C::FORM == kProb || C::FORM == kAccum) M = *a.count;
   if constexpr (C::FORM == kCounted) K = *a.count;
+  int S = a.S;
+  if constexpr (C::FORM == kAccum && SPLIT) S = splits_of(a, M);
   // Sizes reach 2^31 - 1: what passes them by part of a tile is formed unsigned.
   const int tiles_m = ((uint32_t)M + C::BM - 1) / C::BM, tiles_n = ((uint32_t)a.N + C::OUTN - 1) / C::OUTN;
-  const int total = a.L * tiles_m * tiles_n * a.S;
+  const int total = a.L * tiles_m * tiles_n * S;
   const int KT1 = ((uint32_t)K + C::KE - 1) / C::KE, KT = C::NSEG * KT1;
   const int lda = (int)a.lda, ldb = (int)a.ldb;
 
@@ -230,14 +239,14 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
   Item it;
   int m0 = 0, n0 = 0, ks0 = 0, KS = 0;
   auto setup = [&](int work) {
-    it = item_of(work, total, a.S, a.L, tiles_m, tiles_n);
+    it = item_of(work, total, S, a.L, tiles_m, tiles_n);
     m0 = it.tm * C::BM;
     n0 = it.tn * C::OUTN;
     ks0 = 0;
     KS = KT;
     if (SPLIT) {   // S slices; S <= 16 and KT <= 2^25 (the rows of a weight gradient), so 32 bits hold S * KT
-      ks0 = (uint32_t)(it.s * KT) / (uint32_t)a.S;
-      KS = (uint32_t)((it.s + 1) * KT) / (uint32_t)a.S - ks0;
+      ks0 = (uint32_t)(it.s * KT) / (uint32_t)S;
+      KS = (uint32_t)((it.s + 1) * KT) / (uint32_t)S - ks0;
     }
   };
 
@@ -565,8 +574,8 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
             if (m < M && n < pitch) {
 #pragma unroll
               for (int w = 0; w < W; ++w) {
-                const int64_t plane = ((int64_t)it.l * a.S + it.s) * W + w;
-                *reinterpret_cast<sumv*>(static_cast<sum_t*>(a.P) + (plane * a.M + m) * pitch + n) =
+                const int64_t plane = ((int64_t)it.l * S + it.s) * W + w;
+                *reinterpret_cast<sumv*>(static_cast<sum_t*>(a.P) + (plane * M + m) * pitch + n) =
                     sumv{g[k][w * V], g[k][w * V + 1], g[k][w * V + 2], g[k][w * V + 3]};
               }
             }

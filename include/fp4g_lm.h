@@ -105,8 +105,9 @@ fp4g_status cross_entropy_gemm_backward(int64_t M, int64_t V, int64_t K, const f
  * base[M][N]: with i = index[m],
  *   D[m] = base[m] + scales[i] * B[i] (A[i] X[m])
  * for bf16 X[M][K], A[L][R][K], B[L][N][R] and fp32 scales[L] (NULL: 1).  Sums and the R
- * values between the products are fp32 (these enter the second product as two bf16 terms,
- * which keep 16 bits of each); base and D are fp32 or bf16 by d_type, rounded once.  A row
+ * values between the products are fp32 (these enter the second product as bf16 terms that add
+ * up to them: two, which keep 16 bits, for bf16 results, and three, which keep all, for
+ * fp32); base and D are fp32 or bf16 by d_type, rounded once.  A row
  * whose index is outside 0 .. L-1 has no adapter: D[m] = base[m], and its X is not looked at.
  * D may be base itself.  K and R are multiples of 8, R at most 256, K at most 2^21, L at most
  * 8192, M at most 2^25, N at most 2^30 (FP4G_EUNSUPPORTED).  X, A and B are 16-byte aligned,

@@ -1,9 +1,9 @@
 """Low-rank adapters beside a shared projection against the formula in 64 bits.
 
 Tolerance.  u = 2^-24, e the half step of the results' type (2^-24 or 2^-8).  V = A x is a sum of K products in fp32, off by
-(K + 8) u |A| |x|; scaling rounds it once; its two bf16 terms keep it to 2^-16 (half a step of half a step); the second
-product adds 2 R terms in fp32, and D is rounded once, from a sum that may itself be rounded:
-    |B| dV + (2 R + 8) u |B| |V| + u (|base| + |D|) + e |D|,   dV = (K + 8) u s |A| |x| + (2^-16 + 2 u) |V|.
+(K + 8) u |A| |x|; scaling rounds it once; its bf16 terms keep it to 2^-8 each: two for bf16 results, three for fp32; the
+second product adds up to 3 R terms in fp32, and D is rounded once, from a sum that may itself be rounded:
+    |B| dV + (3 R + 8) u |B| |V| + u (|base| + |D|) + e |D|,   dV = (K + 8) u s |A| |x| + (2^-16 or 2^-24, + 2 u) |V|.
 """
 import pytest
 import torch
@@ -50,9 +50,9 @@ def formula(base, x, a, b, index, scales):
         s = 1.0 if scales is None else scales[i].double()
         xd, ad, bd = x[at].double(), a[i].double(), b[i].double()
         v = xd @ ad.t() * s
-        dv = (k + 8) * U * s * (xd.abs() @ ad.abs().t()) + (2.0 ** -16 + 2 * U) * v.abs()
+        dv = (k + 8) * U * s * (xd.abs() @ ad.abs().t()) + ((2.0 ** -16 if base.dtype == BF else U) + 2 * U) * v.abs()
         ref[at] += v @ bd.t()
-        tol[at] += dv @ bd.abs().t() + (2 * r + 8) * U * (v.abs() @ bd.abs().t())
+        tol[at] += dv @ bd.abs().t() + (3 * r + 8) * U * (v.abs() @ bd.abs().t())
     return ref, tol + (U + HALF[base.dtype]) * ref.abs() + 2.0 ** -133
 
 
