@@ -482,14 +482,17 @@ struct Plan {
   int tm;
   int64_t tiles, S;
 };
-Plan plan_of(int64_t M, int64_t K, int64_t R, int64_t L) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   Plan p;
   p.direct = M <= kDirect;
-  p.tm = p.direct ? 16 : 64;
+  // 64 tokens share an adapter's reads, 16 leave more tiles.  In us, 16 and 64: 642 x 795 x 5648
+  // rank 24 16.4, 25.2; 4000 x 2000 x 2048 rank 128 66.6, 73.9; 2000 x 8000 x 4096 rank 32
+  // 40.4, 41.4; 4096 x 14336 x 4096 rank 64 151, 113.
+  p.tm = p.direct || M * N < (int64_t)1 << 25 ? 16 : 64;
   p.tiles = std::min(M, ceil_div(M, p.tm) + L);   // an adapter's last tile may be short; so may that of none
   // Two units of 128 bytes of K a wave at least, and workgroups for the chip.
   const int64_t units = ceil_div(K, 64), work = p.tiles * std::max<int64_t>(1, ceil_div(R, 64));
-  p.S = std::max<int64_t>(1, std::min({units / 8, 4 * device_cus() / work, (int64_t)(p.direct ? 16 : 4)}));
+  p.S = std::max<int64_t>(1, std::min({units / 8, 4 * device_cus() / work, (int64_t)(p.tiles < 64 ? 16 : 4)}));
   return p;
 }
 
@@ -513,6 +516,13 @@ struct AdapterSpace {
         order(s.take<int>(plan.direct ? 0 : M)), count(s.take<int>(1)), tiles(s.take<Tile>(plan.direct ? 0 : plan.tiles)) {}
 };
 
+template <int TM, bool DIRECT>
+hipError_t launch_down(int64_t grid, hipStream_t s, const Args& a) {
+  if (a.R <= 16) return launch(adapter_down_kernel<TM, 1, DIRECT>, grid, 256, s, a);
+  if (a.R <= 32) return launch(adapter_down_kernel<TM, 2, DIRECT>, grid, 256, s, a);
+  return launch(adapter_down_kernel<TM, 4, DIRECT>, grid, 256, s, a);
+}
+
 template <int TM, bool DIRECT, bool BF16>
 hipError_t launch_up(int64_t grid, hipStream_t s, const Args& a, int shares) {
   if (a.R <= 64) return launch(adapter_up_kernel<TM, 64, DIRECT, BF16>, grid, 256, s, a, shares);
@@ -522,36 +532,37 @@ hipError_t launch_up(int64_t grid, hipStream_t s, const Args& a, int shares) {
 
 }  // namespace
 
-int64_t adapter_bytes(int64_t M, int64_t K, int64_t R, int64_t L) {
-  return AdapterSpace(nullptr, M, R, plan_of(M, K, R, L)).s.used;
+int64_t adapter_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+  return AdapterSpace(nullptr, M, R, plan_of(M, N, K, R, L)).s.used;
 }
 
 hipError_t launch_adapter_gemm(const AdapterCall& c, hipStream_t s) {
   // Without adapters, rows of them or columns every token is one without.
   const int64_t L = c.K > 0 && c.R > 0 ? c.L : 0;
   if (L == 0 && c.D == c.base) return hipSuccess;
-  const Plan p = plan_of(c.M, c.K, c.R, c.L);
+  const Plan p = plan_of(c.M, c.N, c.K, c.R, c.L);
   const AdapterSpace w(c.space, c.M, c.R, p);
   Args a{(int)c.M, (int)c.N, (int)c.K, (int)c.R, (int)L, (int)p.S, static_cast<const uint8_t*>(c.X),
          static_cast<const uint8_t*>(c.A), static_cast<const uint8_t*>(c.B), c.scales, c.index, c.base, c.D, w.V,
          w.tiles, w.order, w.count, 1};
   hipError_t e = hipSuccess;
   if (!p.direct)
-    e = launch(adapter_order_kernel<64>, 1, kOrderThreads, s, a.M, a.L, c.index, w.rank, w.order, w.tiles, w.count);
+    e = launch(p.tm == 16 ? adapter_order_kernel<16> : adapter_order_kernel<64>, 1, kOrderThreads, s, a.M, a.L, c.index,
+               w.rank, w.order, w.tiles, w.count);
   if (e == hipSuccess && L > 0) {
     const int64_t grid = p.tiles * ceil_div(c.R, 64) * p.S;
-    if (c.R <= 16) e = launch(p.direct ? adapter_down_kernel<16, 1, true> : adapter_down_kernel<64, 1, false>, grid, 256, s, a);
-    else if (c.R <= 32) e = launch(p.direct ? adapter_down_kernel<16, 2, true> : adapter_down_kernel<64, 2, false>, grid, 256, s, a);
-    else e = launch(p.direct ? adapter_down_kernel<16, 4, true> : adapter_down_kernel<64, 4, false>, grid, 256, s, a);
+    if (p.direct) e = launch_down<16, true>(grid, s, a);
+    else e = p.tm == 16 ? launch_down<16, false>(grid, s, a) : launch_down<64, false>(grid, s, a);
   }
   if (e != hipSuccess) return e;
   const int64_t steps = ceil_div(c.N, 256), most = std::min(steps, ceil_div(4 * device_cus(), p.tiles));
   a.steps = (int)ceil_div(steps, most);
   const int shares = (int)ceil_div(steps, a.steps);
-  if (p.direct) return c.bf16 ? launch_up<16, true, true>(p.tiles * shares, s, a, shares)
-                              : launch_up<16, true, false>(p.tiles * shares, s, a, shares);
-  return c.bf16 ? launch_up<64, false, true>(p.tiles * shares, s, a, shares)
-                : launch_up<64, false, false>(p.tiles * shares, s, a, shares);
+  const int64_t grid = p.tiles * shares;
+  if (p.direct) return c.bf16 ? launch_up<16, true, true>(grid, s, a, shares) : launch_up<16, true, false>(grid, s, a, shares);
+  if (p.tm == 16)
+    return c.bf16 ? launch_up<16, false, true>(grid, s, a, shares) : launch_up<16, false, false>(grid, s, a, shares);
+  return c.bf16 ? launch_up<64, false, true>(grid, s, a, shares) : launch_up<64, false, false>(grid, s, a, shares);
 }
 
 }  // namespace fp4g

@@ -194,7 +194,7 @@ fp4g_status adapter_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
   const fp4g_status st = check_adapter_sizes(M, N, K, R, L);
   if (st != FP4G_OK) return st;
   if (!bytes) return FP4G_EINVAL;
-  *bytes = M == 0 || N == 0 ? 0 : (size_t)fp4g::adapter_bytes(M, K, R, L);
+  *bytes = M == 0 || N == 0 ? 0 : (size_t)fp4g::adapter_bytes(M, N, K, R, L);
   return FP4G_OK;
 }
 
@@ -213,7 +213,7 @@ fp4g_status adapter_gemm(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, 
   if (st != FP4G_OK) return st;
   st = check_buffers({unless(b, {D}), x, wa, wb, s, i}, {buf(D, M * N * e, e), buf(workspace, workspace_bytes)});
   if (st != FP4G_OK) return st;
-  if (workspace_bytes < (size_t)fp4g::adapter_bytes(M, K, R, L)) return FP4G_EINVAL;
+  if (workspace_bytes < (size_t)fp4g::adapter_bytes(M, N, K, R, L)) return FP4G_EINVAL;
   const fp4g::AdapterCall c{M, N, K, R, L, base, X, A, B, scales, index, D, e == 2, static_cast<uint8_t*>(workspace)};
   return finish(fp4g::launch_adapter_gemm(c, reinterpret_cast<hipStream_t>(stream)));
 }

@@ -249,9 +249,23 @@ typedef Tiles<BF, kProb, false, false, 1> Probabilities; // the same
 typedef Tiles<BF, kAccum, false, true, 1> GradInput;     // P W: W's rows are the contraction's
 typedef Tiles<BF, kCounted, true, true, 1> GradWeights;  // P^T X: both operands' rows are
 
-DensePlan forward_plan(int64_t M, int64_t V, int64_t K) {
-  return dense_plan_among(kOneGroup, M, V, 1, ceil_div(K, 64), 1);
+// The plans of this thread's last products, by their sizes and the GPU's compute units: a call and
+// its workspace query ask for the same few several times, and each is chosen in 0.3 to 0.5 us.
+DensePlan plan_among(uint32_t tiles, int64_t rows, int64_t cols, int64_t KT, int64_t cap) {
+  struct Kept { int64_t key[6]; DensePlan plan; };
+  static thread_local Kept kept[8] = {};
+  static thread_local unsigned turn = 0;
+  const int64_t key[6] = {tiles, rows, cols, KT, cap, device_cus()};
+  for (const Kept& k : kept)
+    if (std::equal(key, key + 6, k.key)) return k.plan;
+  Kept& k = kept[turn++ % 8];
+  k.plan = dense_plan_among(tiles, rows, cols, 1, KT, cap);
+  std::copy(key, key + 6, k.key);
+  return k.plan;
 }
+DensePlan plan_of(int64_t rows, int64_t cols, int64_t KT, int64_t cap) { return plan_among(~0u, rows, cols, KT, cap); }
+
+DensePlan forward_plan(int64_t M, int64_t V, int64_t K) { return plan_among(kOneGroup, M, V, ceil_div(K, 64), 1); }
 int wave_cols(DenseTile t) { return t == kTile256 ? 128 : 64; }
 
 // Parts of a workspace, each on a line of its own.
@@ -331,7 +345,7 @@ hipError_t launch_both(const LossArgs& x, const LossArgs& w, hipStream_t s) {
 }
 
 // dX's product over one piece of the vocabulary.
-DensePlan input_plan(int64_t M, int64_t K, int64_t cols) { return dense_plan(M, K, 1, ceil_div(cols, 64), kMaxSplits); }
+DensePlan input_plan(int64_t M, int64_t K, int64_t cols) { return plan_of(M, K, ceil_div(cols, 64), kMaxSplits); }
 
 struct GradSpace {
   Space s;
@@ -401,7 +415,7 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     p.M = (int)c.M, p.N = (int)n, p.K = (int)c.K;
     p.A[0] = w.picked.rows, p.B[0] = W, p.lda = p.ldb = c.K * 2, p.D[0] = w.prob, p.ldp = w.ldp;
     p.count = w.picked.count, p.target = w.picked.wanted, p.col0 = (int)v, p.lse2 = w.lse2, p.g = w.g;
-    e = launch_any<Probabilities, true, false>(p, dense_plan(c.M, n, 1, ceil_div(c.K, 64), 1).tile, s);
+    e = launch_any<Probabilities, true, false>(p, plan_of(c.M, n, ceil_div(c.K, 64), 1).tile, s);
     if (e != hipSuccess) return e;
 
     const DensePlan plan = input_plan(c.M, c.K, n);
@@ -415,7 +429,7 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;
     d.A[0] = w.prob, d.lda = w.ldp * 2, d.B[0] = w.picked.rows, d.ldb = c.K * 2;
     d.D[0] = static_cast<uint8_t*>(c.dW) + v * c.K * 2, d.count = w.picked.count;
-    const DensePlan weights = dense_plan(n, c.K, 1, ceil_div(c.M, 64), 1);
+    const DensePlan weights = plan_of(n, c.K, ceil_div(c.M, 64), 1);
     if (c.dX && c.dW && n == c.V && merges(plan, weights, c.M, n, c.K)) {
       e = launch_both(x, d, s);
     } else {

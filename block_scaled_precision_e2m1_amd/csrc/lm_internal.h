@@ -68,7 +68,7 @@ struct AdapterCall {
   uint8_t* space;
 };
 constexpr int64_t kMaxAdapters = 8192;   // counted in a workgroup's LDS
-int64_t adapter_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
+int64_t adapter_bytes(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L);
 hipError_t launch_adapter_gemm(const AdapterCall& c, hipStream_t s);
 
 }  // namespace fp4g

@@ -19,7 +19,8 @@ HALF = {BF: 2.0 ** -8, F32: U}
 SIZES = [  # M, N, K, R, L
     (1, 1, 8, 8, 1), (1, 4096, 4096, 16, 8), (3, 65, 72, 8, 2), (16, 129, 64, 24, 5), (17, 1000, 520, 16, 40), (64, 300, 1032, 64, 3),
     (100, 77, 136, 72, 100), (256, 513, 264, 128, 7), (257, 513, 264, 40, 7), (300, 1003, 2056, 256, 2), (1000, 130, 72, 16, 300),
-    (2000, 2000, 520, 64, 4), (1500, 260, 64, 8, 1)]
+    (2000, 2000, 520, 64, 4), (1500, 260, 64, 8, 1),
+    (3000, 12000, 72, 40, 9), (2600, 13001, 64, 136, 3)]
 
 
 def gen(seed):

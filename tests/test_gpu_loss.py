@@ -139,6 +139,18 @@ def test_one_row_takes_part_among_many():
     check(x, w, t, dl)
 
 
+@pytest.mark.parametrize("m,v,k,keep", [(512, 8192, 256, 60), (600, 20000, 64, 600), (600, 20000, 64, 1), (2100, 9000, 264, 130)])
+def test_few_rows_of_many_take_part(m, v, k, keep):
+    """The split of dX's sums follows the rows that are there: any number of them in the workspace of all."""
+    x, w, t, dl = inputs(m, v, k, 19, 0.0)
+    out = torch.randperm(m, generator=gen(20), device=DEV)[keep:]
+    t[out] = -100
+    most, _ = fp4.cross_entropy_gemm_backward_workspace_size(m, v, k)
+    space = torch.full((most + 64,), 255, dtype=torch.uint8, device=DEV)
+    check(x, w, t, dl, space[:most])
+    assert (space[most:] == 255).all()
+
+
 def test_targets_outside_the_vocabulary():
     x, w, t, dl = inputs(40, 300, 64, 6, 0.2)
     for at, bad in ((3, 300), (4, -1), (5, 1 << 40), (6, -(1 << 33))):
