@@ -72,7 +72,10 @@ enum Form { kScaled, kGated, kPlain, kLoss, kProb, kAccum, kCounted };
 
 // What the forms of a loss take besides (cross_entropy.hip).
 struct LossArgs : DenseArgs {
-  const int* count = nullptr;       // the rows of A and D (counted: K), known to the GPU alone; M (K) bounds it
+  // The rows of A and D (counted: K), known to the GPU alone; M (K) bounds it.  Loss: null where all
+  // M rows are taken, with the targets as they are (`every`, for N columns).
+  const int* count = nullptr;
+  const int64_t* every = nullptr;
   const int* map = nullptr;         // accum: the row of D that a row of the product is
   const int* target = nullptr;      // loss, prob: the wanted column of each row, -1 for none
   int col0 = 0;                     // the column that B's first row is
@@ -225,7 +228,9 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
   const int hi = lane >> 5, r32 = lane & 31;
   // Rows of the result, or the contraction's length, may be known to the GPU alone.
   int M = a.M, K = a.K;
-  if constexpr (C::FORM == kLoss || C::FORM == kProb || C::FORM == kAccum) M = *a.count;
+  if constexpr (C::FORM == kProb || C::FORM == kAccum) M = *a.count;
+  if constexpr (C::FORM == kLoss)
+    if (a.count) M = *a.count;
   if constexpr (C::FORM == kCounted) K = *a.count;
   int S = a.S;
   if constexpr (C::FORM == kAccum && SPLIT) S = splits_of(a, M);
@@ -461,7 +466,15 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
     }
     if constexpr (C::FORM == kLoss) {
 #pragma unroll
-      for (int i = 0; i < FI; ++i) want[i] = a.target[min(mw + i * 32 + r32, M - 1u)] - a.col0;
+      for (int i = 0; i < FI; ++i) {
+        const uint32_t m = min(mw + i * 32 + r32, M - 1u);
+        if (a.every) {
+          const int64_t t = a.every[m];
+          want[i] = t >= 0 && t < a.N ? (int)t : -1;
+        } else {
+          want[i] = a.target[m];
+        }
+      }
     }
     if constexpr (SCALED) {
 #pragma unroll

@@ -19,7 +19,8 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 U, B = 2.0 ** -24, 2.0 ** -8
 SIZES = [(1, 1, 8), (3, 65, 72), (7, 130, 64), (1, 5000, 256), (130, 257, 136), (64, 1000, 512), (301, 1003, 520), (5, 4099, 2056),
-         (16, 40000, 64), (257, 4099, 264), (700, 2050, 1024), (2100, 12000, 200)]
+         (16, 40000, 64), (257, 4099, 264), (700, 2050, 1024), (2100, 12000, 200),
+         (1100, 9000, 1024), (5000, 2000, 1024)]
 
 
 def gen(seed):
@@ -105,7 +106,7 @@ def test_pieces_of_any_length(m, v, k):
         fp4.cross_entropy_gemm(x, w, t, workspace=torch.empty(size - 16, dtype=torch.uint8, device=DEV))
 
 
-@pytest.mark.parametrize("m,v,k", [(9, 300, 64), (300, 2000, 256), (5000, 130, 64)])
+@pytest.mark.parametrize("m,v,k", [(9, 300, 64), (300, 2000, 256), (5000, 130, 64), (300, 30000, 1024)])
 def test_what_ignored_rows_hold_reaches_nothing(m, v, k):
     x, w, t, dl = inputs(m, v, k, 3, 0.5)
     t[0], t[m - 1] = -100, -100
