@@ -8,7 +8,7 @@
 
 namespace fp4g {
 
-// One product of the tile kernels (dense_gemm.hip).
+// One product of the tile kernels (dense_tile.hpp).
 struct DenseArgs {
   int M = 0, N = 0;            // rows and columns of each output
   int K = 0;                   // contraction length of one segment, in elements
