@@ -316,3 +316,19 @@ def test_rows_past_32_bits():
     d, _ = fp4.rms_norm_backward(x[-3:].clone(), x[-3:].clone(), w)
     torch.cuda.synchronize(DEV)
     assert torch.equal(dx[-3:], d) and torch.isfinite(dw.float()).all()
+
+
+def test_more_rows_than_one_launch_holds():
+    """2^27 + 3 rows of 8: sixteen lanes each, in two launches."""
+    rows = (1 << 27) + 3
+    x = torch.ones(rows, 8, dtype=BF, device=DEV)
+    x[-5:] = torch.randn(5, 8, generator=gen(16), device=DEV).to(BF)
+    y = fp4.rms_norm(x, eps=EPS)
+    alone = fp4.rms_norm(x[-5:].clone(), eps=EPS)
+    torch.cuda.synchronize(DEV)
+    assert torch.equal(y[-5:], alone) and (y[:-5] == 1).all()
+    del y
+    codes, scales = fp4.rms_norm_quantize(x, eps=EPS)
+    c, s = fp4.rms_norm_quantize(x[-5:].clone(), eps=EPS)
+    torch.cuda.synchronize(DEV)
+    assert torch.equal(codes[-5:], c) and torch.equal(scales[-5:], s) and (codes[:-5] == 127).all()

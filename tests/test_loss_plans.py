@@ -1,0 +1,21 @@
+"""The sizes of loss_plans.py reach the kernels that they are listed for (no GPU needed)."""
+import pytest
+import torch
+
+from tests import loss_plans as plans
+from tests.ffn_plans import TILES
+
+
+@pytest.mark.skipif(torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 256,
+                    reason="the plans are for 256 compute units")
+def test_sizes_reach_their_kernels():
+    for size, *want in plans.SIZES:
+        assert list(plans.products(*size)) == want, size
+
+
+def test_every_tile_is_reached():
+    forward, prob, x, w = (set(p[i] for p in plans.SIZES) for i in range(1, 5))
+    assert forward == {"256", "128", "64x128", "64x128Long"}
+    assert prob == set(TILES)
+    assert x == {(t, s) for t in TILES for s in (False, True)} | {plans.BOTH, plans.BOTH_SPLIT}
+    assert w == set(TILES) | {plans.BOTH, plans.BOTH_SPLIT}
