@@ -420,13 +420,14 @@ __global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(int M, int
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, buckets = L + 1;
   for (int b = tid; b < buckets; b += kOrderThreads) counts[b] = 0;
   __syncthreads();
-  int ahead = tid < M ? index[tid] : 0;
-  for (int64_t m0 = 0; m0 < M; m0 += kOrderThreads) {
-    const int64_t m = m0 + tid;
-    const int now = ahead;
-    if (m + kOrderThreads < M) ahead = index[m + kOrderThreads];
-    const int id = m < M ? adapter_of(now, L) : -2, bucket = id < 0 ? L : id;
-    bool left = id != -2;
+  // The first tokens' buckets and ranks stay in registers, their indexes are all asked for at once.
+  constexpr int KEEP = 4;
+  int kept[KEEP], ranks[KEEP];
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) kept[i] = i * kOrderThreads + tid < M ? index[i * kOrderThreads + tid] : 0;
+  auto ranked = [&](int i, bool there) {
+    const int id = adapter_of(i, L), bucket = id < 0 ? L : id;
+    bool left = there;
     int at = 0;
     // Neighbours mostly share an adapter: two of a wave's adapters are counted at once, the
     // others one by one.
@@ -445,6 +446,16 @@ __global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(int M, int
       }
     }
     if (left) at = atomicAdd(&counts[bucket], 1);
+    return at;
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    ranks[i] = 0;
+    if (i * kOrderThreads < M) ranks[i] = ranked(kept[i], i * kOrderThreads + tid < M);
+  }
+  for (int64_t m0 = KEEP * kOrderThreads; m0 < M; m0 += kOrderThreads) {
+    const int64_t m = m0 + tid;
+    const int at = ranked(m < M ? index[m] : 0, m < M);
     if (m < M) rank[m] = at;
   }
   __syncthreads();
@@ -470,10 +481,14 @@ __global__ void __launch_bounds__(kOrderThreads) adapter_order_kernel(int M, int
   }
   if (tid == kOrderThreads - 1) *count = start.y;
   __syncthreads();
-  for (int64_t m = tid; m < M; m += kOrderThreads) {
-    const int id = adapter_of(index[m], L);
-    order[counts[id < 0 ? L : id] + rank[m]] = (int)m;
-  }
+  auto place = [&](int64_t m, int i, int at) {
+    const int id = adapter_of(i, L);
+    order[counts[id < 0 ? L : id] + at] = (int)m;
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i)
+    if (i * kOrderThreads + tid < M) place(i * kOrderThreads + tid, kept[i], ranks[i]);
+  for (int64_t m = KEEP * kOrderThreads + tid; m < M; m += kOrderThreads) place(m, index[m], rank[m]);
 }
 
 // How a call is cut up: tokens a tile, tiles at most, K slices, columns' shares.
@@ -490,9 +505,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   // 40.4, 41.4; 4096 x 14336 x 4096 rank 64 151, 113.
   p.tm = p.direct || M * N < (int64_t)1 << 25 ? 16 : 64;
   p.tiles = std::min(M, ceil_div(M, p.tm) + L);   // an adapter's last tile may be short; so may that of none
-  // Two units of 128 bytes of K a wave at least, and workgroups for the chip.
+  // Two units of 128 bytes of K a wave at least, and workgroups for the chip: of 64 tokens as many as
+  // it holds at once (4096 x 14336 x 4096 rank 64: 17 us with 3 slices, 25 with 4).
   const int64_t units = ceil_div(K, 64), work = p.tiles * std::max<int64_t>(1, ceil_div(R, 64));
-  p.S = std::max<int64_t>(1, std::min({units / 8, 4 * device_cus() / work, (int64_t)(p.tiles < 64 ? 16 : 4)}));
+  const int64_t room = p.tm == 64 ? device_cus() : 4 * device_cus();
+  p.S = std::max<int64_t>(1, std::min({units / 8, room / work, (int64_t)(p.tiles < 64 ? 16 : 4)}));
   return p;
 }
 
