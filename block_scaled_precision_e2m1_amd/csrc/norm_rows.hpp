@@ -1,7 +1,7 @@
 // Rows in registers: what the norm's kernels share.
 //
 // A row of K elements is walked in units of 16 bytes, L lanes a row and C units a lane, unit
-// u = lane + c * L.  L is 16, 32 or 64, four waves a workgroup, or 0: the whole workgroup, of any
+// u = lane + c * L.  L is 8 to 64, four waves a workgroup, or 0: the whole workgroup, of any
 // number of waves, so that a row leaves at most 63 lanes idle.  Rows start at any element (odd
 // K), so units are read and written as unaligned vectors, which cost nothing where they
 // happen to be aligned.  The last unit of a row may be short: it is read whole, into the next
@@ -157,7 +157,7 @@ __device__ __forceinline__ T over_row(T v, F f, T* part) {
   v = pair_step<1>(v, f);
   v = pair_step<2>(v, f);
   v = pair_step<4>(v, f);
-  v = pair_step<8>(v, f);
+  if constexpr (L == 0 || L >= 16) v = pair_step<8>(v, f);
   if constexpr (L == 0 || L >= 32) v = pair_step<16>(v, f);
   if constexpr (L == 0 || L >= 64) v = pair_step<32>(v, f);
   if constexpr (L == 0) {
