@@ -259,11 +259,13 @@ hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
                                  : rms_norm_kernel<BF16, WBF16, QUANT, false, L, C>,                      \
   block = L ? 256 : (int)(ceil_div(units, 64 * C) * 64), per = L ? 256 / (L + !L) : 1
   // Two units a lane: in us, (lanes, units), 131072 x 128 bf16 (8, 2) 12.4, (16, 1) 13.4, (4, 4) 15.5;
-  // 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.
+  // 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.  Few rows are bound by latency, and
+  // take one: 1003 x 1117 fp32 with a residual 5.2, with two 6.2.
   if (units <= 16) SHAPE(8, 2);
   else if (units <= 32) SHAPE(16, 2);
   else if (units <= 64) SHAPE(32, 2);
   else if (units <= 128) SHAPE(64, 2);
+  else if (units <= 512 && a.rows <= 2048) SHAPE(0, 1);
   else if (units <= 2048) SHAPE(0, 2);
   else if (units <= 4096) SHAPE(0, 4);
 #undef SHAPE
