@@ -84,6 +84,7 @@ struct LossArgs : DenseArgs {
   const float* lse2 = nullptr;      // prob: lse * log2(e) of each row
   const float* g = nullptr;         // prob: what each row is multiplied by
   int64_t ldp = 0;                  // prob: elements between rows of D, a multiple of 8
+  void* low = nullptr;              // prob: what D's rounding leaves, rounded itself, if it is wanted
   const float* add = nullptr;       // accum: [M][N] what is added to the product, if anything
   int bm = 1, most = 1;             // accum, split: rows of a tile, K slices at most
 };
@@ -616,6 +617,13 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
               }
               at = m * a.ldp + n;
               left = V;
+              if (a.low) {
+                float r[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                  r[e] = y[e] - __builtin_bit_cast(float, (uint32_t)f32_to_bf16_rne(y[e]) << 16);
+                store_cols<BF16>(a.low, at, left, r);
+              }
             }
             if constexpr (C::FORM == kAccum) {
               if (a.add) {

@@ -85,7 +85,8 @@ fp4g_status cross_entropy_gemm(int64_t M, int64_t V, int64_t K, const void *X, c
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* The gradients of cross_entropy_gemm from the incoming fp32 dL[M] and the lse it gave, both
- * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once,
+ * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once (for M of at most
+ * 128 to two bf16 terms, which keep 16 bits),
  *   dX[M][K] = P W,   dW[V][K] = P^T X   with fp32 sums.
  * P is formed for a piece of the vocabulary at a time, in the workspace: the query gives
  * `bytes`, with which pieces are large enough to fill the GPU, and `least`, the least a call

@@ -20,7 +20,8 @@ def products(m, v, k):
     among.restype, among.argtypes = Plan, [ctypes.c_uint32] + [ctypes.c_int64] * 5
     plan = internal("_ZN4fp4g10dense_planElllll", Plan, 5)
     forward, prob = among(ONE_GROUP, m, v, 1, -(-k // 64), 1), plan(m, v, 1, -(-k // 64), 1)
-    x, w = plan(m, k, 1, -(-v // 64), 16), plan(v, k, 1, -(-m // 64), 1)
+    terms = 2 if m <= 128 else 1                   # few rows: P in two terms along the contraction
+    x, w = plan(m, k, 1, terms * -(-v // 64), 16), plan(v, k, 1, terms * -(-m // 64), 1)
     fx, fw = TILES[x.tile], TILES[w.tile]
     items = (-(-m // 64) * x.S + -(-v // 64)) * -(-k // 64)
     if ROWS.get(fx, 64) == 64 and ROWS.get(fw, 64) == 64 and items + 8 <= 512:
@@ -30,28 +31,36 @@ def products(m, v, k):
 
 # More than one 64 x 64 tile and a ragged end in every dimension.
 SIZES = [
-    ((71, 68, 8240), '64x128Long', '64Long', ('64', False), '64'),
-    ((72, 24714, 72), '128', '128', ('64Long', True), '128'),
-    ((2747, 5167, 72), '256', '256', ('64x128Long', True), '64Long'),
-    ((66, 68, 72), '64x128', '64', BOTH, BOTH),
-    ((322, 68, 8568), '64x128Long', '64Long', ('128', False), '64x128'),
-    ((67, 4833, 648), '64x128', '64Deep', ('64x128', True), '128'),
-    ((69, 25882, 392), '64x128', '64x128', ('64Long', True), '256'),
-    ((67, 979, 80), '64x128', '64', BOTH_SPLIT, BOTH_SPLIT),
-    ((66, 14297, 72), '64x128', '64', ('64Deep', True), '64'),
-    ((67, 4360, 280), '64x128', '64', ('64', True), '64'),
-    ((67, 150, 8248), '64x128Long', '64Long', ('64x128', False), '64'),
-    ((514, 66, 3104), '64x128Long', '64Long', ('64', False), '64Deep'),
-    ((67, 596, 2720), '64x128Long', '64Long', ('64Deep', False), '64'),
-    ((66, 1094, 1680), '64x128Long', '64Long', ('64Long', False), '64'),
+    ((71, 68, 8240), '64x128Long', '64Long', ('64x128', False), '64x128'),
+    ((67, 2023, 456), '64x128', '64', ('64', True), '64'),
+    ((664, 4894, 72), '128', '128', ('64x128', True), '64Deep'),
+    ((386, 26319, 72), '256', '256', ('64Long', True), '64x128'),
+    ((67, 10655, 688), '64x128', '64x128', ('64x128Long', True), '128'),
     ((8345, 67, 1352), '64x128Long', '64x128Long', ('128', False), '64Long'),
-    ((6588, 66, 1824), '64x128Long', '64Long', ('256', False), '64Long'),
-    ((472, 25055, 72), '256', '256', ('64Long', True), '128Deep'),
     ((70, 25038, 488), '64x128', '128Deep', ('64Long', True), '256'),
-    ((131, 1286, 6048), '64x128Long', '64Long', ('64x128Long', False), '64x128'),
-    ((1317, 195, 4232), '64x128Long', '64Long', ('128', False), '64x128Long'),
-    ((1944, 450, 1552), '64x128Long', '64Long', ('128Deep', False), '64Long'),
-    ((68, 7982, 2768), '64x128Long', '64Long', ('128Deep', True), '128'),
+    ((67, 66, 528), '64x128', '64Deep', BOTH, BOTH),
+    ((129, 66, 6984), '64x128Long', '64Long', ('64', False), '64'),
+    ((1348, 16007, 72), '128', '128', ('128Deep', True), '64x128Long'),
     ((196, 3372, 8352), '64x128Long', '64Long', ('128', True), '256'),
     ((1602, 2759, 2536), '64x128', '64x128', ('256', True), '128'),
+    ((136, 67, 72), '64x128', '64', BOTH, BOTH),
+    ((68, 472, 72), '64x128', '64', BOTH_SPLIT, BOTH_SPLIT),
+    ((141, 1002, 72), '64x128', '64', BOTH_SPLIT, BOTH_SPLIT),
+    ((71, 70, 8080), '64x128Long', '64Long', ('64', False), '64'),
+    ((67, 4360, 280), '64x128', '64', ('64Deep', True), '64x128'),
+    ((69, 258, 4880), '64x128Long', '64Long', ('64Deep', False), '64x128'),
+    ((142, 130, 5536), '64x128Long', '64Long', ('64x128', False), '64x128'),
+    ((67, 596, 2720), '64x128Long', '64Long', ('64Long', False), '64x128'),
+    ((70, 2414, 648), '64x128', '64Deep', ('64x128', True), '64x128'),
+    ((138, 13229, 72), '128', '64', ('64Deep', True), '64x128'),
+    ((132, 2062, 520), '64x128', '64Deep', ('64', True), '64x128'),
+    ((132, 521, 2776), '64x128Long', '64Long', ('64Deep', False), '64x128'),
+    ((129, 1175, 1464), '64x128Long', '64Long', ('64Long', False), '64x128'),
+    ((71, 651, 8368), '64x128Long', '64Long', ('64x128Long', False), '128'),
+    ((6588, 66, 1824), '64x128Long', '64Long', ('256', False), '64Long'),
+    ((70, 8099, 1440), '64x128Long', '64Long', ('128Deep', True), '128'),
+    ((472, 25055, 72), '256', '256', ('64Long', True), '128Deep'),
+    ((131, 1286, 6048), '64x128Long', '64Long', ('64x128Long', False), '64x128'),
+    ((2747, 5167, 72), '256', '256', ('64x128Long', True), '64Long'),
+    ((1944, 450, 1552), '64x128Long', '64Long', ('128Deep', False), '64Long'),
 ]

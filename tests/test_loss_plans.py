@@ -14,8 +14,13 @@ def test_sizes_reach_their_kernels():
 
 
 def test_every_tile_is_reached():
-    forward, prob, x, w = (set(p[i] for p in plans.SIZES) for i in range(1, 5))
+    forward, prob = (set(p[i] for p in plans.SIZES) for i in (1, 2))
     assert forward == {"256", "128", "64x128", "64x128Long"}
     assert prob == set(TILES)
-    assert x == {(t, s) for t in TILES for s in (False, True)} | {plans.BOTH, plans.BOTH_SPLIT}
-    assert w == set(TILES) | {plans.BOTH, plans.BOTH_SPLIT}
+    many, few = ([p for p in plans.SIZES if (p[0][0] > 128) == b] for b in (True, False))
+    assert {p[3] for p in many} == {(t, s) for t in TILES for s in (False, True)} | {plans.BOTH, plans.BOTH_SPLIT}
+    assert {p[4] for p in many} == set(TILES) | {plans.BOTH, plans.BOTH_SPLIT}
+    # of few rows' tiles those that any size was found for
+    small = {"64", "64Deep", "64Long", "64x128", "64x128Long"}
+    assert {p[3] for p in few} >= {(t, s) for t in small for s in (False, True)} | {plans.BOTH, plans.BOTH_SPLIT}
+    assert {p[4] for p in few} >= {"64", "64x128", "128", "256", plans.BOTH, plans.BOTH_SPLIT}
