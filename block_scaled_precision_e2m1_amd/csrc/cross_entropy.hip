@@ -9,8 +9,8 @@
 //   * Forward, a tile's end leaves the maximum and the sum of the exponentials of each row over
 //     a wave's columns (8 bytes for 64 or 128 logits), and a last kernel joins them.
 //   * Backward, the vocabulary is taken in pieces.  A piece's logits are formed again and leave
-//     their tiles as P in bf16, the operand of both gradients' products; dW's rows of the piece
-//     are then whole, and dX is summed over the pieces in fp32.
+//     their tiles as P in bf16 (two terms of it for few rows), the operand of both gradients'
+//     products; dW's rows of the piece are then whole, and dX is summed over the pieces in fp32.
 //   * Rows without a loss (a prompt's tokens, padding) take no part: the rows that have one are
 //     gathered first, their number stays on the GPU, and the tiles read it there.  Half of
 //     the rows ignored is half of the time, and what an ignored row holds reaches nothing.
