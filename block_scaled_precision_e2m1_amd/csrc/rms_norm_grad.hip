@@ -40,6 +40,9 @@ __device__ __forceinline__ v4u grad_unit(const v4u& dy, const v4u& x, const WEIG
   return U::pack(d);
 }
 
+// c of a row.  s^2 itself leaves fp32's range where rows of about 1e20 or 1e-20 do not.
+__device__ __forceinline__ float projection(float s, float gx, int K) { return s * (s * (gx / (float)K)); }
+
 // The two sums of a row, in 64 bits and 32.
 struct __attribute__((packed, aligned(4))) Sums {
   double xx;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(L ? 256 : 1024) rms_norm_grad_kernel(const Gra
       if (lane + c * lanes < units) add_unit<BF16>(dy[c], x[c], w[c], &t);
     // Two sets of parts in turn: a wave is at most one row ahead of another's reads.
     t = over_row<L>(t, AddSums{}, parts[turn]);
-    const float s = inv_sqrt(t.xx / (double)a.K + a.eps), k = s * s * (t.gx / (float)a.K);
+    const float s = inv_sqrt(t.xx / (double)a.K + a.eps), k = projection(s, t.gx, a.K);
     const int64_t at = row * a.K * U::ELEM;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(1024) rms_norm_grad_sums_kernel(const Grad a) 
     if (threadIdx.x == 0) {
       const float s = inv_sqrt(t.xx / (double)a.K + a.eps);
       a.S[2 * row] = s;
-      a.S[2 * row + 1] = s * s * (t.gx / (float)a.K);
+      a.S[2 * row + 1] = projection(s, t.gx, a.K);
     }
   }
 }

@@ -60,9 +60,10 @@ fp4g_status rms_norm_quantize(int64_t rows, int64_t K, const void *X, int x_type
  * dY and, where it is not NULL, dH [rows][K], with X the rows that were normed (rms_norm's H
  * where it added a residual), g = dY * w and n = x * s, in fp32 with one rounding each:
  *   dX = s * (g - n * mean(g * n)) + dH,   dW = sum over rows of dY * n.
- * dY, dH and dX have X's type, dW has W's.  dW may be NULL and has to be where W is
- * (FP4G_EINVAL).  dX may be dY or dH itself.  The workspace is required (fewer bytes than
- * the query's are FP4G_EINVAL): it holds dW's partial sums.  rows == 0 zeroes dW. */
+ * mean(g * n) is s times the mean of g * x, whose sum has to be an fp32 number: it is for rows
+ * of up to about 1e33.  dY, dH and dX have X's type, dW has W's.  dW may be NULL and has to be
+ * where W is (FP4G_EINVAL).  dX may be dY or dH itself.  The workspace is required (fewer
+ * bytes than the query's are FP4G_EINVAL): it holds dW's partial sums.  rows == 0 zeroes dW. */
 fp4g_status rms_norm_backward_workspace_size(int64_t rows, int64_t K, int x_type, size_t *bytes);
 fp4g_status rms_norm_backward(int64_t rows, int64_t K, const void *dY, const void *X, int x_type,
                               const void *W, int w_type, double eps, const void *dH,

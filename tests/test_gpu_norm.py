@@ -183,6 +183,22 @@ def test_gradients(rows, k, t, wt, with_dh):
         close(dw, rw, near_w + (HALF[wt] + U) * rw.abs() + TINY[wt], "dW")
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 90, 2.0 ** -90])
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("rows,k", [(3, 24), (40, 128), (9, 1117), (5, 8192), (2, 40001)])
+def test_gradients_of_rows_whose_s_squared_leaves_the_range(rows, k, t, scale):
+    """s is about 2^-90 or 2^90 and its square no fp32 number; every value of the formula is one."""
+    print(f"case rms_norm_backward {rows}x{k} {t} scaled by {scale}", flush=True)
+    x, w, _ = inputs(rows, k, t, t, False, 5)
+    x = x * scale
+    dy = torch.randn(rows, k, generator=gen(6), device=DEV).to(t)
+    dx, dw = fp4.rms_norm_backward(dy, x, w, eps=0.0)
+    torch.cuda.synchronize(DEV)
+    rx, near, rw, near_w = gradients(dy, x, w, None, 0.0)
+    close(dx, rx, near + (HALF[t] + U) * rx.abs() + TINY[t], "dX")
+    close(dw, rw, near_w + (HALF[t] + U) * rw.abs() + TINY[t], "dW")
+
+
 def test_gradients_agree_with_differences():
     """The slope of sum(Y dY) + sum(H dH) along random directions, by central differences of the formula in 64 bits: at
     a step of 1e-5 these are off by about 1e-10 of the slope's terms, the fp32 gradients by 1e-6 of them."""
