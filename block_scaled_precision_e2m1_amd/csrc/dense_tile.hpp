@@ -162,8 +162,11 @@ __device__ __forceinline__ Item item_of(int wg, int total, int S, int L, int til
 }
 
 // The loss's end for one row of 32 of a wave: acc holds columns j * 32 + 8 g + 4 hi + e of row m.
-// A row's maximum is taken over what is there, so that e^(z - maximum) is at most 1; a logit of
-// -infinity gives 0, +infinity and NaN give NaN.
+// A row's maximum is taken over what is there and subtracted before anything is scaled: its own
+// term is exactly 1, so that the logarithm of a row's sum is not negative, and the terms' errors go by
+// the logits' differences, not by their size.  (With the scaled maximum folded into one multiply-add
+// the loss of a certain token at a logit of 3000 came out at up to +-1.6e-4.)  A logit of -infinity
+// gives 0, +infinity and NaN give NaN.
 template <class C, class ARGS, class ACC>
 __device__ __forceinline__ void loss_end(const ARGS& a, const ACC (&acc)[C::FJ], int64_t m, int M, uint32_t nw, int want,
                                          int hi, uint8_t* row) {
@@ -200,7 +203,7 @@ __device__ __forceinline__ void loss_end(const ARGS& a, const ACC (&acc)[C::FJ],
 #pragma unroll
   for (int e = 1; e < E; ++e) most = fmaxf(most, z[e]);
   most = fmaxf(most, __shfl_xor(most, 32));
-  const float from = most == -__builtin_inff() ? 0.0f : most * -kLog2e;
+  const float from = most == -__builtin_inff() ? 0.0f : most;
   const uint32_t at = (uint32_t)want - nw - 4u * hi;   // the wanted column, if it is this lane's
   const bool here = m < M && at < (uint32_t)C::WN && (at & 4) == 0;
   if (__any(here)) {
@@ -211,7 +214,7 @@ __device__ __forceinline__ void loss_end(const ARGS& a, const ACC (&acc)[C::FJ],
   }
   float sum[4] = {};
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum[e % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], kLog2e, from));
+  for (int e = 0; e < E; ++e) sum[e % 4] += __builtin_amdgcn_exp2f((z[e] - from) * kLog2e);
   float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   total += __shfl_xor(total, 32);
   if (m < M && hi == 0) a.parts[(int64_t)(nw / C::WN) * a.M + m] = make_float2(most, total);
