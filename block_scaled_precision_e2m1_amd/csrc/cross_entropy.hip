@@ -37,7 +37,7 @@ struct Pick {
   float *loss, *lse;              // forward: 0 for the rows that take no part
   float* z;                       // forward: the wanted logit, NaN until it is found
   const float *dL, *lse_in;       // backward: taken to the rows that take part
-  float *g, *lse2;
+  float *g, *lse_out;
   v4i* dX;                        // backward: 0 for the rows that take no part
 };
 constexpr int kChunk = 1024;
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
     a.wanted[slot] = known ? (int)t : -1;
     if constexpr (GRAD) {
       a.g[slot] = known ? a.dL[m] : __builtin_nanf("");
-      a.lse2[slot] = a.lse_in[m] * kLog2e;
+      a.lse_out[slot] = a.lse_in[m];
     } else {
       a.z[slot] = __builtin_nanf("");
     }
@@ -389,11 +389,11 @@ DensePlan input_plan(int64_t M, int64_t K, int64_t cols) {
 struct GradSpace {
   Space s;
   Picked picked;
-  float *g, *lse2, *kept, *P;
+  float *g, *lse, *kept, *P;
   int64_t ldp;
   uint8_t* prob;
   GradSpace(uint8_t* p, int64_t M, int64_t V, int64_t K, int64_t cols)
-      : s{p}, picked(s, M, K), g(s.take<float>(M)), lse2(s.take<float>(M)),
+      : s{p}, picked(s, M, K), g(s.take<float>(M)), lse(s.take<float>(M)),
         kept(s.take<float>(cols < V ? M * K : 0)), P(nullptr), ldp(ceil_div(cols, 64) * 64),
         prob(s.take<uint8_t>(terms_of(M) * M * ldp * 2)) {
     // Pieces differ by their last one, which may split further.
@@ -451,7 +451,7 @@ int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K) {
 hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
   const GradSpace w(c.space, c.M, c.V, c.K, c.cols);
   Pick k = pick_of(c, w.picked);
-  k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse2 = w.lse2, k.dX = static_cast<v4i*>(c.dX);
+  k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse_out = w.lse, k.dX = static_cast<v4i*>(c.dX);
   hipError_t e = launch_pick(k, w.picked.counts, true, s);
   if (e != hipSuccess) return e;
   const int terms = terms_of(c.M);
@@ -461,7 +461,7 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     LossArgs p;
     p.M = (int)c.M, p.N = (int)n, p.K = (int)c.K;
     p.A[0] = w.picked.rows, p.B[0] = W, p.lda = p.ldb = c.K * 2, p.D[0] = w.prob, p.ldp = w.ldp;
-    p.count = w.picked.count, p.target = w.picked.wanted, p.col0 = (int)v, p.lse2 = w.lse2, p.g = w.g;
+    p.count = w.picked.count, p.target = w.picked.wanted, p.col0 = (int)v, p.lse = w.lse, p.g = w.g;
     uint8_t* const low = terms == 2 ? w.prob + c.M * w.ldp * 2 : nullptr;
     p.low = low;
     e = launch_any<Probabilities, true, false>(p, plan_of(c.M, n, ceil_div(c.K, 64), 1).tile, s);

@@ -81,7 +81,7 @@ struct LossArgs : DenseArgs {
   int col0 = 0;                     // the column that B's first row is
   float2* parts = nullptr;          // loss: [wave's columns][M] maximum and sum
   float* wanted = nullptr;          // loss: [M] z of the wanted column
-  const float* lse2 = nullptr;      // prob: lse * log2(e) of each row
+  const float* lse = nullptr;       // prob: lse of each row
   const float* g = nullptr;         // prob: what each row is multiplied by
   int64_t ldp = 0;                  // prob: elements between rows of D, a multiple of 8
   void* low = nullptr;              // prob: what D's rounding leaves, rounded itself, if it is wanted
@@ -469,7 +469,7 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
 #pragma unroll
       for (int i = 0; i < FI; ++i) {
         const uint32_t m = min(mw + i * 32 + r32, M - 1u);
-        rows_of[i] = v4f{a.lse2[m], a.g[m], __builtin_bit_cast(float, a.target[m] - a.col0), 0.0f};
+        rows_of[i] = v4f{a.lse[m], a.g[m], __builtin_bit_cast(float, a.target[m] - a.col0), 0.0f};
       }
     }
     if constexpr (C::FORM == kLoss) {
@@ -611,11 +611,14 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
             int64_t at = m * a.N + n;
             int left = a.N - (int)n;
             if constexpr (C::FORM == kProb) {
-              // Past the last column zeros, up to a whole group: P's rows are operands.
+              // Past the last column zeros, up to a whole group: P's rows are operands.  lse is subtracted
+              // before anything is scaled: where the wanted token is certain, p - 1 is what roundings
+              // leave, and that of a scaled lse would add as much again as that of lse itself
+              // (logits of 3000 to 4500 that are lse itself gave P = 2e-4 dL in place of 0).
               const uint32_t want = __builtin_bit_cast(uint32_t, (float)of[k][2]) - n;
 #pragma unroll
               for (int e = 0; e < V; ++e) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(y[e], kLog2e, -of[k][0])) - ((uint32_t)e == want ? 1.0f : 0.0f);
+                const float p = __builtin_amdgcn_exp2f((y[e] - of[k][0]) * kLog2e) - ((uint32_t)e == want ? 1.0f : 0.0f);
                 y[e] = e < left ? p * of[k][1] : 0.0f;
               }
               at = m * a.ldp + n;

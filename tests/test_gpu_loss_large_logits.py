@@ -70,3 +70,18 @@ def test_the_loss_goes_by_differences(m, v, k, top):
     tol = (v / 1024 + 100 + 4 * 16) * U + 8 * U * (want + 16)
     err = (loss.double() - want).abs()
     assert (err <= tol).all(), f"off by {err.max().item():.3g}, allowed {tol.max().item():.3g}"
+
+
+@pytest.mark.parametrize("top", TOPS)
+@pytest.mark.parametrize("m,v,k", [s for s in SIZES if s[1] != 66] + [(200, 66, 528), (129, 2000, 136)])
+def test_a_confident_token_has_no_gradient(m, v, k, top):
+    """lse is the wanted logit itself and so exact: p - 1 is 0, but for one step of the exponential, and the other
+    tokens' p are below e^-40.  P is then at most 2 u dL + V e^-40 dL and what it gives, with weights of 1 and rows of
+    1.5 top, at most that many times over."""
+    print(f"case cross_entropy_gemm_backward {m}x{v}x{k} logits of {top}", flush=True)
+    x, w, t = confident(m, v, k, top)
+    lse = torch.where(t == -100, torch.full_like(x[:, 3], 7), x[:, 3]).float()
+    dx, dw = fp4.cross_entropy_gemm_backward(torch.ones(m, device=DEV), x, w, t, lse)
+    torch.cuda.synchronize(DEV)
+    assert dx.float().abs().max() <= 2.5 * U, dx.float().abs().max().item()
+    assert dw.float().abs().max() <= 2.5 * U * 1.5 * top * m, dw.float().abs().max().item()
