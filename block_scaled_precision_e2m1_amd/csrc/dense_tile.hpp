@@ -626,8 +626,11 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
               if (a.low) {
                 float r[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e)
+                for (int e = 0; e < V; ++e) {
+                  // An infinity or NaN is in the first term alone: less itself it would be NaN.
                   r[e] = y[e] - __builtin_bit_cast(float, (uint32_t)f32_to_bf16_rne(y[e]) << 16);
+                  if (!(__builtin_fabsf(r[e]) < __builtin_inff())) r[e] = 0.0f;
+                }
                 store_cols<BF16>(a.low, at, left, r);
               }
             }
