@@ -10,6 +10,7 @@
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 
@@ -30,6 +31,15 @@ struct Raised {};
 
 [[noreturn]] void type_error(const std::string& what) { throw Refused{PyExc_TypeError, what}; }
 [[noreturn]] void value_error(const std::string& what) { throw Refused{PyExc_ValueError, what}; }
+
+// Forward-mode derivatives: a tensor that carries one does not say so in requires_grad, and read by its
+// pointer it would lose it without a word.  The error is torch's own for a function that has none.
+[[maybe_unused]] void no_tangents(const char* fn, std::initializer_list<const at::Tensor*> ts) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+  for (const at::Tensor* t : ts)
+    if (t->defined() && t->_fw_grad(0).defined())
+      throw Refused{PyExc_NotImplementedError, std::string(fn) + " has no forward-mode derivative"};
+}
 
 std::string dtype_name(at::ScalarType t) {
   switch (t) {

@@ -119,8 +119,10 @@ PyObject* py_gated_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int act = activation(v[3]);
     const int save = PyObject_IsTrue(v[4]);
     if (save < 0) throw Raised{};
+    no_tangents("gated_gemm", {&X, &Wg, &Wu});
     if (c10::GradMode::is_enabled() && (X.requires_grad() || Wg.requires_grad() || Wu.requires_grad())) Py_RETURN_NONE;
     const at::Tensor H = result(v[5], "out", at::kBFloat16, {M, N}, device);
+    no_tangents("gated_gemm", {&H});
     at::Tensor G, U;
     if (save) {
       G = empty({M, N}, at::kFloat, device);

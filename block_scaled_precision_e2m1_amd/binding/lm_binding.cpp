@@ -19,10 +19,11 @@ bool recorded(std::initializer_list<const at::Tensor*> ts) {
 }
 
 // A tensor of the caller's that is written: autograd learns of it where it is kept for a
-// backward pass, and it may not itself be waiting for a gradient.
-at::Tensor written(PyObject* given, const char* name, at::ScalarType dtype, at::IntArrayRef shape, at::Device device) {
+// backward pass, and it may not itself be waiting for a gradient or carry a tangent.
+at::Tensor written(const char* fn, PyObject* given, const char* name, at::ScalarType dtype, at::IntArrayRef shape, at::Device device) {
   const at::Tensor t = result(given, name, dtype, shape, device);
   if (given != Py_None) {
+    no_tangents(fn, {&t});
     if (recorded({&t})) value_error(std::string(name) + " requires a gradient");
     if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   }
@@ -77,12 +78,13 @@ PyObject* py_rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Device device = a.X.device();
     const c10::DeviceGuard guard(device);
     if (v[3] == Py_None && v[5] != Py_None) value_error("sum_out without a residual");
+    no_tangents("rms_norm", {&a.X, &a.W, &a.R});
     if (recorded({&a.X, &a.W, &a.R})) {
       if (v[4] != Py_None || v[5] != Py_None) value_error("out and sum_out are not taken where a gradient is recorded");
       Py_RETURN_NONE;
     }
-    const at::Tensor Y = written(v[4], "out", a.X.scalar_type(), {a.rows, a.K}, device);
-    if (a.R.defined()) a.H = written(v[5], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
+    const at::Tensor Y = written("rms_norm", v[4], "out", a.X.scalar_type(), {a.rows, a.K}, device);
+    if (a.R.defined()) a.H = written("rms_norm", v[5], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
     launch("rms_norm", device, [&](void* stream) {
       return rms_norm(a.rows, a.K, ptr(a.X), type_of(a.X), a.r(), a.w(), a.w_type, a.eps, a.h(), ptr(Y), stream);
     });
@@ -103,11 +105,12 @@ PyObject* py_rms_norm_quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
       value_error(std::string("codes must be \"int8\" or \"e4m3\"") + (name ? std::string(", got ") + name : ""));
     const bool keep = truth(v[5]);
     if (v[3] == Py_None && v[6] != Py_None) value_error("sum_out without a residual");
+    no_tangents("rms_norm_quantize", {&a.X, &a.W, &a.R});
     if (recorded({&a.X, &a.W, &a.R})) value_error("rms_norm_quantize has no gradient: call it under torch.no_grad()");
     const at::Tensor codes = empty({a.rows, a.K}, int8 ? at::kChar : at::kByte, device);
     const at::Tensor scales = empty({a.rows}, at::kFloat, device);
     at::Tensor Y;
-    if (a.R.defined()) a.H = written(v[6], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
+    if (a.R.defined()) a.H = written("rms_norm_quantize", v[6], "sum_out", a.X.scalar_type(), {a.rows, a.K}, device);
     if (keep) Y = empty({a.rows, a.K}, a.X.scalar_type(), device);
     launch("rms_norm_quantize", device, [&](void* stream) {
       return rms_norm_quantize(a.rows, a.K, ptr(a.X), type_of(a.X), a.r(), a.w(), a.w_type, a.eps, a.h(),
@@ -173,6 +176,7 @@ PyObject* py_cross_entropy_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Device device = a.X.device();
     const c10::DeviceGuard guard(device);
     const bool save = truth(v[4]);
+    no_tangents("cross_entropy_gemm", {&a.X, &a.W});
     if (recorded({&a.X, &a.W})) Py_RETURN_NONE;
     const at::Tensor loss = empty({a.M}, at::kFloat, device);
     at::Tensor lse;
@@ -236,8 +240,9 @@ PyObject* py_adapter_gemm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (v[5] != Py_None) scales = need(v[5], "scales", at::kFloat, {L}, device);
     multiple_of(K, 8);
     if (R % 8) value_error("R=" + std::to_string(R) + " must be a multiple of 8");
+    no_tangents("adapter_gemm", {&base, &X, &A, &B, &scales});
     if (recorded({&base, &X, &A, &B, &scales})) value_error("adapter_gemm has no gradient: call it under torch.no_grad()");
-    const at::Tensor D = written(v[6], "out", base.scalar_type(), {M, N}, device);
+    const at::Tensor D = written("adapter_gemm", v[6], "out", base.scalar_type(), {M, N}, device);
     const Space w = space(v[7], device, [&] {
       size_t bytes = 0;
       check_status("adapter_gemm_workspace_size", adapter_gemm_workspace_size(M, N, K, R, L, &bytes));

@@ -160,7 +160,8 @@ def gated_gemm(X, Wg, Wu, act="silu", save=False, out=None, workspace=None):
     products, which gated_gemm_backward takes.
 
     Differentiable in X, Wg and Wu: where one of them requires a gradient, G and U are kept for
-    the backward pass, and H carries the graph (G and U do not)."""
+    the backward pass, and H carries the graph (G and U do not).  A forward-mode tangent raises
+    NotImplementedError."""
     r = (_native or _binding()).gated_gemm(X, Wg, Wu, act, save, out, workspace)
     if r is None:
         r = _GatedGemm.apply(X, Wg, Wu, act, out, workspace)

@@ -14,8 +14,8 @@ Layouts (contiguous, all on one GPU):
   cross_entropy_gemm_backward  : the gradients of cross_entropy_gemm, bfloat16
   adapter_gemm       : base [M, N] float32 or bfloat16, X [M, K], A [L, R, K], B [L, N, R] bfloat16, index [M] int32
                        -> D like base
-K of the loss and K and R of the adapters are multiples of 8.  rms_norm and cross_entropy_gemm take part in autograd; the results of the other
-functions carry no graph.  The functions themselves may be captured into a graph at any time; a backward pass of autograd
+K of the loss and K and R of the adapters are multiples of 8.  rms_norm and cross_entropy_gemm take part in autograd, in
+reverse mode (a forward-mode tangent raises NotImplementedError); the results of the other functions carry no graph.  The functions themselves may be captured into a graph at any time; a backward pass of autograd
 only while no eager graph of the same leaves is alive, as everywhere in torch.
 """
 from __future__ import annotations
