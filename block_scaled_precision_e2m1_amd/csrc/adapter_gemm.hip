@@ -28,6 +28,7 @@ namespace fp4g {
 namespace {
 
 constexpr int kDirect = 256;      // tokens whose tiles need no order made beforehand
+constexpr float kBf16Max = 0x1.fep127f;
 
 struct Tile { int adapter, first, count, pad; };   // adapter -1: none
 
@@ -336,16 +337,23 @@ __global__ void __launch_bounds__(256, TM * RMAX < 64 * 256 || BF16 ? 2 : 1) ada
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] *= scale;
-    // Each term is what the ones before it leave, rounded to bf16; an infinity or NaN is in the
-    // first alone.
+    float c[4];
+    // Each term is what the ones before it leave, rounded to bf16.  The first is held to bf16's
+    // range, past which the end of fp32's would round to infinity; an infinity or NaN is then in
+    // what it leaves, and in the second term alone.
 #pragma unroll
     for (int n = 0; n < TERMS; ++n) {
-      const uint32_t w[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      if (n == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = __builtin_amdgcn_fmed3f(v[k], -kBf16Max, kBf16Max);
+      }
+      const uint32_t w[2] = {pack_bf16x2(c[0], c[1]), pack_bf16x2(c[2], c[3])};
       *reinterpret_cast<v2i*>(terms + (n * TM + m) * pitch + r * 2) = v2i{(int)w[0], (int)w[1]};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         v[k] -= __builtin_bit_cast(float, k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
-        if (!(__builtin_fabsf(v[k]) < __builtin_inff())) v[k] = 0.0f;
+        if (n > 0 && !(__builtin_fabsf(v[k]) < __builtin_inff())) v[k] = 0.0f;
+        c[k] = v[k];
       }
     }
   }
