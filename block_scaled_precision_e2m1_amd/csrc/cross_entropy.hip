@@ -381,10 +381,16 @@ hipError_t launch_products(const LossArgs& x, const DensePlan& px, bool last, co
   return e == hipSuccess && w.D[0] ? launch_any<GradWeights<TERMS>, true, false>(w, pw.tile, s) : e;
 }
 
-// dX's product over one piece of the vocabulary.
-DensePlan input_plan(int64_t M, int64_t K, int64_t cols) {
-  return plan_of(M, K, terms_of(M) * ceil_div(cols, 64), kMaxSplits);
+
+}  // namespace
+
+LossInputPlan loss_input_plan(int64_t M, int64_t K, int64_t cols) {
+  const int64_t KT = terms_of(M) * ceil_div(cols, 64);
+  const DensePlan plan = plan_of(M, K, KT, kMaxSplits);
+  return {plan, (int)std::min<int64_t>(kMaxSplits, std::max<int64_t>(plan.S, KT / 8))};
 }
+
+namespace {
 
 struct GradSpace {
   Space s;
@@ -399,7 +405,7 @@ struct GradSpace {
     // Pieces differ by their last one, which may split further.
     int64_t splits = 0;
     for (int64_t c : {std::min(cols, V), V % cols ? V % cols : cols}) {
-      const int64_t S = input_plan(M, K, std::min(c, V)).S;
+      const int64_t S = loss_input_plan(M, K, std::min(c, V)).plan.S;
       if (S > 1) splits = std::max(splits, S);
     }
     P = s.take<float>(splits * ceil_div(M, 256) * 256 * K);   // whole tiles: splits_of
@@ -467,14 +473,15 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     e = launch_any<Probabilities, true, false>(p, plan_of(c.M, n, ceil_div(c.K, 64), 1).tile, s);
     if (e != hipSuccess) return e;
 
-    const DensePlan plan = input_plan(c.M, c.K, n);
+    const LossInputPlan input = loss_input_plan(c.M, c.K, n);
+    const DensePlan& plan = input.plan;
     const bool last = v + n == c.V;
     LossArgs x, d;
     x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
     x.A[0] = w.prob, x.A[1] = low, x.lda = w.ldp * 2, x.B[0] = x.B[1] = W, x.ldb = c.K * 2, x.P = w.P;
     x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
     x.D[0] = !c.dX ? nullptr : last ? c.dX : w.kept;
-    x.bm = (int)tile_rows(plan.tile), x.most = (int)std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, terms * n / 512));
+    x.bm = (int)tile_rows(plan.tile), x.most = input.most;
     d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;
     d.A[0] = w.prob, d.A[1] = low, d.lda = w.ldp * 2, d.B[0] = d.B[1] = w.picked.rows, d.ldb = c.K * 2;
     if (c.dW) d.D[0] = static_cast<uint8_t*>(c.dW) + v * c.K * 2;

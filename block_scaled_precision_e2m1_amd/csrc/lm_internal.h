@@ -4,6 +4,7 @@
 #pragma once
 
 #include "../../include/fp4g_lm.h"
+#include "ffn_internal.h"
 #include "internal.h"
 
 namespace fp4g {
@@ -55,6 +56,12 @@ struct LossCall {
 int64_t loss_bytes(int64_t M, int64_t V, int64_t K);
 int64_t loss_grad_bytes(int64_t M, int64_t V, int64_t K, int64_t cols);
 int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K);
+// dX's product over a piece of `cols` columns of the vocabulary: its tile and K slices with all M
+// rows, and how many slices it may have where fewer rows take part (splits_of).  Never fewer than
+// planned: a plan's time is that of its slices, and its partial sums are paid for with any number.
+// More only of 8 stages or longer.
+struct LossInputPlan { DensePlan plan; int most; };
+LossInputPlan loss_input_plan(int64_t M, int64_t K, int64_t cols);
 hipError_t launch_loss(const LossCall& a, hipStream_t s);
 hipError_t launch_loss_grad(const LossCall& a, hipStream_t s);
 
