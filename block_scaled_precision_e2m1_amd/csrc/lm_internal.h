@@ -22,6 +22,8 @@ struct NormArgs {
   float* scales = nullptr;
   bool e4m3 = false;
 };
+// How many of the rows one launch takes.
+int64_t rms_norm_launch_rows(int64_t rows, int64_t K, bool bf16);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 
 struct NormGradArgs {

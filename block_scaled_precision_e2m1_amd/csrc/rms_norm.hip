@@ -249,35 +249,56 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const Rows a) {
   }
 }
 
+// Lanes a row (0: a workgroup) and units a lane; units 0: the rows are too long for any shape.
+struct Shape { int lanes, units; };
+// Two units a lane: in us, (lanes, units), 131072 x 128 bf16 (8, 2) 12.4, (16, 1) 13.4, (4, 4) 15.5;
+// 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.  Few rows are bound by latency, and
+// take one: 1003 x 1117 fp32 with a residual 5.2, with two 6.2.
+Shape shape_of(int64_t rows, int64_t units) {
+  if (units <= 16) return {8, 2};
+  if (units <= 32) return {16, 2};
+  if (units <= 64) return {32, 2};
+  if (units <= 128) return {64, 2};
+  if (units <= 512 && rows <= 2048) return {0, 1};
+  if (units <= 2048) return {0, 2};
+  if (units <= 4096) return {0, 4};
+  return {0, 0};
+}
+struct Launch { int block, per; int64_t most; };   // threads and rows of a workgroup, rows of a launch
+Launch launch_of(Shape h, int64_t units) {
+  Launch l{1024, 1, 0};
+  if (h.lanes) l.block = 256, l.per = 256 / h.lanes;
+  else if (h.units) l.block = (int)(ceil_div(units, 64 * h.units) * 64);
+  l.most = ((int64_t)1 << 31) / l.block * l.per;
+  return l;
+}
+
 template <bool BF16, bool WBF16, bool QUANT>
 hipError_t launch_rows(const NormArgs& a, hipStream_t s) {
   const int64_t units = ceil_div(a.K, Unit<BF16>::EPU), elem = Unit<BF16>::ELEM;
+  const Shape shape = shape_of(a.rows, units);
+  const Launch l = launch_of(shape, units);
   void (*kernel)(Rows) = rms_norm_long_kernel<BF16, WBF16, QUANT>;
-  int block = 1024, per = 1;
 #define SHAPE(L, C)                                                                                       \
-  kernel = a.K % Unit<BF16>::EPU ? rms_norm_kernel<BF16, WBF16, QUANT, true, L, C>                        \
-                                 : rms_norm_kernel<BF16, WBF16, QUANT, false, L, C>,                      \
-  block = L ? 256 : (int)(ceil_div(units, 64 * C) * 64), per = L ? 256 / (L + !L) : 1
-  // Two units a lane: in us, (lanes, units), 131072 x 128 bf16 (8, 2) 12.4, (16, 1) 13.4, (4, 4) 15.5;
-  // 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.  Few rows are bound by latency, and
-  // take one: 1003 x 1117 fp32 with a residual 5.2, with two 6.2.
-  if (units <= 16) SHAPE(8, 2);
-  else if (units <= 32) SHAPE(16, 2);
-  else if (units <= 64) SHAPE(32, 2);
-  else if (units <= 128) SHAPE(64, 2);
-  else if (units <= 512 && a.rows <= 2048) SHAPE(0, 1);
-  else if (units <= 2048) SHAPE(0, 2);
-  else if (units <= 4096) SHAPE(0, 4);
+  if (shape.lanes == L && shape.units == C)                                                               \
+    kernel = a.K % Unit<BF16>::EPU ? rms_norm_kernel<BF16, WBF16, QUANT, true, L, C>                      \
+                                   : rms_norm_kernel<BF16, WBF16, QUANT, false, L, C>
+  SHAPE(8, 2);
+  SHAPE(16, 2);
+  SHAPE(32, 2);
+  SHAPE(64, 2);
+  SHAPE(0, 1);
+  SHAPE(0, 2);
+  SHAPE(0, 4);
 #undef SHAPE
-  const int64_t most = ((int64_t)1 << 31) / block * per;
-  for (int64_t first = 0; first < a.rows; first += most) {
-    const int64_t n = std::min(a.rows - first, most), at = first * a.K;
+  for (int64_t first = 0; first < a.rows; first += l.most) {
+    const int64_t n = std::min(a.rows - first, l.most), at = first * a.K;
     auto past = [&](const void* p, int64_t bytes) {
       return p ? const_cast<uint8_t*>(static_cast<const uint8_t*>(p)) + bytes : nullptr;
     };
     const Rows r{n, (int)a.K, past(a.X, at * elem), past(a.R, at * elem), a.W, past(a.H, at * elem),
                  past(a.Y, at * elem), past(a.codes, at), a.scales ? a.scales + first : nullptr, a.eps, a.e4m3};
-    const hipError_t e = launch(kernel, ceil_div(n, per), block, s, r);
+    const hipError_t e = launch(kernel, ceil_div(n, l.per), l.block, s, r);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -289,6 +310,11 @@ hipError_t launch_out(const NormArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t rms_norm_launch_rows(int64_t rows, int64_t K, bool bf16) {
+  const int64_t units = ceil_div(K, bf16 ? 8 : 4);
+  return launch_of(shape_of(rows, units), units).most;
+}
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
   if (a.bf16) return a.w_bf16 ? launch_out<true, true>(a, s) : launch_out<true, false>(a, s);
