@@ -416,17 +416,19 @@ struct GradSpace {
 
 int64_t loss_bytes(int64_t M, int64_t V, int64_t K) { return ForwardSpace(nullptr, M, V, K).s.used; }
 
+// Gathering takes 4 us or more.  One tile's rows cost the same whether they take part or not, and
+// a product of 2^34 operations takes about 12 us with all of them: those take every row as it
+// is, and the join leaves out what takes no part (301 x 1003 x 520 with its gradients 32.7 us
+// with a gathering, 29.1 without).
+bool loss_gathers(int64_t M, int64_t V, int64_t K) { return M > 64 && (double)M * (double)V * (double)K > 8.6e9; }
+
 hipError_t launch_loss(const LossCall& c, hipStream_t s) {
   const ForwardSpace w(c.space, c.M, c.V, c.K);
   LossArgs a;
   a.M = (int)c.M, a.N = (int)c.V, a.K = (int)c.K;
   a.B[0] = static_cast<const uint8_t*>(c.W), a.lda = a.ldb = c.K * 2, a.parts = w.part, a.wanted = w.z;
   Join j{c.M, (int)w.parts, w.part, w.z, nullptr, nullptr, c.target, c.V, c.ignore, c.loss, c.lse};
-  // Gathering takes 4 us or more.  One tile's rows cost the same whether they take part or not, and
-  // a product of 2^34 operations takes about 12 us with all of them: those take every row as it
-  // is, and the join leaves out what takes no part (301 x 1003 x 520 with its gradients 32.7 us
-  // with a gathering, 29.1 without).
-  if (c.M <= 64 || (double)c.M * (double)c.V * (double)c.K <= 8.6e9) {
+  if (!loss_gathers(c.M, c.V, c.K)) {
     a.A[0] = static_cast<const uint8_t*>(c.X), a.every = c.target;
   } else {
     Pick k = pick_of(c, w.picked);

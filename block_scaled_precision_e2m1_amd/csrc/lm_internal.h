@@ -58,6 +58,8 @@ struct LossCall {
 int64_t loss_bytes(int64_t M, int64_t V, int64_t K);
 int64_t loss_grad_bytes(int64_t M, int64_t V, int64_t K, int64_t cols);
 int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K);
+// Whether the forward pass gathers the rows that take part; else its product takes every row.
+bool loss_gathers(int64_t M, int64_t V, int64_t K);
 // dX's product over a piece of `cols` columns of the vocabulary: its tile and K slices with all M
 // rows, and how many slices it may have where fewer rows take part (splits_of).  Never fewer than
 // planned: a plan's time is that of its slices, and its partial sums are paid for with any number.
