@@ -262,15 +262,10 @@ hipError_t launch_any(const LossArgs& a, DenseTile tile, hipStream_t s) {
 }
 typedef Tiles<BF, kLoss, false, false, 1> Forward;       // X W^T: both operands' rows hold K
 typedef Tiles<BF, kProb, false, false, 1> Probabilities; // the same
-// Of P in TERMS bf16 terms, one after the other along the contraction.
-template <int TERMS> using GradInput = Tiles<BF, kAccum, false, true, TERMS>;     // P W: W's rows are the contraction's
-template <int TERMS> using GradWeights = Tiles<BF, kCounted, true, true, TERMS>;  // P^T X: both operands' rows are
-// A gradient is mostly made of P at the wanted tokens.  Over many rows their roundings average
-// (0.0024 of a gradient's norm, of which the results' own rounding is 0.0017); over few they
-// would show by their luck (to 0.004), so P is kept in two terms there, and the products of
-// both are half of the backward pass's time more.
-constexpr int64_t kFewRows = 128;
-int terms_of(int64_t M) { return M <= kFewRows ? 2 : 1; }
+// Of P in one or two bf16 terms, by the rows that take part.
+typedef Tiles<BF, kAccum, false, true, 2> GradInput;     // P W: W's rows are the contraction's
+typedef Tiles<BF, kCounted, true, true, 2> GradWeights;  // P^T X: both operands' rows are
+int terms_of(int64_t M) { return M <= kFewRows ? 2 : 1; }   // with all rows, as products are planned
 
 // The plans of this thread's last products, by their sizes and the GPU's compute units: a call and
 // its workspace query ask for the same few several times, and each is chosen in 0.3 to 0.5 us.
@@ -355,12 +350,11 @@ int64_t tile_rows(DenseTile t) { return t == kTile256 ? 256 : t == kTile128 || t
 // its longest item, and the two run side by side.
 bool merges(const DensePlan& x, const DensePlan& w, int64_t M, int64_t cols, int64_t K) {
   const int64_t items = (ceil_div(M, 64) * x.S + ceil_div(cols, 64)) * ceil_div(K, 64);
-  return tile_rows(x.tile) == 64 && tile_rows(w.tile) == 64 && items + 8 <= device_cus() * GradInput<1>::t64_deep::OCC;
+  return tile_rows(x.tile) == 64 && tile_rows(w.tile) == 64 && items + 8 <= device_cus() * GradInput::t64_deep::OCC;
 }
-template <int TERMS>
 hipError_t launch_both(const LossArgs& x, const LossArgs& w, hipStream_t s) {
-  typedef typename GradInput<TERMS>::t64_deep X;
-  typedef typename GradWeights<TERMS>::t64_deep W;
+  typedef GradInput::t64_deep X;
+  typedef GradWeights::t64_deep W;
   // A multiple of 8 workgroups for x, so that the others' ids keep their XCDs.
   const int split = (int)(ceil_div(ceil_div(x.M, 64) * ceil_div(x.N, 64) * x.S, 8) * 8);
   const int64_t grid = split + ceil_div(w.M, 64) * ceil_div(w.N, 64);
@@ -368,17 +362,16 @@ hipError_t launch_both(const LossArgs& x, const LossArgs& w, hipStream_t s) {
 }
 // dX's and dW's products over a piece of the vocabulary, where they are wanted; a split dX is left in
 // its slices.
-template <int TERMS>
 hipError_t launch_products(const LossArgs& x, const DensePlan& px, bool last, const LossArgs& w, const DensePlan& pw,
                            bool both, hipStream_t s) {
-  if (both) return launch_both<TERMS>(x, w, s);
+  if (both) return launch_both(x, w, s);
   hipError_t e = hipSuccess;
   if (x.D[0]) {
-    if (px.S > 1) e = launch_any<GradInput<TERMS>, false, true>(x, px.tile, s);
-    else if (last) e = launch_any<GradInput<TERMS>, true, false>(x, px.tile, s);
-    else e = launch_any<GradInput<TERMS>, false, false>(x, px.tile, s);
+    if (px.S > 1) e = launch_any<GradInput, false, true>(x, px.tile, s);
+    else if (last) e = launch_any<GradInput, true, false>(x, px.tile, s);
+    else e = launch_any<GradInput, false, false>(x, px.tile, s);
   }
-  return e == hipSuccess && w.D[0] ? launch_any<GradWeights<TERMS>, true, false>(w, pw.tile, s) : e;
+  return e == hipSuccess && w.D[0] ? launch_any<GradWeights, true, false>(w, pw.tile, s) : e;
 }
 
 
@@ -397,11 +390,11 @@ struct GradSpace {
   Picked picked;
   float *g, *lse, *kept, *P;
   int64_t ldp;
-  uint8_t* prob;
+  uint8_t *prob, *low;
   GradSpace(uint8_t* p, int64_t M, int64_t V, int64_t K, int64_t cols)
       : s{p}, picked(s, M, K), g(s.take<float>(M)), lse(s.take<float>(M)),
         kept(s.take<float>(cols < V ? M * K : 0)), P(nullptr), ldp(ceil_div(cols, 64) * 64),
-        prob(s.take<uint8_t>(terms_of(M) * M * ldp * 2)) {
+        prob(s.take<uint8_t>(M * ldp * 2)), low(s.take<uint8_t>(std::min<int64_t>(M, kFewRows) * ldp * 2)) {
     // Pieces differ by their last one, which may split further.
     int64_t splits = 0;
     for (int64_t c : {std::min(cols, V), V % cols ? V % cols : cols}) {
@@ -462,7 +455,6 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
   k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse_out = w.lse, k.dX = static_cast<v4i*>(c.dX);
   hipError_t e = launch_pick(k, w.picked.counts, true, s);
   if (e != hipSuccess) return e;
-  const int terms = terms_of(c.M);
   for (int64_t v = 0; v < c.V; v += c.cols) {
     const int64_t n = std::min(c.cols, c.V - v);
     const uint8_t* W = static_cast<const uint8_t*>(c.W) + v * c.K * 2;
@@ -470,8 +462,7 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     p.M = (int)c.M, p.N = (int)n, p.K = (int)c.K;
     p.A[0] = w.picked.rows, p.B[0] = W, p.lda = p.ldb = c.K * 2, p.D[0] = w.prob, p.ldp = w.ldp;
     p.count = w.picked.count, p.target = w.picked.wanted, p.col0 = (int)v, p.lse = w.lse, p.g = w.g;
-    uint8_t* const low = terms == 2 ? w.prob + c.M * w.ldp * 2 : nullptr;
-    p.low = low;
+    p.low = w.low;
     e = launch_any<Probabilities, true, false>(p, plan_of(c.M, n, ceil_div(c.K, 64), 1).tile, s);
     if (e != hipSuccess) return e;
 
@@ -480,18 +471,17 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     const bool last = v + n == c.V;
     LossArgs x, d;
     x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
-    x.A[0] = w.prob, x.A[1] = low, x.lda = w.ldp * 2, x.B[0] = x.B[1] = W, x.ldb = c.K * 2, x.P = w.P;
+    x.A[0] = w.prob, x.A[1] = w.low, x.lda = w.ldp * 2, x.B[0] = x.B[1] = W, x.ldb = c.K * 2, x.P = w.P;
     x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
     x.D[0] = !c.dX ? nullptr : last ? c.dX : w.kept;
     x.bm = (int)tile_rows(plan.tile), x.most = input.most;
     d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;
-    d.A[0] = w.prob, d.A[1] = low, d.lda = w.ldp * 2, d.B[0] = d.B[1] = w.picked.rows, d.ldb = c.K * 2;
+    d.A[0] = w.prob, d.A[1] = w.low, d.lda = w.ldp * 2, d.B[0] = d.B[1] = w.picked.rows, d.ldb = c.K * 2;
     if (c.dW) d.D[0] = static_cast<uint8_t*>(c.dW) + v * c.K * 2;
     d.count = w.picked.count;
-    const DensePlan weights = plan_of(n, c.K, terms * ceil_div(c.M, 64), 1);
+    const DensePlan weights = plan_of(n, c.K, terms_of(c.M) * ceil_div(c.M, 64), 1);
     const bool both = c.dX && c.dW && n == c.V && merges(plan, weights, c.M, n, c.K);
-    e = terms == 2 ? launch_products<2>(x, plan, last, d, weights, both, s)
-                   : launch_products<1>(x, plan, last, d, weights, both, s);
+    e = launch_products(x, plan, last, d, weights, both, s);
     if (e != hipSuccess) return e;
     if (c.dX && plan.S > 1) {
       const int64_t grid = std::min<int64_t>(ceil_div(c.M * (c.K / 4), 256), device_cus() * 8);

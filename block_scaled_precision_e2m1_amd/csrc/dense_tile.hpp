@@ -84,7 +84,7 @@ struct LossArgs : DenseArgs {
   const float* lse = nullptr;       // prob: lse of each row
   const float* g = nullptr;         // prob: what each row is multiplied by
   int64_t ldp = 0;                  // prob: elements between rows of D, a multiple of 8
-  void* low = nullptr;              // prob: what D's rounding leaves, rounded itself, if it is wanted
+  void* low = nullptr;              // prob: what D's rounding leaves, rounded itself, of few rows (kFewRows)
   const float* add = nullptr;       // accum: [M][N] what is added to the product, if anything
   int bm = 1, most = 1;             // accum, split: rows of a tile, K slices at most
 };
@@ -95,6 +95,12 @@ __device__ __forceinline__ int splits_of(const LossArgs& a, int rows) {
   return min((uint32_t)a.most, a.S * planned / there);
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// A gradient is mostly made of P at the wanted tokens.  Over many rows their roundings average
+// (0.0024 of a gradient's norm, of which the results' own rounding is 0.0017); over few they
+// would show by their luck (to 0.004).  Of up to this many rows that take part P is therefore kept in
+// two terms, which follow one another along the contraction; the products of both are half of the
+// backward pass's time more.
+constexpr int kFewRows = 128;
 
 // KG groups of waves share a tile: group g multiplies quarters QN g .. of every stage, which
 // is ROWB bytes of K.  OCC workgroups share a CU.
@@ -245,7 +251,10 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
   // Sizes reach 2^31 - 1: what passes them by part of a tile is formed unsigned.
   const int tiles_m = ((uint32_t)M + C::BM - 1) / C::BM, tiles_n = ((uint32_t)a.N + C::OUTN - 1) / C::OUTN;
   const int total = a.L * tiles_m * tiles_n * S;
-  const int KT1 = ((uint32_t)K + C::KE - 1) / C::KE, KT = C::NSEG * KT1;
+  int segments = C::NSEG;
+  if constexpr (C::FORM == kAccum) segments = M <= kFewRows ? 2 : 1;
+  if constexpr (C::FORM == kCounted) segments = K <= kFewRows ? 2 : 1;
+  const int KT1 = ((uint32_t)K + C::KE - 1) / C::KE, KT = segments * KT1;
   const int lda = (int)a.lda, ldb = (int)a.ldb;
 
   // ---- the current item ----
@@ -623,7 +632,7 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
               }
               at = m * a.ldp + n;
               left = V;
-              if (a.low) {
+              if (M <= kFewRows) {
                 float r[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
