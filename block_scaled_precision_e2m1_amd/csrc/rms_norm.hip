@@ -252,14 +252,21 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const Rows a) {
 // Lanes a row (0: a workgroup) and units a lane; units 0: the rows are too long for any shape.
 struct Shape { int lanes, units; };
 // Two units a lane: in us, (lanes, units), 131072 x 128 bf16 (8, 2) 12.4, (16, 1) 13.4, (4, 4) 15.5;
-// 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.  Few rows are bound by latency, and
-// take one: 1003 x 1117 fp32 with a residual 5.2, with two 6.2.
+// 8192 x 8192 bf16 with a residual (512, 2) 78.6, (256, 4) 80.1.  Of rows longer than a wave, those that
+// the chip's 2048 lanes a CU hold all at once with one unit a lane (below 8 MB on 256 CUs) are bound by
+// latency and take one; the others need the second unit's loads in flight.  One and two, with a
+// residual:
+//   below  512 x 2048 bf16 3.3 3.7, 1003 x 1117 fp32 4.9 5.6, 2048 x 1117 bf16 7.0 7.4
+//   at it  2048 x 2048 bf16 6.8 6.9 (without 4.9 4.5), 2048 x 1040 fp32 7.9 6.8
+//   above  1500 x 2048 fp32 10.3 9.3, 2048 x 4096 bf16 14.2 14.0 (without 8.2 7.4)
+// Past 512 units the two are within 4% where few rows are there (512 x 6144 bf16 5.8 6.1, 256 x 8192
+// 4.5 4.5).
 Shape shape_of(int64_t rows, int64_t units) {
   if (units <= 16) return {8, 2};
   if (units <= 32) return {16, 2};
   if (units <= 64) return {32, 2};
   if (units <= 128) return {64, 2};
-  if (units <= 512 && rows <= 2048) return {0, 1};
+  if (units <= 512 && rows * units < 2048 * device_cus()) return {0, 1};
   if (units <= 2048) return {0, 2};
   if (units <= 4096) return {0, 4};
   return {0, 0};
