@@ -243,12 +243,16 @@ Plan plan_of(int64_t rows, int64_t K, bool bf16) {
     return {0, 0, std::max<int64_t>(1, std::min<int64_t>({rows, 64, 4 * cus / ceil_div(units, 256) + 1}))};
   const int lanes = units <= 16 ? 16 : units <= 32 ? 32 : units <= 64 ? 64 : 0;
   const int block = lanes ? 256 : (int)(ceil_div(units, units <= 1024 ? 64 : 128) * 64);
-  // Enough workgroups for the chip, and no more: each writes a row of partial sums.  Few rows are
-  // bound by the latency of one after the other, and take twice as many.  In us, 1, 2 and 4
-  // workgroups a CU: 1003 x 1117 fp32 (with the norm) 19.1, 17.7, 21.3; 8192 x 8192 bf16 182,
-  // 187, 200; 8192 x 2048 bf16 53.3, 53.3, 55.6.
+  // Enough workgroups for the chip, and no more: each writes a row of partial sums.  In us, 1, 2 and 4
+  // workgroups a CU: 8192 x 8192 bf16 182, 187, 200 (with the norm); 8192 x 2048 bf16 53.3, 53.3, 55.6.
+  // Few short rows are bound by the latency of one after the other, and take twice as many; of longer
+  // ones the partial sums' way through memory takes more than that gains.  1 and 2 a CU, the gradient
+  // alone:
+  //   512 rows of 1040 bf16 7.7 7.7, of 1117 fp32  8.9  8.7, of 1536 bf16  8.5  9.4, fp32  8.4  8.9
+  //   1003             9.2 8.5,             11.2 10.0,             10.0 10.4,       10.8 10.8
+  //   512 rows of 2048 bf16 9.2 10.9, of 4096 12.7 17.8, of 8192 21.0 28.1
   const int64_t per = lanes ? 256 / lanes : 1, most = cus * std::max(1, 1024 / block);
-  const int64_t many = rows < 4 * cus ? 2 * cus : std::max(cus, std::min(most, rows / 16));
+  const int64_t many = rows < 4 * cus && K <= 1280 ? 2 * cus : std::max(cus, std::min(most, rows / 16));
   return {lanes, block, std::min(ceil_div(rows, per), many)};
 }
 int64_t sums_bytes(int64_t rows) { return (rows * 8 + 15) / 16 * 16; }
