@@ -132,13 +132,15 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
 }
 
 hipError_t launch_pick(Pick p, int* counts, bool grad, hipStream_t s) {
-  // Up to 4096 targets (32 KB) are counted by every workgroup for itself.
+  // Up to 4096 targets (32 KB) are counted by every workgroup for itself: 27.0 us of a backward pass
+  // over 128 tokens, in chunks 29.0; of 8192 42.6 43.0, of 16384 78.9 71.2.
   if (p.M > 4096) {
     const hipError_t e = launch(loss_count_kernel, ceil_div(p.M, kChunk), 256, s, p.M, p.ignore, p.target, counts);
     if (e != hipSuccess) return e;
     p.counts = counts;
   }
-  // Few rows are spread over the chip: 16 x 4096 take 3 us a row to a workgroup, 7 four to one.
+  // Few rows are spread over the chip: 16 x 4096 take 3 us a row to a workgroup, 7 four to one.  Whole
+  // backward passes over 128 tokens: 1024 x 4096 38.0 39.2, 2048 x 4096 47.2 46.3, 2048 x 512 23.1 21.8.
   if (p.M <= 1024) return launch(grad ? loss_pick_kernel<true, 1> : loss_pick_kernel<false, 1>, p.M, 256, s, p);
   return launch(grad ? loss_pick_kernel<true, 4> : loss_pick_kernel<false, 4>, ceil_div(p.M, 4), 256, s, p);
 }
@@ -411,8 +413,10 @@ int64_t loss_bytes(int64_t M, int64_t V, int64_t K) { return ForwardSpace(nullpt
 
 // Gathering takes 4 us or more.  One tile's rows cost the same whether they take part or not, and
 // a product of 2^34 operations takes about 12 us with all of them: those take every row as it
-// is, and the join leaves out what takes no part (301 x 1003 x 520 with its gradients 32.7 us
-// with a gathering, 29.1 without).
+// is, and the join leaves out what takes no part.  Forward, in us, without and with a gathering, none and
+// half of the rows ignored: 301 x 1003 x 520 10.9 14.9 and 10.9 14.9, 1000 x 8192 x 1024 (at the border)
+// 25.9 31.3 and 25.8 25.2, 2000 x 8192 x 1024 41.7 47.9 and 42.4 41.9, 4096 x 8192 x 1024 76.0 82.2
+// and 74.7 47.5.
 bool loss_gathers(int64_t M, int64_t V, int64_t K) { return M > 64 && (double)M * (double)V * (double)K > 8.6e9; }
 
 hipError_t launch_loss(const LossCall& c, hipStream_t s) {
@@ -432,8 +436,11 @@ hipError_t launch_loss(const LossCall& c, hipStream_t s) {
   }
   const hipError_t e = launch_one_group<Forward, true, false>(a, forward_plan(c.M, c.V, c.K).tile, s);
   if (e != hipSuccess) return e;
-  // 16 rows side by side are whole lines of parts; few rows need the threads.
-  const int rows = c.M >= 2048 ? 16 : 1;
+  // 16 rows side by side are whole lines of parts; few rows of many parts need the threads.  Forward, in
+  // us, 1 and 16 rows a workgroup: 301 x 1003 x 128 8.6 7.9, 128 x 4000 (63 parts) 8.3 7.8, 64 x 32000
+  // (500 parts) 9.1 10.2, 301 x 32000 15.1 14.9, 301 x 131072 37.2 41.2, 512 x 131072 56.6 55.5,
+  // 1024 x 32000 31.6 29.3, 2048 x 32000 56.9 50.2.
+  const int rows = c.M >= 512 || w.parts <= 128 ? 16 : 1;
   return launch(rows == 16 ? loss_join_kernel<16> : loss_join_kernel<1>, ceil_div(c.M, rows), 256, s, j);
 }
 
