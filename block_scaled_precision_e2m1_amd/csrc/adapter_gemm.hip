@@ -368,7 +368,10 @@ __global__ void __launch_bounds__(256, TM * RMAX < 64 * 256 || BF16 ? 2 : 1) ada
       for (int b = 0; b < 4; ++b) acc[b] = mfma16(f.v[b], t, acc[b]);
     }
   };
-  // A step's product while the next step's base, and the next rows of B, are on their way.
+  // A step's product, with the next step's base and the next rows of B asked for before it.  As
+  // compiled b0 = b1 waits for all of them, base's loads among them, which are older: with more than 32
+  // of R base is on its way for the first 32 alone.  The choices of an offset, and of the rows that
+  // come next, become branches around the loads of B.
   auto step = [&](int n, Base& now, Base& ahead) {
     v4f acc[FT][4] = {};
     const int next = n + 256 < whole ? n + 256 : n;
@@ -509,8 +512,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
   Plan p;
   p.direct = M <= kDirect;
   // 64 tokens share an adapter's reads, 16 leave more tiles.  In us, 16 and 64: 642 x 795 x 5648
-  // rank 24 16.4, 25.2; 4000 x 2000 x 2048 rank 128 66.6, 73.9; 2000 x 8000 x 4096 rank 32
-  // 40.4, 41.4; 4096 x 14336 x 4096 rank 64 151, 113.
+  // rank 24 16.4, 25.2; 4000 x 2000 x 2048 rank 128 66.6, 73.9; 1000 x 14336 x 4096 rank 16 26.4, 28.2;
+  // about the border, 4 and 64 adapters: 2000 x 16384 x 2048 rank 32 40.2, 45.3 and 54.8, 51.9; 2500 x
+  // 16384 x 2048 rank 32 53.8, 51.1 and 70.8, 58.6; past it 4096 x 14336 x 4096 rank 64 135, 91 and 149,
+  // 107.  The rule does not look at the rank, which moves the border: 4096 x 4096 x 4096 takes 34.6, 37.2 at
+  // rank 16 and 58.4, 49.9 at rank 64.
   p.tm = p.direct || M * N < (int64_t)1 << 25 ? 16 : 64;
   p.tiles = std::min(M, ceil_div(M, p.tm) + L);   // an adapter's last tile may be short; so may that of none
   // Two units of 128 bytes of K a wave at least, and workgroups for the chip: of 64 tokens as many as

@@ -3,18 +3,21 @@
 //   z = X W^T,  lse[m] = log sum_v e^z[m][v],  loss[m] = lse[m] - z[m][target[m]]
 //   P = (e^(z - lse) - [v == target]) dL,  dX = P W,  dW = P^T X
 //
-// Bound by the matrix instructions: 2 M V K operations forward, 8 M V K for the gradients, of
-// which 2 form the logits again.  The products are those of dense_tile.hpp:
+// Bound by the matrix instructions: 2 M V K operations forward and 6 M V K for the gradients, of
+// which 2 form the logits again; M counts the rows that take part.  The products are those of
+// dense_tile.hpp:
 //
 //   * Forward, a tile's end leaves the maximum and the sum of the exponentials of each row over
 //     a wave's columns (8 bytes for 64 or 128 logits), and a last kernel joins them.
 //   * Backward, the vocabulary is taken in pieces.  A piece's logits are formed again and leave
-//     their tiles as P in bf16 (two terms of it for few rows), the operand of both gradients'
-//     products; dW's rows of the piece are then whole, and dX is summed over the pieces in fp32.
-//   * Rows without a loss (a prompt's tokens, padding) take no part: the rows that have one are
-//     gathered first, their number stays on the GPU, and the tiles read it there.  Half of
-//     the rows ignored is half of the time, and what an ignored row holds reaches nothing.
-//     The gathering copy moves 4 M K bytes.
+//     their tiles as P in bf16, the operand of both gradients' products; dW's rows of the piece are
+//     then whole, and dX is summed over the pieces in fp32.  For up to kFewRows rows P has two
+//     terms, and the gradients' products twice the length: 10 M V K.
+//   * Rows without a loss (a prompt's tokens, padding): the rows that have one are gathered first,
+//     their number stays on the GPU, and the tiles read it there.  Half of the rows ignored is
+//     half of the products.  The gathering copy moves 4 M K bytes.  A small forward product
+//     (loss_gathers) takes every row as it is, and what an ignored row gives is left out of
+//     the results.  Either way what it holds reaches nothing.
 #include <algorithm>
 
 #include "dense_tile.hpp"

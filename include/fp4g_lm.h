@@ -73,9 +73,10 @@ fp4g_status rms_norm_backward(int64_t rows, int64_t K, const void *dY, const voi
 /* The softmax cross entropy of bf16 X[M][K] against the vocabulary's bf16 W[V][K], a target
  * token for each row, without the logits z = X W^T in memory:
  *   lse[m] = log sum_v e^z[m][v],   loss[m] = lse[m] - z[m][target[m]],
- * logits with fp32 sums, exponentials and their sums in fp32.  loss and lse are fp32 [M]; lse
- * may be NULL.  Rows whose target is ignore_index take no part: their loss and lse are 0,
- * their X is not looked at.  Any other target outside 0 .. V-1 gives a NaN loss.  target is
+ * logits with fp32 sums, exponentials of their differences from a row's largest and the sums
+ * of these in fp32: no loss is negative.  loss and lse are fp32 [M]; lse may be NULL.  Rows
+ * whose target is ignore_index take no part: their loss and lse are 0, and what their X holds
+ * reaches no result, though it may be read.  Any other target outside 0 .. V-1 gives a NaN loss.  target is
  * int64 [M].  V >= 1 where M > 0 (FP4G_EINVAL); K a multiple of 8 and at most 2^21, M at most
  * 2^25 (FP4G_EUNSUPPORTED).  X and W are 16-byte aligned, the others aligned to their elements
  * (FP4G_EALIGN).  The workspace is required (fewer bytes than the query's are FP4G_EINVAL). */
@@ -86,8 +87,8 @@ fp4g_status cross_entropy_gemm(int64_t M, int64_t V, int64_t K, const void *X, c
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* The gradients of cross_entropy_gemm from the incoming fp32 dL[M] and the lse it gave, both
- * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once (for M of at most
- * 128 to two bf16 terms, which keep 16 bits),
+ * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once (where at most 128
+ * rows take part to two bf16 terms, which keep 16 bits),
  *   dX[M][K] = P W,   dW[V][K] = P^T X   with fp32 sums.
  * P is formed for a piece of the vocabulary at a time, in the workspace: the query gives
  * `bytes`, with which pieces are large enough to fill the GPU, and `least`, the least a call
