@@ -39,32 +39,65 @@ struct Pick {
   int *map, *wanted, *count;      // which row each was, its target or -1, and their number
   float *loss, *lse;              // forward: 0 for the rows that take no part
   float* z;                       // forward: the wanted logit, NaN until it is found
+  const float* tops;              // backward: with counts, the largest |dL| among each 1024
+  float* unscale;                 // backward: what the gradients' products are multiplied by
   const float *dL, *lse_in;       // backward: taken to the rows that take part
   float *g, *lse_out;
   v4i* dX;                        // backward: 0 for the rows that take no part
 };
 constexpr int kChunk = 1024;
 
-__device__ __forceinline__ int block_sum(int v, int* part) {
+// The sum of n and the maximum of top over a workgroup of 4 waves.
+struct Seen { int n; float top; };
+__device__ __forceinline__ Seen over_block(Seen v, Seen* part) {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  for (int d = 1; d < 64; d *= 2) {
+    v.n += __shfl_xor(v.n, d);
+    v.top = fmaxf(v.top, __shfl_xor(v.top, d));
+  }
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
-  return part[0] + part[1] + part[2] + part[3];
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) v.n += part[w].n, v.top = fmaxf(v.top, part[w].top);
+  return v;
 }
 
+// P is rounded to bf16 once dL is in it, and is mostly p - 1 times dL at the wanted tokens.  A mean
+// gives one dL to all rows: where they know little, p near 0, all of their roundings would be
+// that of dL itself, and the gradients off by up to 0.004 of their norm (1 / 1020, 1 / 4095), where their
+// own rounding is 0.0017.  So all dL are multiplied by one number of 1 .. 2 that takes the largest
+// of them to a power of two, and the products by its inverse at the end.  Past these bounds that would
+// leave fp32's range.
+__device__ __forceinline__ float unscale_of(float top) {
+  if (!(top >= 0x1p-126f && top < 0x1p126f)) return 1.0f;
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, top) & 0x7fffffu) | 0x3f000000u);
+}
+__device__ __forceinline__ float top_of(float dl) {
+  const float m = __builtin_fabsf(dl);
+  return m < __builtin_inff() ? m : 0.0f;
+}
+
+template <bool GRAD>
 __global__ void __launch_bounds__(256) loss_count_kernel(int64_t M, int64_t ignore, const int64_t* __restrict__ target,
-                                                         int* __restrict__ counts) {
-  __shared__ int part[4];
+                                                         const float* __restrict__ dL, int* __restrict__ counts,
+                                                         float* __restrict__ tops) {
+  __shared__ Seen part[4];
   const int64_t first = (int64_t)blockIdx.x * kChunk;
-  int n = 0;
+  Seen v{0, 0.0f};
 #pragma unroll
   for (int i = 0; i < kChunk / 256; ++i) {
     const int64_t m = first + i * 256 + threadIdx.x;
-    n += m < M && target[m] != ignore;
+    const bool in = m < M && target[m] != ignore;
+    v.n += in;
+    if constexpr (GRAD)
+      if (in) v.top = fmaxf(v.top, top_of(dL[m]));
   }
-  n = block_sum(n, part);
-  if (threadIdx.x == 0) counts[blockIdx.x] = n;
+  v = over_block(v, part);
+  if (threadIdx.x == 0) {
+    counts[blockIdx.x] = v.n;
+    if constexpr (GRAD) tops[blockIdx.x] = v.top;
+  }
 }
 
 // A wave for each of 4 rows, or (ROWS == 1) the workgroup for one: how many before take part is
@@ -73,7 +106,7 @@ __global__ void __launch_bounds__(256) loss_count_kernel(int64_t M, int64_t igno
 template <bool GRAD, int ROWS>
 __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
   constexpr int LANES = 256 / ROWS, AHEAD = 4;
-  __shared__ int part[4];
+  __shared__ Seen part[4];
   const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES;
   const int64_t row0 = (int64_t)blockIdx.x * ROWS, m = row0 + mine, units = a.K / 8;
   bool in[ROWS], here = false;
@@ -87,22 +120,34 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i)
     if (here && lane + i * LANES < units) held[i] = x[lane + i * LANES];
-  int before = 0;
+  Seen seen{0, 0.0f};
   int64_t from = 0;
   if (a.counts) {
     from = row0 / kChunk * kChunk;
-    for (int64_t c = threadIdx.x; c < row0 / kChunk; c += 256) before += a.counts[c];
+    for (int64_t c = threadIdx.x; c < row0 / kChunk; c += 256) seen.n += a.counts[c];
+    if constexpr (GRAD)
+      for (int64_t c = threadIdx.x; c * kChunk < a.M; c += 256) seen.top = fmaxf(seen.top, a.tops[c]);
   }
+  // With the largest |dL| of all rows to be found, all of their targets are looked at.
+  const int64_t to_row = GRAD && !a.counts ? a.M : row0;
 #pragma unroll 4
-  for (int64_t i = from + threadIdx.x; i < row0; i += 256) before += a.target[i] != a.ignore;
-  before = block_sum(before, part);
-  int slot = before, last = before;
+  for (int64_t i = from + threadIdx.x; i < to_row; i += 256) {
+    const bool in = a.target[i] != a.ignore;
+    seen.n += in && i < row0;
+    if constexpr (GRAD)
+      if (in && !a.counts) seen.top = fmaxf(seen.top, top_of(a.dL[i]));
+  }
+  seen = over_block(seen, part);
+  int slot = seen.n, last = seen.n;
 #pragma unroll
   for (int w = 0; w < ROWS; ++w) {
     slot += w < mine && in[w];
     last += in[w];
   }
-  if (row0 + ROWS >= a.M && threadIdx.x == 0) *a.count = last;
+  if (row0 + ROWS >= a.M && threadIdx.x == 0) {
+    *a.count = last;
+    if constexpr (GRAD) *a.unscale = unscale_of(seen.top);
+  }
   if (m >= a.M) return;
   if (!here) {
     if constexpr (GRAD) {
@@ -126,7 +171,7 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
     a.map[slot] = (int)m;
     a.wanted[slot] = known ? (int)t : -1;
     if constexpr (GRAD) {
-      a.g[slot] = known ? a.dL[m] : __builtin_nanf("");
+      a.g[slot] = known ? a.dL[m] * (1.0f / unscale_of(seen.top)) : __builtin_nanf("");
       a.lse_out[slot] = a.lse_in[m];
     } else {
       a.z[slot] = __builtin_nanf("");
@@ -134,13 +179,14 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
   }
 }
 
-hipError_t launch_pick(Pick p, int* counts, bool grad, hipStream_t s) {
+hipError_t launch_pick(Pick p, int* counts, float* tops, bool grad, hipStream_t s) {
   // Up to 4096 targets (32 KB) are counted by every workgroup for itself: 27.0 us of a backward pass
   // over 128 tokens, in chunks 29.0; of 8192 42.6 43.0, of 16384 78.9 71.2.
   if (p.M > 4096) {
-    const hipError_t e = launch(loss_count_kernel, ceil_div(p.M, kChunk), 256, s, p.M, p.ignore, p.target, counts);
+    const hipError_t e = launch(grad ? loss_count_kernel<true> : loss_count_kernel<false>, ceil_div(p.M, kChunk), 256, s, p.M,
+                                p.ignore, p.target, p.dL, counts, tops);
     if (e != hipSuccess) return e;
-    p.counts = counts;
+    p.counts = counts, p.tops = tops;
   }
   // Few rows are spread over the chip: 16 x 4096 take 3 us a row to a workgroup, 7 four to one.  Whole
   // backward passes over 128 tokens: 1024 x 4096 38.0 39.2, 2048 x 4096 47.2 46.3, 2048 x 512 23.1 21.8.
@@ -344,6 +390,7 @@ __global__ void __launch_bounds__(256) loss_reduce_kernel(const LossArgs a) {
 #pragma unroll 4
     for (int k = 1; k < S; ++k) t += p[k * plane];
     if (a.add) t += *reinterpret_cast<const v4f*>(a.add + (int64_t)m * a.N + n);
+    if constexpr (BF16) t *= *a.unscale;
     const float y[4] = {t[0], t[1], t[2], t[3]};
     store_cols<BF16>(a.D[0], (int64_t)(BF16 ? a.map[m] : (int)m) * a.N + n, 4, y);
   }
@@ -393,11 +440,12 @@ namespace {
 struct GradSpace {
   Space s;
   Picked picked;
-  float *g, *lse, *kept, *P;
+  float *g, *lse, *tops, *unscale, *kept, *P;
   int64_t ldp;
   uint8_t *prob, *low;
   GradSpace(uint8_t* p, int64_t M, int64_t V, int64_t K, int64_t cols)
       : s{p}, picked(s, M, K), g(s.take<float>(M)), lse(s.take<float>(M)),
+        tops(s.take<float>(ceil_div(M, kChunk))), unscale(s.take<float>(1)),
         kept(s.take<float>(cols < V ? M * K : 0)), P(nullptr), ldp(ceil_div(cols, 64) * 64),
         prob(s.take<uint8_t>(M * ldp * 2)), low(s.take<uint8_t>(std::min<int64_t>(M, kFewRows) * ldp * 2)) {
     // Pieces differ by their last one, which may split further.
@@ -433,7 +481,7 @@ hipError_t launch_loss(const LossCall& c, hipStream_t s) {
   } else {
     Pick k = pick_of(c, w.picked);
     k.loss = c.loss, k.lse = c.lse, k.z = w.z;
-    const hipError_t e = launch_pick(k, w.picked.counts, false, s);
+    const hipError_t e = launch_pick(k, w.picked.counts, nullptr, false, s);
     if (e != hipSuccess) return e;
     a.A[0] = w.picked.rows, a.count = j.count = w.picked.count, a.target = w.picked.wanted, j.map = w.picked.map;
   }
@@ -462,8 +510,8 @@ int64_t loss_grad_cols(int64_t M, int64_t V, int64_t K) {
 hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
   const GradSpace w(c.space, c.M, c.V, c.K, c.cols);
   Pick k = pick_of(c, w.picked);
-  k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse_out = w.lse, k.dX = static_cast<v4i*>(c.dX);
-  hipError_t e = launch_pick(k, w.picked.counts, true, s);
+  k.dL = c.dL, k.lse_in = c.lse, k.g = w.g, k.lse_out = w.lse, k.unscale = w.unscale, k.dX = static_cast<v4i*>(c.dX);
+  hipError_t e = launch_pick(k, w.picked.counts, w.tops, true, s);
   if (e != hipSuccess) return e;
   for (int64_t v = 0; v < c.V; v += c.cols) {
     const int64_t n = std::min(c.cols, c.V - v);
@@ -482,7 +530,7 @@ hipError_t launch_loss_grad(const LossCall& c, hipStream_t s) {
     LossArgs x, d;
     x.M = (int)c.M, x.N = (int)c.K, x.K = (int)n, x.S = plan.S;
     x.A[0] = w.prob, x.A[1] = w.low, x.lda = w.ldp * 2, x.B[0] = x.B[1] = W, x.ldb = c.K * 2, x.P = w.P;
-    x.count = w.picked.count, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
+    x.count = w.picked.count, x.unscale = d.unscale = w.unscale, x.map = w.picked.map, x.add = v > 0 ? w.kept : nullptr;
     x.D[0] = !c.dX ? nullptr : last ? c.dX : w.kept;
     x.bm = (int)tile_rows(plan.tile), x.most = input.most;
     d.M = (int)n, d.N = (int)c.K, d.K = (int)c.M;

@@ -83,6 +83,7 @@ struct LossArgs : DenseArgs {
   float* wanted = nullptr;          // loss: [M] z of the wanted column
   const float* lse = nullptr;       // prob: lse of each row
   const float* g = nullptr;         // prob: what each row is multiplied by
+  const float* unscale = nullptr;   // accum to bf16, counted: what all results are multiplied by
   int64_t ldp = 0;                  // prob: elements between rows of D, a multiple of 8
   void* low = nullptr;              // prob: what D's rounding leaves, rounded itself, of few rows (kFewRows)
   const float* add = nullptr;       // accum: [M][N] what is added to the product, if anything
@@ -95,11 +96,12 @@ __device__ __forceinline__ int splits_of(const LossArgs& a, int rows) {
   return min((uint32_t)a.most, a.S * planned / there);
 }
 constexpr float kLog2e = 1.4426950408889634f;
-// A gradient is mostly made of P at the wanted tokens.  Over many rows their roundings average
-// (0.0024 of a gradient's norm, of which the results' own rounding is 0.0017); over few they
-// would show by their luck (to 0.004).  Of up to this many rows that take part P is therefore kept in
-// two terms, which follow one another along the contraction; the products of both are half of the
-// backward pass's time more.
+// A gradient is mostly made of P at the wanted tokens.  Over many rows their roundings average:
+// the results are off by 0.0017 to 0.0020 of their norm where all rows have one dL and by 0.0022 to
+// 0.0024 where dL spread over a binade and a half, of which their own rounding is 0.0017.  Over few
+// they would show by their luck (to 0.004).  Of up to this many rows that take part P is therefore
+// kept in two terms, which follow one another along the contraction; the products of both are half
+// of the backward pass's time more.
 constexpr int kFewRows = 128;
 
 // KG groups of waves share a tile: group g multiplies quarters QN g .. of every stage, which
@@ -251,6 +253,8 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
   // Sizes reach 2^31 - 1: what passes them by part of a tile is formed unsigned.
   const int tiles_m = ((uint32_t)M + C::BM - 1) / C::BM, tiles_n = ((uint32_t)a.N + C::OUTN - 1) / C::OUTN;
   const int total = a.L * tiles_m * tiles_n * S;
+  float unscale = 1.0f;
+  if constexpr (C::FORM == kCounted || (C::FORM == kAccum && BF16)) unscale = *a.unscale;
   int segments = C::NSEG;
   if constexpr (C::FORM == kAccum) segments = M <= kFewRows ? 2 : 1;
   if constexpr (C::FORM == kCounted) segments = K <= kFewRows ? 2 : 1;
@@ -653,6 +657,10 @@ __device__ __forceinline__ void dense_gemm(const ARGS& a, int block, int grid, u
                 }
               }
               if constexpr (BF16) at = (int64_t)a.map[m] * a.N + n;
+            }
+            if constexpr (C::FORM == kCounted || (C::FORM == kAccum && BF16)) {
+#pragma unroll
+              for (int e = 0; e < V; ++e) y[e] *= unscale;
             }
             if constexpr (C::GATED) {
 #pragma unroll
