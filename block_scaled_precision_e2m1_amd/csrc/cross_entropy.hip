@@ -180,8 +180,9 @@ __global__ void __launch_bounds__(256) loss_pick_kernel(const Pick a) {
 }
 
 hipError_t launch_pick(Pick p, int* counts, float* tops, bool grad, hipStream_t s) {
-  // Up to 4096 targets (32 KB) are counted by every workgroup for itself: 27.0 us of a backward pass
-  // over 128 tokens, in chunks 29.0; of 8192 42.6 43.0, of 16384 78.9 71.2.
+  // Up to 4096 targets (32 KB) are counted by every workgroup for itself.  Backward passes over 128
+  // tokens, in us, so and in chunks: 2048 x 256 20.0 22.2, 4096 x 256 29.4 30.2, 4096 x 4096 68.4 66.1,
+  // 6000 x 256 38.7 36.4, 8192 x 256 53.4 44.7; forward passes differ by less.
   if (p.M > 4096) {
     const hipError_t e = launch(grad ? loss_count_kernel<true> : loss_count_kernel<false>, ceil_div(p.M, kChunk), 256, s, p.M,
                                 p.ignore, p.target, p.dL, counts, tops);
@@ -189,7 +190,7 @@ hipError_t launch_pick(Pick p, int* counts, float* tops, bool grad, hipStream_t 
     p.counts = counts, p.tops = tops;
   }
   // Few rows are spread over the chip: 16 x 4096 take 3 us a row to a workgroup, 7 four to one.  Whole
-  // backward passes over 128 tokens: 1024 x 4096 38.0 39.2, 2048 x 4096 47.2 46.3, 2048 x 512 23.1 21.8.
+  // backward passes over 128 tokens: 1024 x 4096 38.7 39.7, 2048 x 4096 51.1 48.5, 2048 x 512 26.1 23.1.
   if (p.M <= 1024) return launch(grad ? loss_pick_kernel<true, 1> : loss_pick_kernel<false, 1>, p.M, 256, s, p);
   return launch(grad ? loss_pick_kernel<true, 4> : loss_pick_kernel<false, 4>, ceil_div(p.M, 4), 256, s, p);
 }
