@@ -66,12 +66,11 @@ __device__ __forceinline__ Seen over_block(Seen v, Seen* part) {
 // P is rounded to bf16 once dL is in it, and is mostly p - 1 times dL at the wanted tokens.  A mean
 // gives one dL to all rows: where they know little, p near 0, all of their roundings would be
 // that of dL itself, and the gradients off by up to 0.004 of their norm (1 / 1020, 1 / 4095), where their
-// own rounding is 0.0017.  So all dL are multiplied by one number of 1 .. 2 that takes the largest
-// of them to a power of two, and the products by its inverse at the end.  Past these bounds that would
-// leave fp32's range.
+// own rounding is 0.0017.  So all dL are divided by one number of 1 .. 2 that takes the largest of them
+// down to a power of two, and the products multiplied by it at the end: no sum is larger for it.
 __device__ __forceinline__ float unscale_of(float top) {
-  if (!(top >= 0x1p-126f && top < 0x1p126f)) return 1.0f;
-  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, top) & 0x7fffffu) | 0x3f000000u);
+  if (top < 0x1p-126f) return 1.0f;   // nothing to scale, or nothing to scale it by
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, top) & 0x7fffffu) | 0x3f800000u);
 }
 __device__ __forceinline__ float top_of(float dl) {
   const float m = __builtin_fabsf(dl);

@@ -89,7 +89,7 @@ fp4g_status cross_entropy_gemm(int64_t M, int64_t V, int64_t K, const void *X, c
 /* The gradients of cross_entropy_gemm from the incoming fp32 dL[M] and the lse it gave, both
  * bf16:  P = (e^(z - lse) - [v == target]) * dL in fp32, rounded to bf16 once (where at most 128
  * rows take part to two bf16 terms, which keep 16 bits; for that the dL of all rows are
- * multiplied by one number of 1 to 2, and the products by its inverse),
+ * divided by one number of 1 to 2, and the products multiplied by it),
  *   dX[M][K] = P W,   dW[V][K] = P^T X   with fp32 sums.
  * P is formed for a piece of the vocabulary at a time, in the workspace: the query gives
  * `bytes`, with which pieces are large enough to fill the GPU, and `least`, the least a call

@@ -64,3 +64,22 @@ def test_rows_that_take_no_part_do_not_scale():
         got = fp4.cross_entropy_gemm_backward(other, x, w, t, lse)
         torch.cuda.synchronize(DEV)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("m", [3, 300])
+def test_results_next_to_the_largest_number(m):
+    """A gradient that fp32 and bf16 hold, made of sums that no scaling may take past it: dX = -+1.8 * 2^126."""
+    v, k = 2, 24
+    x, w = torch.full((m, k), 0.5, device=DEV), torch.zeros(v, k, device=DEV)
+    w[0, 0], w[1, 0] = 1.0, -1.125
+    x[:, 1], w[0, 1], w[1, 1] = 0.5, -1.0, 1.125                 # the logits are 0
+    t = torch.zeros(m, dtype=torch.int64, device=DEV)
+    dl = torch.zeros(m, device=DEV)
+    dl[1] = 1.7 * 2.0 ** 126
+    x, w = x.bfloat16(), w.bfloat16()
+    _, lse = fp4.cross_entropy_gemm(x, w, t, save=True)
+    dx, dw = fp4.cross_entropy_gemm_backward(dl, x, w, t, lse)
+    torch.cuda.synchronize(DEV)
+    want = -0.5 * 1.7 * 2.0 ** 126 * 2.125
+    assert abs(dx[1, 0].double().item() / want - 1) <= 3 * B and abs(dx[1, 1].double().item() / want + 1) <= 3 * B
+    assert torch.isfinite(dx.float()).all() and torch.isfinite(dw.float()).all()
